@@ -9,7 +9,8 @@
  *   4. kronq_cholesky_inv   damping and the inverse Cholesky factor of H_X
  *   5. kronq_quantize_layer column-wise OBS quantization with lazy block updates
  *   6. kronq_pack           2/4-bit codes packed into 32-bit words
- * plus kronq_unpack and kronq_layer_loss (a measurement helper).
+ * plus kronq_unpack and kronq_layer_loss (a measurement helper), and for serving
+ * kronq_deploy_matvec and the 4-bit key/value cache (kronq_kv4_*).
  *
  * Conventions shared by every call
  *   - Matrices are row-major and contiguous unless a leading dimension is
@@ -379,6 +380,128 @@ int kronq_pack(const uint8_t* codes, int64_t m, int64_t n, int bits,
 /* Exact inverse of kronq_pack. */
 int kronq_unpack(const uint32_t* packed, int64_t m, int64_t n, int bits,
                  uint8_t* codes, void* stream);
+
+/*
+ * The 4-bit key/value cache: what a served model's attention layers read,
+ * next to the packed weights that kronq_deploy_matvec reads.  (The KronQ pages
+ * quantize weights and, in their weight-and-activation mode, activations with
+ * 4-bit asymmetric grids after Hadamard rotations; a cache is not described
+ * there.  The grid and the rotation are the library's own.)
+ *
+ * Cache: pages x heads x page_size (head_dim + 8) bytes, 16-byte aligned,
+ * owned by the caller; heads are the key/value heads.  head_dim 64, 128 or
+ * 256; page_size 16, 32, 64, 128 or 256 tokens (others:
+ * KRONQ_ERR_UNSUPPORTED).  The block of one (page, head) holds
+ *   key codes    page_size x head_dim/2 bytes (byte i of a token: dims 2i in
+ *                the low half, 2i + 1 in the high half, as kronq_pack)
+ *   value codes  the same
+ *   key words    page_size x uint32
+ *   value words  page_size x uint32
+ * A word is the token's fp32 scale with its low 4 bits replaced by the zero
+ * point (0 .. 15); value = scale (code - zero).  A NaN scale marks a vector
+ * that held a NaN or an infinity: it reads as NaN.
+ *
+ * Batch (all int32, on the device, so that a captured graph serves any
+ * lengths): the new tokens of sequence b are the rows q_start[b] ..
+ * q_start[b+1] - 1 of the token-major tensors (q_start has batch + 1
+ * entries, not decreasing); kv_len[b] tokens of it are in the cache, the new
+ * ones included, so new token i has index kv_len[b] - (q_start[b+1] -
+ * q_start[b]) + i; tokens page_size t .. lie in page block_table[b table_ld + t],
+ * t < max_pages.  Rows in front of q_start[0] and from q_start[batch] up to T
+ * are padding: never read, never written.  Pages may be shared between
+ * sequences for reading; two new tokens must not have the same place.
+ *
+ * A batch that contradicts itself or the cache (a length beyond the table or
+ * below the sequence's new tokens where that matters, a page number outside
+ * the cache, a position outside the rotation table, rows beyond T) is noticed
+ * on the device: `info` (optional device int32) becomes
+ * KRONQ_ERR_INVALID_ARG, nothing outside the caller's tensors is touched, and
+ * tokens without a place are skipped (not written; keys nobody sees).
+ */
+enum kronq_dtype { KRONQ_BF16 = 0, KRONQ_FP16 = 1, KRONQ_FP32 = 2 };
+
+/* Bytes of one page of one head (0 for sizes that are not supported). */
+size_t kronq_kv4_block_bytes(int page_size, int head_dim);
+
+/*
+ * New tokens into the cache, rotated on the way; queries rotated alongside.
+ *
+ * Keys and queries: the rotation by position, when rot > 0 (rot a multiple of
+ * 16, at most head_dim; dims from rot on are left), with
+ *   y_a = a cos - b sin,  y_b = b cos + a sin
+ * on the pairs (i, i + rot/2) or, interleaved, (2i, 2i + 1), i < rot/2; row p
+ * of `table` (table_rows x rot fp32, 16-byte aligned) holds the rot/2 cosines
+ * and then the sines of position p; p is positions[row] or, when that is NULL,
+ * the token's index.  Then, when `signs` (head_dim int8, +-1) is given, the
+ * signed Hadamard transform x -> head_dim^-1/2 H (signs x) of every head, as
+ * kronq_biip_rotate applies it: it spreads outlier channels over the head,
+ * and scores of equally transformed queries and keys do not change.
+ * Keys (after that) and values: the 4-bit grid of each vector,
+ *   lo = min(0, min x), hi = max(0, max x), s = max((hi - lo) (1/15), 2^-100)
+ *   rounded to 20 bits, zero = clamp(rint(-lo r), 0, 15),
+ *   code = clamp(rint(x r) + zero, 0, 15), r = 1/s.
+ * All of it fp32, one rounding per operation, in the order written (butterflies
+ * of distance 1, 2, 4, ...).
+ *
+ * q (T x q_heads x head_dim), k, v (T x heads x head_dim): dtype KRONQ_BF16 or
+ * KRONQ_FP16, last dimension contiguous, token and head strides in elements
+ * (>= 0; any, with addresses and strides that are multiples of 16 bytes read
+ * fastest).  q_out: T x q_heads x head_dim contiguous, 16-byte aligned, same
+ * type.  q_heads = 0: no queries (q, q_out NULL).
+ */
+int kronq_kv4_append(const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                     const void* k, int64_t k_stride_t, int64_t k_stride_h,
+                     const void* v, int64_t v_stride_t, int64_t v_stride_h,
+                     int dtype, int64_t T, int q_heads, void* q_out,
+                     const float* table, int64_t table_rows, int rot, int interleaved,
+                     const int32_t* positions, const int8_t* signs,
+                     void* cache, int64_t pages, int page_size, int heads, int head_dim,
+                     const int32_t* block_table, int64_t table_ld, int64_t max_pages,
+                     const int32_t* q_start, const int32_t* kv_len, int64_t batch,
+                     int32_t* info, void* stream);
+
+/*
+ * The values the cache holds for the batch's new tokens (for all of a
+ * sequence's tokens with q_start[b+1] - q_start[b] = kv_len[b]): k_out, v_out
+ * T x heads x head_dim contiguous, 16-byte aligned, dtype any of kronq_dtype.
+ */
+int kronq_kv4_gather(void* k_out, void* v_out, int dtype, int64_t T,
+                     const void* cache, int64_t pages, int page_size, int heads, int head_dim,
+                     const int32_t* block_table, int64_t table_ld, int64_t max_pages,
+                     const int32_t* q_start, const int32_t* kv_len, int64_t batch,
+                     int32_t* info, void* stream);
+
+/*
+ * Attention of the new queries over the cache:
+ *   out = sum_j softmax_j(scale q . k_j) v_j
+ * Query index p sees the keys j of its sequence with j <= p (causal = 1) or all
+ * kv_len[b] (causal = 0); with window > 0 (causal only) those with j > p - window
+ * or j < sinks: a sliding window and a few first tokens that stay visible.  Pages no
+ * query sees are not read, and their table entries may be anything.  A query
+ * that sees no key gets 0.
+ * Sums, maxima and scores are fp32; probabilities, relative to a running
+ * maximum and times the value's scale, are rounded to fp16 for the product.
+ *
+ * q (T x q_heads x head_dim), out (same): KRONQ_BF16 or KRONQ_FP16, strides in
+ * elements as above; out 8-byte aligned with strides that are multiples of 4.
+ * q_heads is a multiple of heads; query head h reads key/value head
+ * h / (q_heads / heads).  lse: optional T x q_heads fp32, the natural
+ * log-sum-exp of the scaled scores (-inf where no key is seen), to join results
+ * over disjoint sets of keys.
+ * ws: kronq_kv4_attention_workspace_size bytes; its contents need no set-up and
+ * nothing in it is kept.  Two calls may share it only when ordered one after the
+ * other (the same stream, the same graph).
+ */
+size_t kronq_kv4_attention_workspace_size(int64_t T, int q_heads, int heads, int head_dim,
+                                          int64_t batch);
+int kronq_kv4_attention(const void* q, int64_t q_stride_t, int64_t q_stride_h, int dtype,
+                        int64_t T, int q_heads,
+                        const void* cache, int64_t pages, int page_size, int heads, int head_dim,
+                        const int32_t* block_table, int64_t table_ld, int64_t max_pages,
+                        const int32_t* q_start, const int32_t* kv_len, int64_t batch,
+                        float scale, int causal, int window, int sinks,
+                        void* out, int64_t out_stride_t, int64_t out_stride_h, float* lse,
+                        int32_t* info, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Layer loss tr(H_G dW H_X dW^T), dW = W_ref - W_hat (a measurement helper,

@@ -69,6 +69,13 @@ def lib() -> ctypes.CDLL:
         "kronq_biip_rotate_input": ([P, I64, P, P, I32, P, SZ, P], I32),
         "kronq_gptaq_correction": ([P, P, I64, F32, P, P, P, SZ, P], I32),
         "kronq_quantize_layer_gptaq": ([P, I64, I64, P, P, I32, I32, I32, P, P, P, P, P, P, SZ, P], I32),
+        "kronq_kv4_block_bytes": ([I32, I32], SZ),
+        "kronq_kv4_append": ([P, I64, I64, P, I64, I64, P, I64, I64, I32, I64, I32, P, P, I64, I32, I32, P, P,
+                              P, I64, I32, I32, I32, P, I64, I64, P, P, I64, P, P], I32),
+        "kronq_kv4_gather": ([P, P, I32, I64, P, I64, I32, I32, I32, P, I64, I64, P, P, I64, P, P], I32),
+        "kronq_kv4_attention_workspace_size": ([I64, I32, I32, I32, I64], SZ),
+        "kronq_kv4_attention": ([P, I64, I64, I32, I64, I32, P, I64, I32, I32, I32, P, I64, I64, P, P, I64,
+                                 F32, I32, I32, I32, P, I64, I64, P, P, P, SZ, P], I32),
         "kronq_timing_enable": ([I32], I32),
         "kronq_timing_read": ([I32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_uint64)], I32),
     }
@@ -82,6 +89,11 @@ def lib() -> ctypes.CDLL:
 
 def _p(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _a(t):
+    """The address of a tensor, None for none."""
+    return None if t is None else t.data_ptr()
 
 
 def _s(stream):
@@ -483,6 +495,147 @@ def kronq_quantize_layer_gptaq(W, U, P, bits: int, group: int, block: int, codes
         _p(W), m, n, _p(U), _p(P), bits, group, block, _p(codes), _p(scales), _p(zeros),
         _p(W_hat), _p(info), _p(ws), 0 if ws is None else ws.numel() * ws.element_size(),
         _s(stream)))
+
+
+# ------------------------------------------------ 4-bit key/value cache
+KV_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_KV_ROWS = (torch.bfloat16, torch.float16)
+
+
+def kronq_kv4_block_bytes(page_size: int, head_dim: int) -> int:
+    return int(lib().kronq_kv4_block_bytes(page_size, head_dim))
+
+
+def _kv_rows(t, name, dtype, T, D):
+    """A T x heads x D tensor with a contiguous last dimension."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({T}, heads, {D})")
+    st, sh, sd = t.stride()
+    if sd != 1 and D != 1:
+        raise ValueError(f"{name} needs unit stride along its last dimension")
+    return t.data_ptr(), st, sh
+
+
+def _kv_args(fn, cache, block_table, q_start, kv_len, head_dim, named):
+    """The (cache, batch) part of a kronq_kv4 call after its checks."""
+    _dev(cache, torch.uint8, "cache", 3)
+    _dev(block_table, torch.int32, "block_table", 2)
+    _dev(q_start, torch.int32, "q_start", 1)
+    _dev(kv_len, torch.int32, "kv_len", 1)
+    _contig(cache, "cache")
+    B, max_pages = block_table.shape
+    if q_start.numel() != B + 1 or kv_len.numel() != B:
+        raise ValueError(f"{fn}: block_table has {B} rows, q_start {q_start.numel()} entries "
+                         f"({B + 1} expected), kv_len {kv_len.numel()} ({B} expected)")
+    if (max_pages > 1 and block_table.stride(1) != 1) or (B > 0 and q_start.stride(0) != 1) or \
+            (B > 1 and kv_len.stride(0) != 1):
+        raise ValueError(f"{fn}: block_table, q_start and kv_len need unit stride along their last dimension")
+    pages, heads, nbytes = cache.shape
+    page = nbytes // (head_dim + 8)
+    if page * (head_dim + 8) != nbytes:
+        raise ValueError(f"{fn}: a cache block of {nbytes} bytes does not hold whole tokens of head_dim {head_dim}")
+    _on_current_device((cache, "cache"), (block_table, "block_table"), (q_start, "q_start"),
+                       (kv_len, "kv_len"), *named)
+    ld = block_table.stride(0) if B > 1 else max_pages
+    if ld < max_pages:
+        raise ValueError(f"{fn}: block_table's rows overlap")
+    return (cache.data_ptr(), pages, page, heads, head_dim, block_table.data_ptr(), ld, max_pages,
+            q_start.data_ptr(), kv_len.data_ptr(), B)
+
+
+def kronq_kv4_append(q, k, v, cache, block_table, q_start, kv_len, q_out=None, table=None,
+                     interleaved: bool = False, positions=None, signs=None, info=None, stream=None):
+    """New keys and values (T x heads x D, bf16 or fp16) into the 4-bit cache,
+    keys and queries rotated on the way (see kronq.h).  q and q_out may be None."""
+    _dev(k, _KV_ROWS, "k", 3)
+    _dev(v, None, "v", 3)
+    _dev(info, torch.int32, "info")
+    _dev(table, torch.float32, "table", 2)
+    _dev(positions, torch.int32, "positions", 1)
+    _dev(signs, torch.int8, "signs", 1)
+    T, heads, D = k.shape
+    kr = _kv_rows(k, "k", k.dtype, T, D)
+    vr = _kv_rows(v, "v", k.dtype, T, D)
+    if (q is None) != (q_out is None):
+        raise ValueError("kronq_kv4_append: q and q_out go together")
+    if v.shape[1] != heads or (isinstance(cache, torch.Tensor) and cache.dim() == 3 and cache.shape[1] != heads):
+        raise ValueError("kronq_kv4_append: k, v and the cache differ in their heads")
+    qr, q_heads, qo = (None, 0, 0), 0, None
+    if q is not None:
+        _dev(q, k.dtype, "q", 3)
+        _dev(q_out, k.dtype, "q_out", 3)
+        qr = _kv_rows(q, "q", k.dtype, T, D)
+        q_heads = q.shape[1]
+        _shape(q_out, q.shape, "q_out")
+        _contig(q_out, "q_out")
+        qo = q_out.data_ptr()
+    rows = rot = 0
+    if table is not None:
+        rows, rot = table.shape
+        _contig(table, "table")
+    if positions is not None:
+        _numel(positions, T, "positions")
+        _contig(positions, "positions")
+    if signs is not None:
+        _numel(signs, D, "signs")
+        _contig(signs, "signs")
+    args = _kv_args("kronq_kv4_append", cache, block_table, q_start, kv_len, D,
+                    ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out"), (table, "table"),
+                     (positions, "positions"), (signs, "signs"), (info, "info")))
+    _check("kronq_kv4_append", lib().kronq_kv4_append(
+        *qr, *kr, *vr, KV_DTYPES[k.dtype], T, q_heads, qo, _a(table), rows, rot, int(bool(interleaved)),
+        _a(positions), _a(signs), *args, _a(info), _s(stream)))
+
+
+def kronq_kv4_gather(cache, block_table, q_start, kv_len, k_out, v_out, info=None, stream=None):
+    """The values the cache holds for the batch's new tokens (see kronq.h)."""
+    _dev(k_out, tuple(KV_DTYPES), "k_out", 3)
+    _dev(v_out, k_out.dtype, "v_out", 3)
+    _dev(info, torch.int32, "info")
+    _shape(v_out, k_out.shape, "v_out")
+    _contig(k_out, "k_out"); _contig(v_out, "v_out")
+    T, heads, D = k_out.shape
+    args = _kv_args("kronq_kv4_gather", cache, block_table, q_start, kv_len, D,
+                    ((k_out, "k_out"), (v_out, "v_out"), (info, "info")))
+    if cache.shape[1] != heads:
+        raise ValueError("kronq_kv4_gather: k_out and the cache differ in their heads")
+    _check("kronq_kv4_gather", lib().kronq_kv4_gather(
+        k_out.data_ptr(), v_out.data_ptr(), KV_DTYPES[k_out.dtype], T, *args, _a(info), _s(stream)))
+
+
+def kronq_kv4_attention_workspace_size(T: int, q_heads: int, heads: int, head_dim: int, batch: int) -> int:
+    return int(lib().kronq_kv4_attention_workspace_size(T, q_heads, heads, head_dim, batch))
+
+
+def kv4_workspace(T: int, q_heads: int, heads: int, head_dim: int, batch: int, device=None):
+    """A caller-owned workspace tensor for kronq_kv4_attention."""
+    nbytes = kronq_kv4_attention_workspace_size(T, q_heads, heads, head_dim, batch)
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def kronq_kv4_attention(q, cache, block_table, q_start, kv_len, out, ws, scale: float, causal: bool = True,
+                        window: int = 0, sinks: int = 0, lse=None, info=None, stream=None):
+    """out = attention of q (T x q_heads x D) over the 4-bit cache (see kronq.h)."""
+    _dev(q, _KV_ROWS, "q", 3)
+    _dev(out, q.dtype, "out", 3)
+    _dev(lse, torch.float32, "lse", 2)
+    _dev(info, torch.int32, "info")
+    _dev(ws, None, "ws")
+    T, q_heads, D = q.shape
+    qr = _kv_rows(q, "q", q.dtype, T, D)
+    orow = _kv_rows(out, "out", q.dtype, T, D)
+    _shape(out, q.shape, "out")
+    if lse is not None:
+        _shape(lse, (T, q_heads), "lse")
+        _contig(lse, "lse")
+    _contig(ws, "ws")
+    args = _kv_args("kronq_kv4_attention", cache, block_table, q_start, kv_len, D,
+                    ((q, "q"), (out, "out"), (lse, "lse"), (info, "info"), (ws, "ws")))
+    _check("kronq_kv4_attention", lib().kronq_kv4_attention(
+        *qr, KV_DTYPES[q.dtype], T, q_heads, *args, scale, int(bool(causal)), window, sinks, *orow,
+        _a(lse), _a(info), _a(ws), 0 if ws is None else ws.numel() * ws.element_size(), _s(stream)))
 
 
 TIMERS = {"lazy_update": 0, "chol_update": 1, "chol_panel": 2, "obs_block": 3}

@@ -5,7 +5,7 @@
 #include <mutex>
 #include <vector>
 
-#include "common.cuh"
+#include "kv4.cuh"
 
 size_t kq_cholesky_ws(int64_t n);
 size_t kq_biip_ws(int64_t m, int64_t n);
@@ -333,6 +333,65 @@ int kronq_quantize_layer_gptaq(float* W, int64_t m, int64_t n, const float* U_c,
                                size_t ws_bytes, void* stream) {
   return kq_quantize_layer_asym(W, m, n, U_c, P, bits, group, block, codes, scales, zeros, W_hat,
                                 info, ws, ws_bytes, S(stream));
+}
+
+size_t kronq_kv4_block_bytes(int page_size, int head_dim) {
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return 0;
+  return (size_t)page_size * (head_dim + 8);
+}
+
+int kronq_kv4_append(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                     int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                     int64_t v_stride_h, int dtype, int64_t T, int q_heads, void* q_out,
+                     const float* table, int64_t table_rows, int rot, int interleaved,
+                     const int32_t* positions, const int8_t* signs, void* cache, int64_t pages,
+                     int page_size, int heads, int head_dim, const int32_t* block_table,
+                     int64_t table_ld, int64_t max_pages, const int32_t* q_start,
+                     const int32_t* kv_len, int64_t batch, int32_t* info, void* stream) {
+  kv4::Cache c;
+  kv4::Batch b;
+  const int s = kq_kv4_views(cache, pages, page_size, heads, head_dim, block_table, table_ld,
+                             max_pages, q_start, kv_len, batch, &c, &b);
+  if (s != KRONQ_OK) return s;
+  return kq_kv4_append(q, q_stride_t, q_stride_h, k, k_stride_t, k_stride_h, v, v_stride_t,
+                       v_stride_h, dtype, T, q_heads, q_out, table, table_rows, rot, interleaved,
+                       positions, signs, head_dim, c, b, info, S(stream));
+}
+
+int kronq_kv4_gather(void* k_out, void* v_out, int dtype, int64_t T, const void* cache,
+                     int64_t pages, int page_size, int heads, int head_dim,
+                     const int32_t* block_table, int64_t table_ld, int64_t max_pages,
+                     const int32_t* q_start, const int32_t* kv_len, int64_t batch, int32_t* info,
+                     void* stream) {
+  kv4::Cache c;
+  kv4::Batch b;
+  const int s = kq_kv4_views(const_cast<void*>(cache), pages, page_size, heads, head_dim,
+                             block_table, table_ld, max_pages, q_start, kv_len, batch, &c, &b);
+  if (s != KRONQ_OK) return s;
+  return kq_kv4_gather(k_out, v_out, dtype, T, head_dim, c, b, info, S(stream));
+}
+
+size_t kronq_kv4_attention_workspace_size(int64_t T, int q_heads, int heads, int head_dim,
+                                          int64_t batch) {
+  return kq_kv4_attention_ws(T, q_heads, heads, head_dim, batch);
+}
+
+int kronq_kv4_attention(const void* q, int64_t q_stride_t, int64_t q_stride_h, int dtype, int64_t T,
+                        int q_heads, const void* cache, int64_t pages, int page_size, int heads,
+                        int head_dim, const int32_t* block_table, int64_t table_ld,
+                        int64_t max_pages, const int32_t* q_start, const int32_t* kv_len,
+                        int64_t batch, float scale, int causal, int window, int sinks, void* out,
+                        int64_t out_stride_t, int64_t out_stride_h, float* lse, int32_t* info,
+                        void* ws, size_t ws_bytes, void* stream) {
+  kv4::Cache c;
+  kv4::Batch b;
+  const int s = kq_kv4_views(const_cast<void*>(cache), pages, page_size, heads, head_dim,
+                             block_table, table_ld, max_pages, q_start, kv_len, batch, &c, &b);
+  if (s != KRONQ_OK) return s;
+  return kq_kv4_attention(q, q_stride_t, q_stride_h, dtype, T, q_heads, head_dim, c, b, scale,
+                          causal, window, sinks, out, out_stride_t, out_stride_h, lse, info, ws,
+                          ws_bytes, S(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,635 @@
+// Attention of new queries over the paged 4-bit cache, few query rows per key:
+// one pass over the codes with the running maximum and sum of the softmax.
+//
+//   x_rj = scale log2(e) s_j (sum_d q_rd c_jd - z_j sum_d q_rd)
+//   o_r  = sum_j 2^(x_rj - m_r) s'_j (c'_jd - z'_j) / sum_j 2^(x_rj - m_r)
+//
+// (s, z, c: scale, zero point and codes of key j; primed of value j).  Scales
+// and zero points are per token, so they are taken out of both products: the
+// tensor cores multiply the bare codes, and 128 codes of a token cost one
+// scale.  A code in the low bits of a half is the subnormal c 2^-24 (and
+// c 2^-20 four bits up), exact in fp16 x fp16 -> fp32 products: unpacking is
+// one AND per two codes and one shift per four pairs; the factors 16 go into
+// the queries (keys) and into the epilogue (values).
+//
+// S^T = K Q^T and O^T = V^T P^T with mma.m16n8k16: keys (or dims) are the 16
+// rows and the query rows of one key/value head the 8 columns, so a group of 8
+// or fewer query heads wastes none of the code operand.  (A tensor-memory
+// accumulator of 128 lanes would be filled the same way, but its operand has
+// to be written to shared or tensor memory after unpacking; with mma.sync the
+// unpacked words are the fragment.)  Between the two products the 8 x 8 blocks
+// of probabilities are turned with movmatrix.
+//
+// One block = one (sequence, tile of 8 NT rows, split of its keys) of one
+// key/value head; warp w takes keys 16 w .. of every 64, straight from global
+// memory to registers (16 bytes per lane and token: a quad reads a token's
+// row), the next step's codes in flight while this one is multiplied.  The
+// running maximum is only moved when a score passes it by 2^8 (all lanes of a
+// column agree by vote), so most steps have no cross-lane reduction.
+#include "kv4_attend.cuh"
+
+namespace kv4 {
+namespace {
+
+constexpr int THREADS = 128, WARPS = 4, BLK = 64;
+
+KQ_DEV void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                     uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+KQ_DEV uint32_t turn8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+KQ_DEV float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+KQ_DEV uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int N>
+KQ_DEV void load_words(uint32_t (&w)[N], const uint8_t* p) {
+  if constexpr (N == 1) {
+    asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+  } else if constexpr (N == 2) {
+    asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                   : "l"(p + 4 * i));
+  }
+}
+
+// Codes and words of 16 tokens as the fragments want them.  Key rows of the
+// MMA: row r of block k (0: rows 0-7, 1: rows 8-15) is token
+// 4 (r >> 1) + 2 k + (r & 1), the order in which the turned probabilities come
+// out as pairs of neighbouring tokens.
+template <int D>
+struct Step {
+  static constexpr int KW = D / 32;      // key words per lane and token
+  static constexpr int VW = D / 64;      // value words per lane and token
+  uint32_t k[2][KW];
+  uint32_t v[4][VW];
+  uint32_t kw[2], vw[2];
+};
+
+template <int D>
+KQ_DEV void load_step(Step<D>& s, const AttendArgs& a, const uint8_t* blk, int slot0, int gr, int t) {
+  const int P = a.cache.P;
+  const int tok = slot0 + 4 * (gr >> 1) + (gr & 1);
+  const uint8_t* kp = blk + tok * (D / 2) + t * (D / 8);
+  load_words(s.k[0], kp);
+  load_words(s.k[1], kp + 2 * (D / 2));
+  const uint8_t* vp = blk + P * (D / 2) + (slot0 + 4 * t) * (D / 2) + gr * (D / 16);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) load_words(s.v[i], vp + i * (D / 2));
+  const uint32_t* wp = reinterpret_cast<const uint32_t*>(blk + P * D) + tok;
+  s.kw[0] = __ldg(wp);
+  s.kw[1] = __ldg(wp + 2);
+  s.vw[0] = __ldg(wp + P);
+  s.vw[1] = __ldg(wp + P + 2);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a) {
+  constexpr int R = 8 * NT;
+  constexpr int KW = D / 32, VW = D / 64, MT = D / 16;
+  extern __shared__ float merge_o[];                 // [WARPS][R][D]
+  __shared__ float merge_ml[WARPS][R][2];
+
+  Unit u;
+  if (!find_unit<R, BLK, THREADS>(a, blockIdx.x, &u)) return;
+  const int head = blockIdx.y;
+  // (only a batch whose rows overlap can ask for more slots than there are)
+  if (u.nsplit > 1 && (u.slot0 < 0 || u.slot0 + (int)blockIdx.x - u.base >= a.slots)) {
+    kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
+    return;
+  }
+  const Seq s = seq_of(a, u.b, nullptr);
+  if (threadIdx.x == 0 && head == 0 && u.tile == 0 && u.split == 0)
+    a.meta[u.b] = make_int2(u.slot0, u.nsplit);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int gr = lane >> 2, t = lane & 3;
+  const int rows = s.n * a.g, r0 = u.tile * R;
+  const int q0 = r0 / a.g, q1 = (min(rows, r0 + R) - 1) / a.g;
+  const Span sp = span_of<BLK>(a, s, q0, q1);
+  const int per = ceil_div(sp.nb, u.nsplit);
+  const int i0 = u.split * per, i1 = min(sp.nb, i0 + per);
+
+  // ---- queries: fp16 fragments of q 2^e (e per row: the largest becomes about
+  // 2^10, so bf16's range is kept and so are 20 binades below the row's largest)
+  uint32_t qf[NT][KW][4];
+  float qsum[NT][2], qmul[NT][2];        // of columns 2t, 2t + 1
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = r0 + 8 * nt + gr;
+    float x[KW][8];
+    float big = 0.f, sum = 0.f;
+    if (r < rows) {
+      const int qi = r / a.g;
+      const uint16_t* p = a.q + (int64_t)(s.row0 + qi) * a.q_st +
+                          (int64_t)(head * a.g + r - qi * a.g) * a.q_sh + t * (D / 4);
+#pragma unroll
+      for (int w = 0; w < KW; ++w)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint16_t h = __ldg(p + 8 * w + j);
+          x[w][j] = a.dt == BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
+          big = fmaxf(big, fabsf(x[w][j]));
+        }
+    } else {
+#pragma unroll
+      for (int w = 0; w < KW; ++w)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[w][j] = 0.f;
+    }
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    const int e = min(max(137 - (int)(__float_as_uint(big) >> 23), -126), 126);
+    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[w][j] *= up;
+        sum += x[w][j];
+      }
+      qf[nt][w][0] = pack_half2(x[w][0], x[w][4]);
+      qf[nt][w][1] = pack_half2(x[w][1] * 0.0625f, x[w][5] * 0.0625f);
+      qf[nt][w][2] = pack_half2(x[w][2], x[w][6]);
+      qf[nt][w][3] = pack_half2(x[w][3] * 0.0625f, x[w][7] * 0.0625f);
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    sum *= 0x1p-24f;
+    const float mul = a.scale_log2 * down * 0x1p24f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      qsum[nt][c] = __shfl_sync(0xffffffffu, sum, (2 * t + c) * 4);
+      qmul[nt][c] = __shfl_sync(0xffffffffu, mul, (2 * t + c) * 4);
+    }
+  }
+  // the keys each column's row sees: j < chi and (j >= clo or j < sinks)
+  int clo[NT][2], chi[NT][2];
+  int all_lo = 0, all_hi = INT32_MAX, any_lo = INT32_MAX, any_hi = 0;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = r0 + 8 * nt + 2 * t + c;
+      const int p = s.L - s.n + (r < rows ? r : rows - 1) / a.g;
+      chi[nt][c] = max(0, a.causal ? min(s.L, p + 1) : s.L);
+      clo[nt][c] = a.window ? max(0, p - a.window + 1) : 0;
+      all_lo = max(all_lo, clo[nt][c]);
+      all_hi = min(all_hi, chi[nt][c]);
+      any_lo = min(any_lo, clo[nt][c]);
+      any_hi = max(any_hi, chi[nt][c]);
+    }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
+    all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
+    any_lo = min(any_lo, __shfl_xor_sync(0xffffffffu, any_lo, o));
+    any_hi = max(any_hi, __shfl_xor_sync(0xffffffffu, any_hi, o));
+  }
+
+  float o[NT][MT][4];
+  float m[NT][2], me[NT][2], l[NT][2], zs[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      m[nt][c] = -INFINITY;     // the running maximum
+      me[nt][c] = 0.f;          // the same, 0 while there is none
+      l[nt][c] = zs[nt][c] = 0.f;
+    }
+  }
+  // values' scales are taken relative to 2^-ve so that p s' fits fp16: the
+  // largest so far lies below 2^6 (times 2^8 of a lagging maximum, below 2^14)
+  float fv = 0.f;
+
+  // ---- keys: the warp's steps are its 16 tokens of every block i0 .. i1 - 1;
+  // page ids for 32 steps at a time, one per lane
+  const int steps = i1 > i0 ? i1 - i0 : 0;
+  int page_lane = -1;
+  auto tok_of = [&](int i) { return (i < sp.sb ? i : sp.lb + i - sp.sb) * BLK + 16 * warp; };
+  auto fetch_pages = [&](int st) {
+    const int i = i0 + st + lane;
+    page_lane = -1;
+    if (st + lane < steps) {
+      const int j = tok_of(i);
+      if (j < any_hi) {
+        page_lane = a.b.table[u.b * a.b.table_ld + (j >> a.cache.lgP)];
+        if (page_lane < 0 || page_lane >= a.cache.pages) {
+          const bool seen = j + 16 > any_lo || j < a.sinks;
+          if (seen) kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
+          page_lane = -1;
+        }
+      }
+    }
+  };
+  // the step's codes, zeros where it has no page
+  auto fetch = [&](Step<D>& d, int st) -> bool {
+    if ((st & 31) == 0) fetch_pages(st);
+    const int pg = __shfl_sync(0xffffffffu, page_lane, st & 31);
+    if (pg < 0) return false;
+    const uint8_t* blk = a.cache.base + ((int64_t)pg * a.cache.heads + head) * a.cache.block_bytes;
+    load_step<D>(d, a, blk, tok_of(i0 + st) & (a.cache.P - 1), gr, t);
+    return true;
+  };
+
+  Step<D> cur, nxt;
+  bool have = steps > 0 && fetch(nxt, 0);
+  for (int st = 0; st < steps; ++st) {
+    cur = nxt;
+    const bool valid = have;
+    have = st + 1 < steps && fetch(nxt, st + 1);
+    if (!valid) continue;
+    const int j0 = tok_of(i0 + st);
+    const int ja = j0 + 4 * (gr >> 1) + (gr & 1);        // this lane's two tokens: ja, ja + 2
+    const bool masked = !(j0 + 16 <= all_hi && (j0 >= all_lo || j0 + 16 <= a.sinks));
+    if (masked) {
+      // what no row sees may be memory that was never written
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int j = ja + 2 * k;
+        if (!(j < any_hi && (j >= any_lo || j < a.sinks))) cur.kw[k] = cur.vw[k] = 0;
+      }
+    }
+    float sk[2], zk[2], sv[2], zv[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      sk[k] = word_scale(cur.kw[k]);
+      zk[k] = word_zero(cur.kw[k]);
+      sv[k] = word_scale(cur.vw[k]);
+      zv[k] = word_zero(cur.vw[k]);
+    }
+    float x[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) x[nt][2 * k + c] = -zk[k] * qsum[nt][c];
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        const uint32_t ua = cur.k[0][w], ub = cur.k[1][w];
+        mma16816(x[nt], ua & 0x000f000fu, ub & 0x000f000fu, ua & 0x00f000f0u, ub & 0x00f000f0u,
+                 qf[nt][w][0], qf[nt][w][1]);
+        const uint32_t va = ua >> 8, vb = ub >> 8;
+        mma16816(x[nt], va & 0x000f000fu, vb & 0x000f000fu, va & 0x00f000f0u, vb & 0x00f000f0u,
+                 qf[nt][w][2], qf[nt][w][3]);
+      }
+    }
+    bool move = sv[0] * fv > 64.f || sv[1] * fv > 64.f || fv == 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float& y = x[nt][2 * k + c];
+          y *= sk[k] * qmul[nt][c];
+          if (masked) {
+            const int j = ja + 2 * k;
+            if (!(j < chi[nt][c] && (j >= clo[nt][c] || j < a.sinks))) y = -INFINITY;
+          }
+          move |= y > m[nt][c] + 8.f;
+        }
+    if (__any_sync(0xffffffffu, move)) {
+      // new maxima (per column, over the lanes of equal t) and value scale
+      float big = fmaxf(sv[0], sv[1]);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+      float turn = 1.f;
+      if (big * fv > 64.f || (fv == 0.f && big > 0.f)) {
+        const int e = min(max(127 - (int)(__float_as_uint(big) >> 23), -100), 100);
+        const float nf = __uint_as_float((uint32_t)(127 + e) << 23);
+        // (kept finite when the scale is infinite or NaN: those rows are NaN)
+        turn = fv == 0.f ? 1.f : nf / fv;
+        fv = nf;
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float al[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float y = fmaxf(x[nt][c], x[nt][2 + c]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+          const float nm = fmaxf(m[nt][c], y);
+          al[c] = m[nt][c] == nm ? 1.f : exp2_approx(m[nt][c] - nm);
+          m[nt][c] = nm;
+          me[nt][c] = nm == -INFINITY ? 0.f : nm;
+          l[nt][c] *= al[c];
+          al[c] *= turn;
+          zs[nt][c] *= al[c];
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[nt][i][j] *= al[j & 1];
+      }
+    }
+    const float svf[2] = {sv[0] * fv, sv[1] * fv};
+    uint32_t pf[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float pp[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float y = x[nt][2 * k + c];
+          const float p = exp2_approx(y - me[nt][c]);
+          l[nt][c] += p;
+          pp[c] = p * svf[k];
+          if (masked && y == -INFINITY) pp[c] = 0.f;     // (0 times a NaN scale)
+        }
+        const uint32_t h = pack_half2(pp[0], pp[1]);
+        // the zero points' part from the same rounded probabilities
+        const float2 rp = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        zs[nt][0] += rp.x * zv[k];
+        zs[nt][1] += rp.y * zv[k];
+        pf[nt][k] = turn8x8(h);
+      }
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {
+      uint32_t lo01 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x5410);
+      uint32_t hi01 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x7632);
+      uint32_t lo23 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x5410);
+      uint32_t hi23 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x7632);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t p01 = q == 0 ? lo01 : q == 1 ? lo01 >> 8 : q == 2 ? hi01 : hi01 >> 8;
+        const uint32_t p23 = q == 0 ? lo23 : q == 1 ? lo23 >> 8 : q == 2 ? hi23 : hi23 >> 8;
+        const uint32_t a0 = p01 & 0x000f000fu, a1 = p01 & 0x00f000f0u, a2 = p23 & 0x000f000fu,
+                       a3 = p23 & 0x00f000f0u;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][4 * w + q], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+      }
+    }
+  }
+
+  // ---- join the warps
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], d);
+        zs[nt][c] += __shfl_xor_sync(0xffffffffu, zs[nt][c], d);
+      }
+      if (gr == 0) {
+        merge_ml[warp][8 * nt + 2 * t + c][0] = m[nt][c];
+        merge_ml[warp][8 * nt + 2 * t + c][1] = l[nt][c];
+      }
+    }
+  __syncthreads();
+  const float rfv = fv == 0.f ? 0.f : 1.f / fv;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = 8 * nt + 2 * t + c;
+      float mx = merge_ml[0][r][0];
+#pragma unroll
+      for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, merge_ml[w][r][0]);
+      const float f = m[nt][c] == -INFINITY ? (l[nt][c] == 0.f ? 0.f : NAN)
+                                            : exp2_approx(m[nt][c] - mx) * rfv;
+      float* row = merge_o + (warp * R + r) * D;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        // tile 4 w + q: dims gr (D / 8) + 8 w + 2 q and the next
+        const int d = gr * (D / 8) + 8 * (i >> 2) + 2 * (i & 3);
+        row[d] = (o[nt][i][c] * 0x1p24f - zs[nt][c]) * f;
+        row[d + 1] = (o[nt][i][2 + c] * 0x1p20f - zs[nt][c]) * f;
+      }
+    }
+  __syncthreads();
+  const int64_t slot = ((int64_t)(u.slot0 + (int)blockIdx.x - u.base) * a.cache.heads + head) * R;
+  for (int e = threadIdx.x; e < R * (D / 4); e += THREADS) {
+    const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
+    if (r0 + r >= rows) break;
+    float mx = merge_ml[0][r][0];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, merge_ml[w][r][0]);
+    float ls = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float mw = merge_ml[w][r][0], lw = merge_ml[w][r][1];
+      ls += mw == -INFINITY ? lw : lw * exp2_approx(mw - mx);
+      const float4 v = *reinterpret_cast<const float4*>(merge_o + (w * R + r) * D + d);
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
+    if (u.nsplit > 1) {
+      *reinterpret_cast<float4*>(a.part_o + (slot + r) * D + d) = acc;
+      if (d == 0) a.part_ml[slot + r] = {mx, ls};
+      continue;
+    }
+    const int qi = (r0 + r) / a.g, hq = head * a.g + (r0 + r) - qi * a.g;
+    store_row(a, s.row0 + qi, hq, d, acc, mx, ls);
+  }
+}
+
+// Joins the splits of the rows that have some: a block per token and `hpb` query
+// heads, its warps one row each at a time.
+template <int D>
+__global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, int R, int hpb) {
+  constexpr int E = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i = blockIdx.x;
+  const int b = find_sequence(a.b.q_start, a.b.B, i);
+  if (b < 0 || b >= a.b.B) return;
+  const Seq s = seq_of(a, b, nullptr);
+  if (i < s.row0 || i >= s.row0 + s.n) return;
+  const int2 mt = a.meta[b];
+  const int ns = mt.y;
+  if (ns <= 1) return;
+  for (int h = warp; h < hpb; h += WARPS) {
+    const int hq = blockIdx.y * hpb + h;
+    if (hq >= a.Hq) return;
+    const int head = hq / a.g, r = (i - s.row0) * a.g + hq - head * a.g;
+    const int tile = r / R;
+    if (mt.x < 0 || mt.x + (tile + 1) * ns > a.slots) return;
+    const int64_t stride = (int64_t)a.cache.heads * R;
+    const int64_t s0 = ((int64_t)(mt.x + tile * ns) * a.cache.heads + head) * R + (r - tile * R);
+    float m = -INFINITY;
+    for (int k = lane; k < ns; k += 32) m = fmaxf(m, a.part_ml[s0 + k * stride].m);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float l = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int k0 = 0; k0 < ns; k0 += 32) {
+      float w = 0.f;
+      if (k0 + lane < ns) {
+        const Part p = a.part_ml[s0 + (k0 + lane) * stride];
+        // a split without a key (m = -inf, l = 0) counts nothing; a NaN stays
+        w = p.m == -INFINITY ? (p.l == 0.f ? 0.f : NAN) : exp2_approx(p.m - m);
+        l += w == 0.f ? 0.f : p.l * w;
+      }
+      const int kn = min(32, ns - k0);
+#pragma unroll 4
+      for (int k = 0; k < kn; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const float* p = a.part_o + (s0 + (k0 + k) * stride) * D + lane * E;
+        float v[E];
+        if constexpr (E == 2) {
+          const float2 x = *reinterpret_cast<const float2*>(p);
+          v[0] = x.x;
+          v[1] = x.y;
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; e += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(p + e);
+            v[e] = x.x;
+            v[e + 1] = x.y;
+            v[e + 2] = x.z;
+            v[e + 3] = x.w;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(wk, v[e], o[e]);
+      }
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if constexpr (E == 2) {
+      const float x = __shfl_down_sync(0xffffffffu, o[0], 1), y = __shfl_down_sync(0xffffffffu, o[1], 1);
+      if (!(lane & 1)) store_row(a, i, hq, 2 * lane, make_float4(o[0], o[1], x, y), m, l);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; e += 4)
+        store_row(a, i, hq, lane * E + e, make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]), m, l);
+    }
+  }
+}
+
+size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+constexpr unsigned long long TARGET = 148ull * 12;   // units over all heads
+constexpr int MIN_CHUNK = 2;                         // 128 keys
+
+struct Layout {
+  size_t meta, ml, o, total;
+};
+
+Layout layout_of(int R, int D, int heads, int64_t B) {
+  const size_t rows = (size_t)max_slots(heads, TARGET) * heads * R;
+  Layout w;
+  w.meta = 0;
+  w.ml = up256((size_t)B * sizeof(int2));
+  w.o = w.ml + up256(rows * sizeof(Part));
+  w.total = w.o + up256(rows * D * sizeof(float));
+  return w;
+}
+
+template <int D, int NT>
+int launch(AttendArgs& a, cudaStream_t st) {
+  constexpr int R = 8 * NT;
+  const long long ux = max_units(a.T, a.g, a.b.B, R, a.cache.heads, a.target);
+  if (ux > INT32_MAX) return KRONQ_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)ux, (unsigned)a.cache.heads);
+  kv4_attend_kernel<D, NT><<<grid, THREADS, (size_t)WARPS * R * D * sizeof(float), st>>>(a);
+  KQ_CHECK_LAUNCH();
+  // no sequence can be split when the longest one the table holds is one chunk
+  const long long most = (((long long)a.b.max_pages << a.cache.lgP) + BLK - 1) / BLK;
+  if (most <= a.min_chunk) return KRONQ_OK;
+  const int hpb = (long long)a.T * a.Hq <= 16384 ? WARPS : a.Hq;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.T, (unsigned)((a.Hq + hpb - 1) / hpb));
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D>, (const AttendArgs)a, R, hpb) != cudaSuccess)
+    return KRONQ_ERR_CUDA;
+  KQ_CHECK_LAUNCH();
+  return KRONQ_OK;
+}
+
+}  // namespace
+}  // namespace kv4
+
+size_t kq_kv4_attention_ws(int64_t T, int Hq, int heads, int D, int64_t B) {
+  if (T < 0 || Hq <= 0 || heads <= 0 || Hq % heads || B <= 0 || (D != 64 && D != 128 && D != 256)) return 0;
+  return kv4::layout_of(16, D, heads, B).total;
+}
+
+int kq_kv4_attention(const void* q, int64_t q_st, int64_t q_sh, int dtype, int64_t T, int Hq, int D,
+                     const kv4::Cache& c, const kv4::Batch& b, float scale, int causal, int window,
+                     int sinks, void* out, int64_t o_st, int64_t o_sh, float* lse, int32_t* info,
+                     void* ws, size_t ws_bytes, cudaStream_t st) {
+  using namespace kv4;
+  if (dtype != BF16 && dtype != FP16) return KRONQ_ERR_UNSUPPORTED;
+  if (T < 0 || T > INT32_MAX || Hq <= 0 || Hq % c.heads || window < 0 || sinks < 0 ||
+      (window && !causal) || !(scale == scale))
+    return KRONQ_ERR_INVALID_ARG;
+  if (T == 0) return KRONQ_OK;
+  if (!q || !out || !kqh::aligned(q, 2) || !kqh::aligned(out, 8) || q_st < 0 || q_sh < 0 || o_st < 0 ||
+      o_sh < 0 || o_st % 4 || o_sh % 4 || !kqh::aligned(lse, 4))
+    return KRONQ_ERR_INVALID_ARG;
+  if (!ws || !kqh::aligned(ws, 256) || ws_bytes < kq_kv4_attention_ws(T, Hq, c.heads, D, b.B))
+    return KRONQ_ERR_WORKSPACE;
+  const int g = Hq / c.heads;
+  if (T * g > INT32_MAX / 2) return KRONQ_ERR_UNSUPPORTED;
+  AttendArgs a = {};
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_st = q_st;
+  a.q_sh = q_sh;
+  a.out = out;
+  a.o_st = o_st;
+  a.o_sh = o_sh;
+  a.lse = lse;
+  a.cache = c;
+  a.b = b;
+  a.T = (int)T;
+  a.Hq = Hq;
+  a.g = g;
+  a.dt = dtype;
+  a.causal = causal;
+  a.window = window > (1 << 30) ? 0 : window;    // wider than any sequence
+  a.sinks = !a.window ? 0 : sinks > (1 << 30) ? 1 << 30 : sinks;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.min_chunk = MIN_CHUNK;
+  a.target = TARGET;
+  a.slots = (int)max_slots(c.heads, TARGET);
+  a.info = info;
+  const int NT = D == 256 || T * g <= 8 * (long long)b.B ? 1 : 2;
+  const Layout w = layout_of(8 * NT, D, c.heads, b.B);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  a.meta = reinterpret_cast<int2*>(base + w.meta);
+  a.part_ml = reinterpret_cast<Part*>(base + w.ml);
+  a.part_o = reinterpret_cast<float*>(base + w.o);
+  if (D == 64) return NT == 1 ? launch<64, 1>(a, st) : launch<64, 2>(a, st);
+  if (D == 128) return NT == 1 ? launch<128, 1>(a, st) : launch<128, 2>(a, st);
+  return launch<256, 1>(a, st);
+}

@@ -1,0 +1,199 @@
+// What the attention kernels over the 4-bit cache share: arguments, the keys
+// a tile of query rows sees, and the division of the work.
+//
+// Rows of a sequence and key/value head: r = query * group + (query head within
+// the group), so a tile of R consecutive rows shares the keys it reads.  Key
+// blocks a tile sees: the first `sb` blocks (the sinks) and blocks lb .. he-1
+// (the window, or everything); block i of the tile's nb is i < sb ? i : lb + i - sb.
+//
+// Lengths are on the device (a captured graph serves any), so the division is
+// made there: every block adds up the work of the batch, sets the chunk of key
+// blocks that gives about `target` units, and finds its own (sequence, tile,
+// split) in the running sum of units.  A sequence with one split is written
+// straight to the output; the units of the others leave partial results, in
+// slots counted over those sequences alone, that kv4_merge_kernel joins.
+#pragma once
+
+#include "kv4.cuh"
+
+namespace kv4 {
+
+struct Part {            // one (row, split): unnormalised sum relative to 2^m
+  float m, l;
+};
+
+struct AttendArgs {
+  const uint16_t* q;
+  int64_t q_st, q_sh;
+  void* out;
+  int64_t o_st, o_sh;
+  float* lse;            // T x Hq, or null
+  Cache cache;
+  Batch b;
+  int T, Hq, g, dt;
+  int causal, window, sinks;
+  float scale_log2;      // softmax scale x log2 e
+  int min_chunk;         // key blocks
+  unsigned long long target;
+  float* part_o;         // slots x heads x R x D
+  Part* part_ml;         // slots x heads x R
+  int2* meta;            // per sequence: first slot, splits
+  int slots;             // there are that many
+  int32_t* info;
+};
+
+struct Seq {
+  int row0, n, L;        // first token row, new tokens, cached tokens
+};
+
+struct Unit {
+  int b, tile, split, nsplit;
+  int base, slot0;       // the sequence's first unit and first slot
+};
+
+struct Span {
+  int sb, lb, nb;
+};
+
+// bad: set when the batch's numbers contradict each other or the table
+KQ_DEV Seq seq_of(const AttendArgs& a, int b, bool* bad) {
+  Seq s;
+  const int s0 = a.b.q_start[b], s1 = a.b.q_start[b + 1];
+  const int len = a.b.kv_len[b];
+  const int cap = a.b.max_pages << a.cache.lgP;
+  s.row0 = s0;
+  s.n = s1 > s0 && s0 >= 0 && s1 <= a.T ? s1 - s0 : 0;
+  s.L = len < 0 ? 0 : len > cap ? cap : len;
+  if (bad) *bad = s0 < 0 || s1 < s0 || s1 > a.T || len < 0 || len > cap;
+  return s;
+}
+
+KQ_DEV int ceil_div(int x, int y) { return (x + y - 1) / y; }
+
+template <int R, int BLK>
+KQ_DEV void seq_work(const AttendArgs& a, const Seq& s, int* tiles, int* blocks) {
+  *tiles = (int)(((long long)s.n * a.g + R - 1) / R);
+  int nb = ceil_div(s.L, BLK);
+  if (a.window) {
+    const long long w = (long long)min(a.sinks, s.L) / BLK + 1 +
+                        ((long long)a.window + min(s.n, R / a.g + 2)) / BLK + 2;
+    if (w < nb) nb = (int)w;
+  }
+  *blocks = nb;
+}
+
+// Key blocks the rows of queries q0 .. q1 see.
+template <int BLK>
+KQ_DEV Span span_of(const AttendArgs& a, const Seq& s, int q0, int q1) {
+  const int p0 = s.L - s.n + q0, p1 = s.L - s.n + q1;
+  const int hi = a.causal ? min(s.L, p1 + 1) : s.L;
+  Span r = {0, 0, 0};
+  if (hi <= 0) return r;
+  const int lo = a.window ? max(0, min(hi, p0 - a.window + 1)) : 0;
+  r.sb = ceil_div(min(a.sinks, lo), BLK);
+  r.lb = max(r.sb, lo / BLK);
+  r.nb = r.sb + max(0, ceil_div(hi, BLK) - r.lb);
+  return r;
+}
+
+// Finds unit u (all threads of the block call it; false: there is none).
+template <int R, int BLK, int THREADS>
+KQ_DEV bool find_unit(const AttendArgs& a, int u, Unit* out) {
+  __shared__ unsigned long long sums[THREADS / 32];
+  __shared__ unsigned long long wsum[THREADS / 32];
+  __shared__ Unit found;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = ceil_div(a.b.B, THREADS);
+  const int b0 = min(a.b.B, tid * per), b1 = min(a.b.B, b0 + per);
+  int tiles1 = 0, blocks1 = 0;                 // kept when a thread has one sequence
+  unsigned long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    bool bad;
+    seq_work<R, BLK>(a, seq_of(a, b, &bad), &tiles1, &blocks1);
+    if (bad && (blockIdx.x | blockIdx.y) == 0) kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
+    mine += (unsigned long long)tiles1 * blocks1;
+  }
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) sums[warp] = mine;
+  if (tid == 0) found.b = -1;
+  __syncthreads();
+  unsigned long long total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) total += sums[w];
+  const unsigned long long c = (total * a.cache.heads + a.target - 1) / a.target;
+  const int chunk = (int)max((unsigned long long)a.min_chunk, c);
+  // low half: units; high half: those that need a slot
+  unsigned long long units = 0;
+  for (int b = b0; b < b1; ++b) {
+    if (per > 1) seq_work<R, BLK>(a, seq_of(a, b, nullptr), &tiles1, &blocks1);
+    const int ns = max(1, ceil_div(blocks1, chunk));
+    const unsigned long long k = (unsigned long long)tiles1 * ns;
+    units += k + (ns > 1 ? k << 32 : 0);
+  }
+  unsigned long long incl = units;
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  unsigned long long before = incl - units;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w)
+    if (w < warp) before += wsum[w];
+  int base = (int)(uint32_t)before, slot0 = (int)(before >> 32);
+  if (u >= base && u < base + (int)(uint32_t)units) {
+    for (int b = b0; b < b1; ++b) {
+      if (per > 1) seq_work<R, BLK>(a, seq_of(a, b, nullptr), &tiles1, &blocks1);
+      const int ns = max(1, ceil_div(blocks1, chunk)), k = tiles1 * ns;
+      if (u < base + k) {
+        found.tile = (u - base) / ns;
+        found.split = u - base - found.tile * ns;
+        found.nsplit = ns;
+        found.base = base;
+        found.slot0 = slot0;
+        found.b = b;
+        break;
+      }
+      base += k;
+      if (ns > 1) slot0 += k;
+    }
+  }
+  __syncthreads();
+  *out = found;
+  return found.b >= 0;
+}
+
+// Four dims from d on of one output row from its sum relative to 2^m; a row
+// that saw no key is 0 with a log-sum-exp of -inf.
+KQ_DEV void store_row(const AttendArgs& a, int row, int hq, int d, float4 o, float m, float l) {
+  const float r = l == 0.f ? 0.f : 1.f / l;
+  o.x *= r;
+  o.y *= r;
+  o.z *= r;
+  o.w *= r;
+  uint16_t* p = static_cast<uint16_t*>(a.out) + (int64_t)row * a.o_st + (int64_t)hq * a.o_sh + d;
+  uint2 w;
+  if (a.dt == BF16) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x, o.y), y = __floats2bfloat162_rn(o.z, o.w);
+    w = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  } else {
+    const __half2 x = __floats2half2_rn(o.x, o.y), y = __floats2half2_rn(o.z, o.w);
+    w = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  }
+  *reinterpret_cast<uint2*>(p) = w;
+  if (a.lse && d == 0)
+    a.lse[(int64_t)row * a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// Bounds of what find_unit hands out: a sequence with t tiles and w key blocks
+// has t ceil(w / chunk) <= t + t w / chunk units, and at most twice t w / chunk
+// when it is split.
+inline long long max_units(long long T, int g, int B, int R, int heads, unsigned long long target) {
+  return (T * g) / R + B + (long long)(target / heads) + 1;
+}
+inline long long max_slots(int heads, unsigned long long target) {
+  return 2 * (long long)(target / heads) + 2;
+}
+
+}  // namespace kv4

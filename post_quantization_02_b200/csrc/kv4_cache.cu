@@ -1,0 +1,454 @@
+// Writing and reading back the paged 4-bit key/value cache (layout: kv4.cuh).
+//
+// kv4_append_kernel: for each new token the rotation by its position, then the
+// signed Hadamard transform (keys and queries), then the 4-bit grid (keys and
+// values).  Every step is one fp32 operation with its own rounding, in a fixed
+// order, so codes and words are reproducible bit for bit:
+//   rotation      y_a = a cos - b sin, y_b = b cos + a sin
+//   Hadamard      x -> D^-1/2 H (signs x), butterflies of distance 1, 2, 4, ...
+//   grid          lo = min(0, min x), hi = max(0, max x),
+//                 s = max((hi - lo) (1/15), 2^-100) rounded to 20 bits, r = 1/s,
+//                 zero = clamp(rint(-lo r), 0, 15),
+//                 code = clamp(rint(x r) + zero, 0, 15)
+// (the library's asymmetric grid with the division by s as a product with
+// 1/s, taken once per vector: a division per value would cost more than the
+// whole rest).  A vector with a NaN or an infinity, or wider than fp32, gets a
+// NaN scale: it reads back as NaN instead of as some other value.
+//
+// Split: 8 lanes per vector (a query, key or value head of one token), four
+// vectors of the same token per warp; lane l holds dims 8 l + 64 r .. + 8, so
+// loads are 16 bytes per lane and 128 bytes per vector and r, the first three
+// butterflies and the last (D/64) are inside the lane, three go by shuffle, and
+// a run of 8 dims is one word of codes.
+#include "kv4.cuh"
+
+namespace {
+
+using namespace kv4;
+
+constexpr int TPB = 128;
+constexpr int ITEMS = TPB / 8;      // vectors per block
+
+KQ_DEV float to_f32(uint16_t h, int dt) {
+  return dt == BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
+}
+
+KQ_DEV void unpack8(const uint4& u, int dt, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (dt == BF16) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+}
+
+KQ_DEV uint4 pack8(const float (&x)[8], int dt) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (dt == BF16) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 8 consecutive elements at p: one 16-byte load, or element loads where the
+// tensor's address or strides are not multiples of 16 bytes.
+KQ_DEV void load8(const uint16_t* p, bool vec, int dt, float (&x)[8]) {
+  if (vec) {
+    unpack8(__ldg(reinterpret_cast<const uint4*>(p)), dt, x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = to_f32(__ldg(p + i), dt);
+  }
+}
+
+struct Rows {
+  const uint16_t* p;
+  int64_t st, sh;     // strides of the token and of the head (elements)
+  int vec;
+};
+
+struct AppendArgs {
+  Rows q, k, v;
+  uint16_t* q_out;
+  Cache cache;
+  Batch b;
+  const float* table;         // table_rows x rot: cosines, then sines
+  const int32_t* positions;
+  const int8_t* signs;
+  int64_t table_rows;
+  int T, Hq, dt, rot, interleaved, blocks_per_token;
+  int32_t* info;
+};
+
+// Where a sequence's token `at` lies: its page, or -1 when it is not a token
+// of a cached page.
+KQ_DEV int64_t page_of(const Batch& b, const Cache& c, int s, int at) {
+  const int pg = at >> c.lgP;
+  if (at < 0 || pg >= b.max_pages) return -1;
+  const int64_t id = b.table[s * b.table_ld + pg];
+  return id >= 0 && id < c.pages ? id : -1;
+}
+
+template <int D>
+__global__ void __launch_bounds__(TPB) kv4_append_kernel(const AppendArgs a) {
+  constexpr int R = D / 64;
+  const int i = blockIdx.x / a.blocks_per_token;
+  const int item = (blockIdx.x - i * a.blocks_per_token) * ITEMS + (threadIdx.x >> 3);
+  const int l = threadIdx.x & 7;
+  const int s = find_sequence(a.b.q_start, a.b.B, i);
+  if (s < 0 || s >= a.b.B) return;                       // a row of no sequence (whole warp)
+  const int at = a.b.kv_len[s] - (a.b.q_start[s + 1] - i);
+  const int Hkv = a.cache.heads;
+  const bool act = item < a.Hq + 2 * Hkv;
+  const int kind = item < a.Hq ? 0 : item < a.Hq + Hkv ? 1 : 2;   // query, key, value
+  const int head = kind == 0 ? item : kind == 1 ? item - a.Hq : item - a.Hq - Hkv;
+  const Rows& src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+
+  int64_t pos = a.positions ? a.positions[i] : at;
+  bool ok = act && at >= 0;
+  if (a.rot && (pos < 0 || pos >= a.table_rows)) ok = false;
+  int64_t page = -1;
+  if (ok && kind) {
+    page = page_of(a.b, a.cache, s, at);
+    if (page < 0) ok = false;
+  }
+  if (act && !ok) {
+    if (l == 0) kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
+  }
+
+  float x[R][8];
+  if (ok) {
+    const uint16_t* p = src.p + (int64_t)i * src.st + (int64_t)head * src.sh;
+#pragma unroll
+    for (int r = 0; r < R; ++r) load8(p + 8 * l + 64 * r, src.vec, a.dt, x[r]);
+    if (kind < 2 && a.rot) {
+      const int half = a.rot >> 1;
+      const float* row = a.table + pos * a.rot;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int d = 8 * l + 64 * r;
+        if (d >= a.rot) continue;
+        if (a.interleaved) {
+          const float4 co = __ldg(reinterpret_cast<const float4*>(row + d / 2));
+          const float4 si = __ldg(reinterpret_cast<const float4*>(row + half + d / 2));
+          const float c4[4] = {co.x, co.y, co.z, co.w}, s4[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float u = x[r][2 * j], w = x[r][2 * j + 1];
+            x[r][2 * j] = __fsub_rn(__fmul_rn(u, c4[j]), __fmul_rn(w, s4[j]));
+            x[r][2 * j + 1] = __fadd_rn(__fmul_rn(w, c4[j]), __fmul_rn(u, s4[j]));
+          }
+        } else {
+          // the other half of each pair is a run of another lane (or of this
+          // one): read again, from L1
+          const bool up = d >= half;
+          const int e = up ? d - half : d;
+          float o[8];
+          load8(p + (up ? e : e + half), src.vec, a.dt, o);
+#pragma unroll
+          for (int j4 = 0; j4 < 2; ++j4) {
+            const float4 co = __ldg(reinterpret_cast<const float4*>(row + e + 4 * j4));
+            const float4 si = __ldg(reinterpret_cast<const float4*>(row + half + e + 4 * j4));
+            const float c4[4] = {co.x, co.y, co.z, co.w}, s4[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float u = __fmul_rn(x[r][4 * j4 + j], c4[j]), w = __fmul_rn(o[4 * j4 + j], s4[j]);
+              x[r][4 * j4 + j] = up ? __fadd_rn(u, w) : __fsub_rn(u, w);
+            }
+          }
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[r][j] = 0.f;
+  }
+
+  if (a.signs) {                                          // (all lanes: shuffles)
+    if (kind < 2) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[r][j] = a.signs[8 * l + 64 * r + j] < 0 ? -x[r][j] : x[r][j];
+    }
+    float y[R][8];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[r][j] = x[r][j];
+#pragma unroll
+    for (int h = 1; h < 8; h *= 2)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (!(j & h)) {
+            const float u = y[r][j], w = y[r][j + h];
+            y[r][j] = __fadd_rn(u, w);
+            y[r][j + h] = __fsub_rn(u, w);
+          }
+#pragma unroll
+    for (int h = 1; h < 8; h *= 2)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float w = __shfl_xor_sync(0xffffffffu, y[r][j], h);
+          y[r][j] = (l & h) ? __fsub_rn(w, y[r][j]) : __fadd_rn(y[r][j], w);
+        }
+#pragma unroll
+    for (int h = 1; h < R; h *= 2)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (!(r & h))
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float u = y[r][j], w = y[r + h][j];
+            y[r][j] = __fadd_rn(u, w);
+            y[r + h][j] = __fsub_rn(u, w);
+          }
+    constexpr float norm = D == 64 ? 0.125f : D == 128 ? 0.08838834764831845f : 0.0625f;
+    if (kind < 2) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[r][j] = __fmul_rn(y[r][j], norm);
+    }
+  }
+
+  if (kind == 0) {
+    if (ok) {
+      uint16_t* o = a.q_out + ((int64_t)i * a.Hq + head) * D;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        *reinterpret_cast<uint4*>(o + 8 * l + 64 * r) = pack8(x[r], a.dt);
+    }
+  }
+  // a warp that holds only queries is done; in a mixed warp all lanes go on
+  if (__all_sync(0xffffffffu, kind == 0)) return;
+
+  float lo = 0.f, hi = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      lo = min_nan(lo, x[r][j]);
+      hi = max_nan(hi, x[r][j]);
+    }
+#pragma unroll
+  for (int h = 1; h < 8; h *= 2) {
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, h));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, h));
+  }
+  if (!ok || kind == 0) return;
+  float sc = fmaxf(__fmul_rn(__fsub_rn(hi, lo), 1.f / 15.f), 0x1p-100f);
+  if (!(__fsub_rn(hi, lo) < INFINITY)) sc = INFINITY;     // NaN, infinite or too wide
+  sc = __uint_as_float((__float_as_uint(sc) + 8u) & ~15u);
+  uint32_t word, code[R];
+  if (sc < INFINITY) {
+    const float rs = __fdiv_rn(1.f, sc);
+    const float z = fminf(fmaxf(rintf(__fmul_rn(-lo, rs)), 0.f), 15.f);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      code[r] = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float c = fminf(fmaxf(__fadd_rn(rintf(__fmul_rn(x[r][j], rs)), z), 0.f), 15.f);
+        // c is a whole number: adding 2^23 leaves it in the low mantissa bits
+        code[r] |= (__float_as_uint(__fadd_rn(c, 8388608.f)) & 15u) << (4 * j);
+      }
+    }
+    word = __float_as_uint(sc) | (uint32_t)z;
+  } else {
+    word = 0x7FC00000u;
+#pragma unroll
+    for (int r = 0; r < R; ++r) code[r] = 0;
+  }
+  const int P = a.cache.P, slot = at & (P - 1);
+  uint8_t* blk = a.cache.base + (page * Hkv + head) * (int64_t)a.cache.block_bytes;
+  uint32_t* codes = reinterpret_cast<uint32_t*>(blk + (kind == 2 ? P * (D / 2) : 0)) + slot * (D / 8);
+  uint32_t* words = reinterpret_cast<uint32_t*>(blk + P * D) + (kind == 2 ? P : 0);
+#pragma unroll
+  for (int r = 0; r < R; ++r) codes[l + 8 * r] = code[r];
+  if (l == 0) words[slot] = word;
+}
+
+struct GatherArgs {
+  void* k_out;        // T x heads x D
+  void* v_out;
+  Cache cache;
+  Batch b;
+  int T, dt, blocks_per_token;
+  int32_t* info;
+};
+
+// Reads tokens back as the values they stand for; 8 lanes per vector as above.
+template <int D>
+__global__ void __launch_bounds__(TPB) kv4_gather_kernel(const GatherArgs a) {
+  constexpr int R = D / 64;
+  const int i = blockIdx.x / a.blocks_per_token;
+  const int item = (blockIdx.x - i * a.blocks_per_token) * ITEMS + (threadIdx.x >> 3);
+  const int l = threadIdx.x & 7;
+  const int s = find_sequence(a.b.q_start, a.b.B, i);
+  if (s < 0 || s >= a.b.B) return;
+  const int Hkv = a.cache.heads;
+  if (item >= 2 * Hkv) return;
+  const int isv = item >= Hkv, head = isv ? item - Hkv : item;
+  const int at = a.b.kv_len[s] - (a.b.q_start[s + 1] - i);
+  const int64_t page = page_of(a.b, a.cache, s, at);
+  if (page < 0) {
+    if (l == 0) kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
+    return;
+  }
+  const int P = a.cache.P, slot = at & (P - 1);
+  const uint8_t* blk = a.cache.base + (page * Hkv + head) * (int64_t)a.cache.block_bytes;
+  const uint32_t* codes =
+      reinterpret_cast<const uint32_t*>(blk + (isv ? P * (D / 2) : 0)) + slot * (D / 8);
+  const uint32_t word = reinterpret_cast<const uint32_t*>(blk + P * D)[(isv ? P : 0) + slot];
+  const float sc = word_scale(word), z = word_zero(word);
+  const int64_t row = ((int64_t)i * Hkv + head) * D;
+  void* out = isv ? a.v_out : a.k_out;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const uint32_t c = codes[l + 8 * r];
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      x[j] = __fmul_rn(sc, __fsub_rn(__uint_as_float(0x4B000000u | ((c >> (4 * j)) & 15u)), 8388608.f + z));
+    const int64_t o = row + 8 * l + 64 * r;
+    if (a.dt == FP32) {
+      float4* f = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
+      f[0] = make_float4(x[0], x[1], x[2], x[3]);
+      f[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o) = pack8(x, a.dt);
+    }
+  }
+}
+
+}  // namespace
+
+int kq_kv4_views(void* cache, int64_t pages, int page_size, int heads, int D, const int32_t* table,
+                 int64_t table_ld, int64_t max_pages, const int32_t* q_start, const int32_t* kv_len,
+                 int64_t B, Cache* c, Batch* b) {
+  if (D != 64 && D != 128 && D != 256) return KRONQ_ERR_UNSUPPORTED;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256)
+    return KRONQ_ERR_UNSUPPORTED;
+  if (!cache || !q_start || !kv_len || pages <= 0 || pages > INT32_MAX || heads <= 0 || heads > 65535 ||
+      B <= 0 || B > (1 << 20))
+    return KRONQ_ERR_INVALID_ARG;
+  if (max_pages < 0 || table_ld < max_pages || (max_pages && !table)) return KRONQ_ERR_INVALID_ARG;
+  if (max_pages > (1 << 30) / page_size) return KRONQ_ERR_UNSUPPORTED;   // token indices stay below 2^30
+  if (!kqh::aligned(cache, 16) || !kqh::aligned(table, 4) || !kqh::aligned(q_start, 4) ||
+      !kqh::aligned(kv_len, 4))
+    return KRONQ_ERR_INVALID_ARG;
+  c->base = static_cast<uint8_t*>(cache);
+  c->pages = pages;
+  c->P = page_size;
+  c->lgP = 31 - __builtin_clz((unsigned)page_size);
+  c->heads = heads;
+  c->block_bytes = page_size * (D + 8);
+  b->table = table;
+  b->q_start = q_start;
+  b->kv_len = kv_len;
+  b->table_ld = table_ld;
+  b->B = (int)B;
+  b->max_pages = (int)max_pages;
+  return KRONQ_OK;
+}
+
+namespace {
+
+bool rows_ok(const void* p, int64_t st, int64_t sh, Rows* r) {
+  if (!p || !kqh::aligned(p, 2) || st < 0 || sh < 0) return false;
+  r->p = static_cast<const uint16_t*>(p);
+  r->st = st;
+  r->sh = sh;
+  r->vec = kqh::aligned(p, 16) && st % 8 == 0 && sh % 8 == 0;
+  return true;
+}
+
+}  // namespace
+
+int kq_kv4_append(const void* q, int64_t q_st, int64_t q_sh, const void* k, int64_t k_st, int64_t k_sh,
+                  const void* v, int64_t v_st, int64_t v_sh, int dtype, int64_t T, int Hq, void* q_out,
+                  const float* table, int64_t table_rows, int rot, int interleaved,
+                  const int32_t* positions, const int8_t* signs, int D, const Cache& c, const Batch& b,
+                  int32_t* info, cudaStream_t st) {
+  if (dtype != BF16 && dtype != FP16) return KRONQ_ERR_UNSUPPORTED;
+  if (T < 0 || Hq < 0 || Hq > 65535 || rot < 0 || rot > D || rot % 16) return KRONQ_ERR_INVALID_ARG;
+  if (rot && (!table || table_rows <= 0 || !kqh::aligned(table, 16))) return KRONQ_ERR_INVALID_ARG;
+  if (!kqh::aligned(positions, 4)) return KRONQ_ERR_INVALID_ARG;
+  if (T == 0) return KRONQ_OK;
+  AppendArgs a = {};
+  if (!rows_ok(k, k_st, k_sh, &a.k) || !rows_ok(v, v_st, v_sh, &a.v)) return KRONQ_ERR_INVALID_ARG;
+  if (Hq) {
+    if (!rows_ok(q, q_st, q_sh, &a.q) || !q_out || !kqh::aligned(q_out, 16)) return KRONQ_ERR_INVALID_ARG;
+  }
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.cache = c;
+  a.b = b;
+  a.table = table;
+  a.positions = positions;
+  a.signs = signs;
+  a.table_rows = table_rows;
+  a.Hq = Hq;
+  a.dt = dtype;
+  a.rot = rot;
+  a.interleaved = interleaved;
+  a.blocks_per_token = (Hq + 2 * c.heads + ITEMS - 1) / ITEMS;
+  a.info = info;
+  if (T > INT32_MAX / a.blocks_per_token) return KRONQ_ERR_UNSUPPORTED;
+  a.T = (int)T;
+  const unsigned grid = (unsigned)(T * a.blocks_per_token);
+  if (D == 64)
+    kv4_append_kernel<64><<<grid, TPB, 0, st>>>(a);
+  else if (D == 128)
+    kv4_append_kernel<128><<<grid, TPB, 0, st>>>(a);
+  else
+    kv4_append_kernel<256><<<grid, TPB, 0, st>>>(a);
+  KQ_CHECK_LAUNCH();
+  return KRONQ_OK;
+}
+
+int kq_kv4_gather(void* k_out, void* v_out, int dtype, int64_t T, int D, const Cache& c, const Batch& b,
+                  int32_t* info, cudaStream_t st) {
+  if (dtype != BF16 && dtype != FP16 && dtype != FP32) return KRONQ_ERR_UNSUPPORTED;
+  if (T < 0) return KRONQ_ERR_INVALID_ARG;
+  if (T == 0) return KRONQ_OK;
+  if (!k_out || !v_out || !kqh::aligned(k_out, 16) || !kqh::aligned(v_out, 16)) return KRONQ_ERR_INVALID_ARG;
+  GatherArgs a = {};
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.cache = c;
+  a.b = b;
+  a.dt = dtype;
+  a.blocks_per_token = (2 * c.heads + ITEMS - 1) / ITEMS;
+  a.info = info;
+  if (T > INT32_MAX / a.blocks_per_token) return KRONQ_ERR_UNSUPPORTED;
+  a.T = (int)T;
+  const unsigned grid = (unsigned)(T * a.blocks_per_token);
+  if (D == 64)
+    kv4_gather_kernel<64><<<grid, TPB, 0, st>>>(a);
+  else if (D == 128)
+    kv4_gather_kernel<128><<<grid, TPB, 0, st>>>(a);
+  else
+    kv4_gather_kernel<256><<<grid, TPB, 0, st>>>(a);
+  KQ_CHECK_LAUNCH();
+  return KRONQ_OK;
+}

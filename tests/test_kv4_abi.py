@@ -1,0 +1,116 @@
+"""Refusals of the 4-bit cache's entry points, on the host: through the C ABI
+(nothing is launched) and through the binding's own checks."""
+
+import ctypes
+
+import pytest
+import torch
+
+from post_quantization_02_b200 import abi, build, kv4
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return abi.lib()
+
+
+P = ctypes.c_void_p(4096)   # never dereferenced: refused before any launch
+
+
+def _append(L, **kw):
+    a = dict(q=P, qt=512, qh=128, k=P, kt=512, kh=128, v=P, vt=512, vh=128, dtype=0, T=4, q_heads=4, q_out=P,
+             table=P, rows=16, rot=128, inter=0, pos=None, signs=None, cache=P, pages=8, page=16, heads=2, D=128,
+             bt=P, ld=4, mp=4, qs=P, kv=P, B=2)
+    a.update(kw)
+    return L.kronq_kv4_append(a["q"], a["qt"], a["qh"], a["k"], a["kt"], a["kh"], a["v"], a["vt"], a["vh"], a["dtype"],
+                              a["T"], a["q_heads"], a["q_out"], a["table"], a["rows"], a["rot"], a["inter"], a["pos"],
+                              a["signs"], a["cache"], a["pages"], a["page"], a["heads"], a["D"], a["bt"], a["ld"],
+                              a["mp"], a["qs"], a["kv"], a["B"], None, None)
+
+
+def _attend(L, **kw):
+    a = dict(q=P, qt=512, qh=128, dtype=0, T=4, q_heads=4, cache=P, pages=8, page=16, heads=2, D=128, bt=P, ld=4, mp=4,
+             qs=P, kv=P, B=2, scale=0.1, causal=1, window=0, sinks=0, out=P, ot=512, oh=128, lse=None, ws=P, n=None)
+    a.update(kw)
+    n = L.kronq_kv4_attention_workspace_size(4, 4, 2, 128, 2) if a["n"] is None else a["n"]
+    return L.kronq_kv4_attention(a["q"], a["qt"], a["qh"], a["dtype"], a["T"], a["q_heads"], a["cache"], a["pages"],
+                                 a["page"], a["heads"], a["D"], a["bt"], a["ld"], a["mp"], a["qs"], a["kv"], a["B"],
+                                 ctypes.c_float(a["scale"]), a["causal"], a["window"], a["sinks"], a["out"], a["ot"],
+                                 a["oh"], a["lse"], None, a["ws"], n, None)
+
+
+def test_block_bytes(L):
+    assert L.kronq_kv4_block_bytes(64, 128) == 64 * 136
+    assert L.kronq_kv4_block_bytes(24, 128) == 0 and L.kronq_kv4_block_bytes(512, 128) == 0
+    assert L.kronq_kv4_block_bytes(64, 96) == 0
+
+
+SHARED = [
+    (dict(D=96), -2), (dict(page=48), -2), (dict(page=8), -2), (dict(page=512), -2), (dict(cache=None), -1),
+    (dict(cache=ctypes.c_void_p(4104)), -1), (dict(pages=0), -1), (dict(pages=1 << 31), -1), (dict(heads=0), -1),
+    (dict(B=0), -1), (dict(qs=None), -1), (dict(kv=None), -1), (dict(bt=None), -1), (dict(ld=3), -1),
+    (dict(mp=-1), -1), (dict(mp=1 << 27, ld=1 << 27), -2), (dict(dtype=2), -2), (dict(dtype=9), -2), (dict(T=-1), -1),
+    (dict(qs=ctypes.c_void_p(4098)), -1),
+]
+
+
+@pytest.mark.parametrize("kw,code", SHARED)
+def test_refusals_of_both(L, kw, code):
+    assert _append(L, **kw) == code
+    assert _attend(L, **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(k=None), -1), (dict(v=None), -1), (dict(q=None), -1), (dict(q_out=None), -1),
+    (dict(q_out=ctypes.c_void_p(4104)), -1), (dict(k=ctypes.c_void_p(4097)), -1), (dict(kt=-512), -1),
+    (dict(rot=8), -1), (dict(rot=144), -1), (dict(rot=-16), -1), (dict(table=None), -1), (dict(rows=0), -1),
+    (dict(table=ctypes.c_void_p(4100)), -1), (dict(pos=ctypes.c_void_p(4098)), -1), (dict(q_heads=-1), -1),
+    (dict(T=0), 0),
+])
+def test_append_refusals(L, kw, code):
+    assert _append(L, **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), -1), (dict(out=None), -1), (dict(out=ctypes.c_void_p(4100)), -1), (dict(ot=510), -1),
+    (dict(q_heads=5), -1), (dict(q_heads=0), -1), (dict(window=-1), -1), (dict(sinks=-1), -1),
+    (dict(window=4, causal=0), -1), (dict(scale=float("nan")), -1), (dict(ws=None), -6), (dict(n=1000), -6),
+    (dict(ws=ctypes.c_void_p(4112)), -6), (dict(T=0), 0),
+])
+def test_attention_refusals(L, kw, code):
+    assert _attend(L, **kw) == code
+
+
+def test_workspace_sizes(L):
+    f = L.kronq_kv4_attention_workspace_size
+    assert f(4, 4, 2, 128, 2) > 0
+    assert f(4, 5, 2, 128, 2) == 0 and f(4, 4, 2, 96, 2) == 0 and f(4, 4, 2, 128, 0) == 0 and f(-1, 4, 2, 128, 2) == 0
+
+
+def test_binding_refusals(L):
+    """Types, shapes and devices are refused before the library is called."""
+    with pytest.raises(ValueError):
+        kv4.make_cache(4, 48, 2, 128, device="cpu")
+    cache = kv4.make_cache(4, 16, 2, 128, device="cpu")
+    assert cache.shape == (4, 2, 16 * 136)
+    q = torch.zeros(3, 4, 128, dtype=torch.bfloat16)
+    k = torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    bt, qs, kv = torch.zeros(1, 4, dtype=torch.int32), torch.tensor([0, 3], dtype=torch.int32), torch.tensor(
+        [3], dtype=torch.int32)
+    good = dict(q=q, k=k, v=k, cache=cache, block_table=bt, q_start=qs, kv_len=kv)
+    for change in (dict(), dict(k=k.float()), dict(v=k.half()), dict(q=q.half()), dict(v=k[:, :1]), dict(k=k[:2]),
+                   dict(block_table=bt.long()), dict(q_start=qs[:1]), dict(kv_len=qs), dict(cache=cache[:, :1]),
+                   dict(cache=cache.view(torch.int8)), dict(cache=cache[:, :, :-1]), dict(k=k.transpose(1, 2)),
+                   dict(block_table=bt.expand(2, 4), q_start=torch.zeros(3, dtype=torch.int32), kv_len=qs),
+                   dict(rope=torch.zeros(4, 128, dtype=torch.float64)), dict(signs=torch.ones(64, dtype=torch.int8)),
+                   dict(positions=torch.zeros(2, dtype=torch.int32))):
+        with pytest.raises(ValueError):      # the unchanged call: these tensors are not on a GPU
+            kv4.append(**{**good, **change})
+    good = dict(q=q, cache=cache, block_table=bt, q_start=qs, kv_len=kv, ws=torch.empty(256, dtype=torch.uint8))
+    for change in (dict(), dict(q=q.float()), dict(out=q.half()), dict(out=q[:2]), dict(lse=torch.zeros(3, 3)),
+                   dict(lse=torch.zeros(3, 4, dtype=torch.float64)), dict(q=q[:, :, :64])):
+        with pytest.raises(ValueError):
+            kv4.attend(**{**good, **change})
+    with pytest.raises(ValueError):
+        kv4.gather(cache, bt, qs, kv, 3, 128)
