@@ -91,11 +91,6 @@ def _p(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _a(t):
-    """The address of a tensor, None for none."""
-    return None if t is None else t.data_ptr()
-
-
 def _s(stream):
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
@@ -506,103 +501,125 @@ def kronq_kv4_block_bytes(page_size: int, head_dim: int) -> int:
     return int(lib().kronq_kv4_block_bytes(page_size, head_dim))
 
 
+# These run once per layer and token, so the checks below go straight to the
+# tensors' fields: a decode step's kernels take a few microseconds themselves.
 def _kv_rows(t, name, dtype, T, D):
-    """A T x heads x D tensor with a contiguous last dimension."""
+    """Address and strides of a T x heads x D tensor with a contiguous last dimension."""
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({T}, heads, {D})")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != D:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected ({T}, heads, {D})")
     st, sh, sd = t.stride()
-    if sd != 1 and D != 1:
+    if sd != 1:
         raise ValueError(f"{name} needs unit stride along its last dimension")
     return t.data_ptr(), st, sh
 
 
-def _kv_args(fn, cache, block_table, q_start, kv_len, head_dim, named):
+def _kv_vector(t, name, dtype, count, dev):
+    """Address of a contiguous vector (None: none)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != count or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {count} {dtype} elements in order, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    return t.data_ptr()
+
+
+def _kv_device(*tensors):
+    """The current CUDA device, on which all of them have to be."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev or dev < 0:
+            raise ValueError(f"tensors on {[str(x.device) for x in tensors]}: one CUDA device is wanted")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _kv_args(fn, cache, block_table, q_start, kv_len, D):
     """The (cache, batch) part of a kronq_kv4 call after its checks."""
-    _dev(cache, torch.uint8, "cache", 3)
-    _dev(block_table, torch.int32, "block_table", 2)
-    _dev(q_start, torch.int32, "q_start", 1)
-    _dev(kv_len, torch.int32, "kv_len", 1)
-    _contig(cache, "cache")
+    if cache.dtype is not torch.uint8 or cache.dim() != 3 or not cache.is_contiguous():
+        raise ValueError(f"{fn}: cache must be a contiguous uint8 tensor of 3 dims (pages, heads, bytes)")
+    if block_table.dtype is not torch.int32 or q_start.dtype is not torch.int32 or kv_len.dtype is not torch.int32:
+        raise ValueError(f"{fn}: block_table, q_start and kv_len must be int32")
+    if block_table.dim() != 2 or q_start.dim() != 1 or kv_len.dim() != 1:
+        raise ValueError(f"{fn}: block_table has 2 dims, q_start and kv_len have 1")
     B, max_pages = block_table.shape
-    if q_start.numel() != B + 1 or kv_len.numel() != B:
+    if q_start.shape[0] != B + 1 or kv_len.shape[0] != B:
         raise ValueError(f"{fn}: block_table has {B} rows, q_start {q_start.numel()} entries "
                          f"({B + 1} expected), kv_len {kv_len.numel()} ({B} expected)")
-    if (max_pages > 1 and block_table.stride(1) != 1) or (B > 0 and q_start.stride(0) != 1) or \
-            (B > 1 and kv_len.stride(0) != 1):
+    ld, last = block_table.stride()
+    if B == 1:
+        ld = max_pages
+    if (max_pages > 1 and last != 1) or not q_start.is_contiguous() or not kv_len.is_contiguous():
         raise ValueError(f"{fn}: block_table, q_start and kv_len need unit stride along their last dimension")
-    pages, heads, nbytes = cache.shape
-    page = nbytes // (head_dim + 8)
-    if page * (head_dim + 8) != nbytes:
-        raise ValueError(f"{fn}: a cache block of {nbytes} bytes does not hold whole tokens of head_dim {head_dim}")
-    _on_current_device((cache, "cache"), (block_table, "block_table"), (q_start, "q_start"),
-                       (kv_len, "kv_len"), *named)
-    ld = block_table.stride(0) if B > 1 else max_pages
     if ld < max_pages:
         raise ValueError(f"{fn}: block_table's rows overlap")
-    return (cache.data_ptr(), pages, page, heads, head_dim, block_table.data_ptr(), ld, max_pages,
+    pages, heads, nbytes = cache.shape
+    page = nbytes // (D + 8)
+    if page * (D + 8) != nbytes:
+        raise ValueError(f"{fn}: a cache block of {nbytes} bytes does not hold whole tokens of head_dim {D}")
+    return (cache.data_ptr(), pages, page, heads, D, block_table.data_ptr(), ld, max_pages,
             q_start.data_ptr(), kv_len.data_ptr(), B)
+
+
+def _kv_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def kronq_kv4_append(q, k, v, cache, block_table, q_start, kv_len, q_out=None, table=None,
                      interleaved: bool = False, positions=None, signs=None, info=None, stream=None):
     """New keys and values (T x heads x D, bf16 or fp16) into the 4-bit cache,
     keys and queries rotated on the way (see kronq.h).  q and q_out may be None."""
-    _dev(k, _KV_ROWS, "k", 3)
-    _dev(v, None, "v", 3)
-    _dev(info, torch.int32, "info")
-    _dev(table, torch.float32, "table", 2)
-    _dev(positions, torch.int32, "positions", 1)
-    _dev(signs, torch.int8, "signs", 1)
+    dt = k.dtype
+    if dt not in _KV_ROWS or k.dim() != 3:
+        raise ValueError(f"k must be bf16 or fp16 with 3 dims, got {dt} {tuple(k.shape)}")
     T, heads, D = k.shape
-    kr = _kv_rows(k, "k", k.dtype, T, D)
-    vr = _kv_rows(v, "v", k.dtype, T, D)
+    kr = _kv_rows(k, "k", dt, T, D)
+    vr = _kv_rows(v, "v", dt, T, D)
+    args = _kv_args("kronq_kv4_append", cache, block_table, q_start, kv_len, D)
+    if v.shape[1] != heads or args[3] != heads:
+        raise ValueError("kronq_kv4_append: k, v and the cache differ in their heads")
     if (q is None) != (q_out is None):
         raise ValueError("kronq_kv4_append: q and q_out go together")
-    if v.shape[1] != heads or (isinstance(cache, torch.Tensor) and cache.dim() == 3 and cache.shape[1] != heads):
-        raise ValueError("kronq_kv4_append: k, v and the cache differ in their heads")
-    qr, q_heads, qo = (None, 0, 0), 0, None
-    if q is not None:
-        _dev(q, k.dtype, "q", 3)
-        _dev(q_out, k.dtype, "q_out", 3)
-        qr = _kv_rows(q, "q", k.dtype, T, D)
-        q_heads = q.shape[1]
-        _shape(q_out, q.shape, "q_out")
-        _contig(q_out, "q_out")
-        qo = q_out.data_ptr()
+    if q is None:
+        dev = _kv_device(k, v, cache, block_table, q_start, kv_len)
+        qr, q_heads, qo = (None, 0, 0), 0, None
+    else:
+        qr = _kv_rows(q, "q", dt, T, D)
+        if q_out.dtype is not dt or q_out.shape != q.shape or not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous with q's type and shape")
+        dev = _kv_device(k, v, cache, block_table, q_start, kv_len, q, q_out)
+        q_heads, qo = q.shape[1], q_out.data_ptr()
     rows = rot = 0
     if table is not None:
+        if table.dim() != 2:
+            raise ValueError("table must have 2 dims (positions, rot)")
         rows, rot = table.shape
-        _contig(table, "table")
-    if positions is not None:
-        _numel(positions, T, "positions")
-        _contig(positions, "positions")
-    if signs is not None:
-        _numel(signs, D, "signs")
-        _contig(signs, "signs")
-    args = _kv_args("kronq_kv4_append", cache, block_table, q_start, kv_len, D,
-                    ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out"), (table, "table"),
-                     (positions, "positions"), (signs, "signs"), (info, "info")))
     _check("kronq_kv4_append", lib().kronq_kv4_append(
-        *qr, *kr, *vr, KV_DTYPES[k.dtype], T, q_heads, qo, _a(table), rows, rot, int(bool(interleaved)),
-        _a(positions), _a(signs), *args, _a(info), _s(stream)))
+        *qr, *kr, *vr, KV_DTYPES[dt], T, q_heads, qo, _kv_vector(table, "table", torch.float32, rows * rot, dev),
+        rows, rot, 1 if interleaved else 0, _kv_vector(positions, "positions", torch.int32, T, dev),
+        _kv_vector(signs, "signs", torch.int8, D, dev), *args, _kv_vector(info, "info", torch.int32, 1, dev),
+        _kv_stream(stream, dev)))
 
 
 def kronq_kv4_gather(cache, block_table, q_start, kv_len, k_out, v_out, info=None, stream=None):
     """The values the cache holds for the batch's new tokens (see kronq.h)."""
-    _dev(k_out, tuple(KV_DTYPES), "k_out", 3)
-    _dev(v_out, k_out.dtype, "v_out", 3)
-    _dev(info, torch.int32, "info")
-    _shape(v_out, k_out.shape, "v_out")
-    _contig(k_out, "k_out"); _contig(v_out, "v_out")
+    dt = k_out.dtype
+    if dt not in KV_DTYPES or k_out.dim() != 3 or not k_out.is_contiguous():
+        raise ValueError(f"k_out must be contiguous bf16, fp16 or fp32 with 3 dims, got {dt} {tuple(k_out.shape)}")
+    if v_out.dtype is not dt or v_out.shape != k_out.shape or not v_out.is_contiguous():
+        raise ValueError("v_out must be contiguous with k_out's type and shape")
     T, heads, D = k_out.shape
-    args = _kv_args("kronq_kv4_gather", cache, block_table, q_start, kv_len, D,
-                    ((k_out, "k_out"), (v_out, "v_out"), (info, "info")))
-    if cache.shape[1] != heads:
+    args = _kv_args("kronq_kv4_gather", cache, block_table, q_start, kv_len, D)
+    if args[3] != heads:
         raise ValueError("kronq_kv4_gather: k_out and the cache differ in their heads")
+    dev = _kv_device(k_out, v_out, cache, block_table, q_start, kv_len)
     _check("kronq_kv4_gather", lib().kronq_kv4_gather(
-        k_out.data_ptr(), v_out.data_ptr(), KV_DTYPES[k_out.dtype], T, *args, _a(info), _s(stream)))
+        k_out.data_ptr(), v_out.data_ptr(), KV_DTYPES[dt], T, *args, _kv_vector(info, "info", torch.int32, 1, dev),
+        _kv_stream(stream, dev)))
 
 
 def kronq_kv4_attention_workspace_size(T: int, q_heads: int, heads: int, head_dim: int, batch: int) -> int:
@@ -618,24 +635,24 @@ def kv4_workspace(T: int, q_heads: int, heads: int, head_dim: int, batch: int, d
 def kronq_kv4_attention(q, cache, block_table, q_start, kv_len, out, ws, scale: float, causal: bool = True,
                         window: int = 0, sinks: int = 0, lse=None, info=None, stream=None):
     """out = attention of q (T x q_heads x D) over the 4-bit cache (see kronq.h)."""
-    _dev(q, _KV_ROWS, "q", 3)
-    _dev(out, q.dtype, "out", 3)
-    _dev(lse, torch.float32, "lse", 2)
-    _dev(info, torch.int32, "info")
-    _dev(ws, None, "ws")
+    dt = q.dtype
+    if dt not in _KV_ROWS or q.dim() != 3:
+        raise ValueError(f"q must be bf16 or fp16 with 3 dims, got {dt} {tuple(q.shape)}")
     T, q_heads, D = q.shape
-    qr = _kv_rows(q, "q", q.dtype, T, D)
-    orow = _kv_rows(out, "out", q.dtype, T, D)
-    _shape(out, q.shape, "out")
-    if lse is not None:
-        _shape(lse, (T, q_heads), "lse")
-        _contig(lse, "lse")
-    _contig(ws, "ws")
-    args = _kv_args("kronq_kv4_attention", cache, block_table, q_start, kv_len, D,
-                    ((q, "q"), (out, "out"), (lse, "lse"), (info, "info"), (ws, "ws")))
+    qr = _kv_rows(q, "q", dt, T, D)
+    orow = _kv_rows(out, "out", dt, T, D)
+    if out.shape[1] != q_heads:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
+    if lse is not None and tuple(lse.shape) != (T, q_heads):
+        raise ValueError(f"lse has shape {tuple(lse.shape)}, expected {(T, q_heads)}")
+    args = _kv_args("kronq_kv4_attention", cache, block_table, q_start, kv_len, D)
+    if ws is None or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor")
+    dev = _kv_device(q, out, cache, block_table, q_start, kv_len, ws)
     _check("kronq_kv4_attention", lib().kronq_kv4_attention(
-        *qr, KV_DTYPES[q.dtype], T, q_heads, *args, scale, int(bool(causal)), window, sinks, *orow,
-        _a(lse), _a(info), _a(ws), 0 if ws is None else ws.numel() * ws.element_size(), _s(stream)))
+        *qr, KV_DTYPES[dt], T, q_heads, *args, scale, 1 if causal else 0, window, sinks, *orow,
+        _kv_vector(lse, "lse", torch.float32, T * q_heads, dev), _kv_vector(info, "info", torch.int32, 1, dev),
+        ws.data_ptr(), ws.numel() * ws.element_size(), _kv_stream(stream, dev)))
 
 
 TIMERS = {"lazy_update": 0, "chol_update": 1, "chol_panel": 2, "obs_block": 3}

@@ -21,11 +21,13 @@
 // of probabilities are turned with movmatrix.
 //
 // One block = one (sequence, tile of 8 NT rows, split of its keys) of one
-// key/value head; warp w takes keys 16 w .. of every 64, straight from global
-// memory to registers (16 bytes per lane and token: a quad reads a token's
-// row), the next step's codes in flight while this one is multiplied.  The
-// running maximum is only moved when a score passes it by 2^8 (all lanes of a
-// column agree by vote), so most steps have no cross-lane reduction.
+// key/value head; warp w takes keys 16 w .. of every 64 through a ring of its
+// own in shared memory, filled by cp.async three steps ahead: no barrier
+// between warps, and some 100 KB in flight per SM.  (Bulk copies cannot place
+// the swizzle that keeps the value reads, four tokens apart, off each other's
+// banks.)  The running maximum is only moved when a score passes it by 2^8
+// (all lanes of a column agree by vote), so most steps have no cross-lane
+// reduction.
 #include "kv4_attend.cuh"
 
 namespace kv4 {
@@ -58,56 +60,91 @@ KQ_DEV uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+KQ_DEV void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+KQ_DEV void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
-KQ_DEV void load_words(uint32_t (&w)[N], const uint8_t* p) {
-  if constexpr (N == 1) {
-    asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(w[0]) : "l"(p));
-  } else if constexpr (N == 2) {
-    asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-      asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                   : "l"(p + 4 * i));
-  }
+KQ_DEV void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Codes and words of 16 tokens as the fragments want them.  Key rows of the
-// MMA: row r of block k (0: rows 0-7, 1: rows 8-15) is token
+template <int N>
+KQ_DEV void lds_words(uint32_t* w, uint32_t p) {
+  if constexpr (N == 1)
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(p));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(p));
+  else
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(p));
+}
+
+// A step's 16 tokens in shared memory: key codes, value codes (16 x D/2 bytes
+// each, in 128-byte lines whose 16-byte chunks are swizzled by the token),
+// key words, value words.
+//
+// Key rows of the MMA: row r of block k (0: rows 0-7, 1: rows 8-15) is token
 // 4 (r >> 1) + 2 k + (r & 1), the order in which the turned probabilities come
-// out as pairs of neighbouring tokens.
+// out as pairs of neighbouring tokens.  Lane (gr, t) reads D/4 dims of the two
+// tokens of row gr, and D/8 dims of the tokens 4t .. 4t + 3 of the values.
 template <int D>
-struct Step {
-  static constexpr int KW = D / 32;      // key words per lane and token
-  static constexpr int VW = D / 64;      // value words per lane and token
-  uint32_t k[2][KW];
-  uint32_t v[4][VW];
-  uint32_t kw[2], vw[2];
+struct Stage {
+  static constexpr int TOK = D / 2;                 // bytes of a token's codes
+  static constexpr int CODES = 16 * TOK;
+  static constexpr int BYTES = 2 * CODES + 128;
+  static constexpr int KW = D / 32;                 // key words per lane and token
+  static constexpr int VW = D / 64;                 // value words per lane and token
+  static constexpr int KLOADS = KW > 4 ? 2 : 1;
+
+  // byte offset of 16-byte chunk c of the keys (values): lines of 8 chunks
+  KQ_DEV static int key_at(int c) {
+    const int tok = c / (TOK / 16);
+    const int x = D == 256 ? 4 * (tok & 1) : D == 128 ? 0 : 4 * ((tok >> 2) & 1);
+    return (c ^ x) * 16;
+  }
+  KQ_DEV static int value_at(int c) {
+    const int tok = c / (TOK / 16);
+    return CODES + (c ^ (2 * ((tok >> 2) & 3))) * 16;
+  }
+  // where lane (gr, t) reads: keys of its first token (load i of KLOADS) and
+  // values of token 4 t + i.  Its second key token is 2 tokens on.
+  KQ_DEV static int key_lane(int gr, int t, int i) {
+    const int tok = 4 * (gr >> 1) + (gr & 1);
+    const int byte = KLOADS == 2 ? 16 * (t + 4 * i) : t * (D / 8);
+    const int at = tok * TOK + byte;
+    return key_at(at / 16) + at % 16;
+  }
+  KQ_DEV static int value_lane(int gr, int t, int i) {
+    const int at = (4 * t + i) * TOK + gr * (D / 16);
+    return value_at(at / 16) + at % 16;
+  }
+  // dims of word w of lane t's keys
+  KQ_DEV static int key_dim(int t, int w) {
+    return KLOADS == 2 ? 32 * (t + 4 * (w >> 2)) + 8 * (w & 3) : t * (D / 4) + 8 * w;
+  }
 };
 
+// the lane's second key token lies 2 tokens behind the first; within a line that
+// may cross the swizzle
 template <int D>
-KQ_DEV void load_step(Step<D>& s, const AttendArgs& a, const uint8_t* blk, int slot0, int gr, int t) {
-  const int P = a.cache.P;
-  const int tok = slot0 + 4 * (gr >> 1) + (gr & 1);
-  const uint8_t* kp = blk + tok * (D / 2) + t * (D / 8);
-  load_words(s.k[0], kp);
-  load_words(s.k[1], kp + 2 * (D / 2));
-  const uint8_t* vp = blk + P * (D / 2) + (slot0 + 4 * t) * (D / 2) + gr * (D / 16);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) load_words(s.v[i], vp + i * (D / 2));
-  const uint32_t* wp = reinterpret_cast<const uint32_t*>(blk + P * D) + tok;
-  s.kw[0] = __ldg(wp);
-  s.kw[1] = __ldg(wp + 2);
-  s.vw[0] = __ldg(wp + P);
-  s.vw[1] = __ldg(wp + P + 2);
+KQ_DEV int second_key(int off, int k) {
+  if (!k) return off;
+  if constexpr (D == 64) return off ^ 64;       // 2 tokens of 32 bytes: the line's other half
+  return off + 2 * (D / 2);
 }
+
+constexpr int RING = 4;
+constexpr int FLUSH = 8;      // steps between subtractions of the zero points' part
 
 template <int D, int NT>
 __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a) {
   constexpr int R = 8 * NT;
-  constexpr int KW = D / 32, VW = D / 64, MT = D / 16;
-  extern __shared__ float merge_o[];                 // [WARPS][R][D]
+  using SG = Stage<D>;
+  constexpr int KW = SG::KW, VW = SG::VW, MT = D / 16;
+  extern __shared__ __align__(128) uint8_t smem[];   // the warps' rings; then [WARPS][R][D] floats
+  float* merge_o = reinterpret_cast<float*>(smem);
   __shared__ float merge_ml[WARPS][R][2];
 
   Unit u;
@@ -129,6 +166,77 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
   const int per = ceil_div(sp.nb, u.nsplit);
   const int i0 = u.split * per, i1 = min(sp.nb, i0 + per);
 
+  // the keys each column's row sees: j < chi and (j >= clo or j < sinks)
+  int clo[NT][2], chi[NT][2];
+  int all_lo = 0, all_hi = INT32_MAX, any_lo = INT32_MAX, any_hi = 0;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = r0 + 8 * nt + 2 * t + c;
+      const int p = s.L - s.n + (r < rows ? r : rows - 1) / a.g;
+      chi[nt][c] = max(0, a.causal ? min(s.L, p + 1) : s.L);
+      clo[nt][c] = a.window ? max(0, p - a.window + 1) : 0;
+      all_lo = max(all_lo, clo[nt][c]);
+      all_hi = min(all_hi, chi[nt][c]);
+      any_lo = min(any_lo, clo[nt][c]);
+      any_hi = max(any_hi, chi[nt][c]);
+    }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
+    all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
+    any_lo = min(any_lo, __shfl_xor_sync(0xffffffffu, any_lo, o));
+    any_hi = max(any_hi, __shfl_xor_sync(0xffffffffu, any_hi, o));
+  }
+
+  // ---- keys: the warp's steps are its 16 tokens of every block i0 .. i1 - 1;
+  // page ids for 32 steps at a time, one per lane
+  const int steps = i1 > i0 ? i1 - i0 : 0;
+  const uint32_t ring = kq::smem_u32(smem) + warp * (RING * SG::BYTES);
+  int page_lane = -1;
+  uint32_t present = 0;                  // bit k: the ring's stage k holds tokens
+  auto tok_of = [&](int i) { return (i < sp.sb ? i : sp.lb + i - sp.sb) * BLK + 16 * warp; };
+  auto fetch = [&](int st) {
+    if (st < steps) {
+      if ((st & 31) == 0) {
+        page_lane = -1;
+        if (st + lane < steps) {
+          const int j = tok_of(i0 + st + lane);
+          if (j < any_hi) {
+            page_lane = a.b.table[u.b * a.b.table_ld + (j >> a.cache.lgP)];
+            if (page_lane < 0 || page_lane >= a.cache.pages) {
+              if (j + 16 > any_lo || j < a.sinks) kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
+              page_lane = -1;
+            }
+          }
+        }
+      }
+      const int pg = __shfl_sync(0xffffffffu, page_lane, st & 31);
+      const int k = st % RING;
+      present &= ~(1u << k);
+      if (pg >= 0) {
+        present |= 1u << k;
+        const int slot0 = tok_of(i0 + st) & (a.cache.P - 1);
+        const uint8_t* blk = a.cache.base + ((int64_t)pg * a.cache.heads + head) * a.cache.block_bytes;
+        const uint8_t* kp = blk + slot0 * SG::TOK + lane * 16;
+        const uint8_t* vp = kp + a.cache.P * SG::TOK;
+        const uint32_t dst = ring + k * SG::BYTES;
+#pragma unroll
+        for (int c = 0; c < SG::CODES / 16; c += 32) {
+          copy16(dst + SG::key_at(c + lane), kp + c * 16);
+          copy16(dst + SG::value_at(c + lane), vp + c * 16);
+        }
+        if (lane < 8)
+          copy16(dst + 2 * SG::CODES + lane * 16,
+                 blk + a.cache.P * D + ((lane & 4) ? a.cache.P * 4 : 0) + slot0 * 4 + (lane & 3) * 16);
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < RING - 1; ++k) fetch(k);
+
   // ---- queries: fp16 fragments of q 2^e (e per row: the largest becomes about
   // 2^10, so bf16's range is kept and so are 20 binades below the row's largest)
   uint32_t qf[NT][KW][4];
@@ -141,15 +249,13 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
     if (r < rows) {
       const int qi = r / a.g;
       const uint16_t* p = a.q + (int64_t)(s.row0 + qi) * a.q_st +
-                          (int64_t)(head * a.g + r - qi * a.g) * a.q_sh + t * (D / 4);
+                          (int64_t)(head * a.g + r - qi * a.g) * a.q_sh;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) load8(p + SG::key_dim(t, w), a.q_vec, a.dt, x[w]);
 #pragma unroll
       for (int w = 0; w < KW; ++w)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint16_t h = __ldg(p + 8 * w + j);
-          x[w][j] = a.dt == BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
-          big = fmaxf(big, fabsf(x[w][j]));
-        }
+        for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(x[w][j]));
     } else {
 #pragma unroll
       for (int w = 0; w < KW; ++w)
@@ -183,30 +289,6 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
       qmul[nt][c] = __shfl_sync(0xffffffffu, mul, (2 * t + c) * 4);
     }
   }
-  // the keys each column's row sees: j < chi and (j >= clo or j < sinks)
-  int clo[NT][2], chi[NT][2];
-  int all_lo = 0, all_hi = INT32_MAX, any_lo = INT32_MAX, any_hi = 0;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int r = r0 + 8 * nt + 2 * t + c;
-      const int p = s.L - s.n + (r < rows ? r : rows - 1) / a.g;
-      chi[nt][c] = max(0, a.causal ? min(s.L, p + 1) : s.L);
-      clo[nt][c] = a.window ? max(0, p - a.window + 1) : 0;
-      all_lo = max(all_lo, clo[nt][c]);
-      all_hi = min(all_hi, chi[nt][c]);
-      any_lo = min(any_lo, clo[nt][c]);
-      any_hi = max(any_hi, chi[nt][c]);
-    }
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
-    all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
-    any_lo = min(any_lo, __shfl_xor_sync(0xffffffffu, any_lo, o));
-    any_hi = max(any_hi, __shfl_xor_sync(0xffffffffu, any_hi, o));
-  }
-
   float o[NT][MT][4];
   float m[NT][2], me[NT][2], l[NT][2], zs[NT][2];
 #pragma unroll
@@ -226,43 +308,31 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
   // largest so far lies below 2^6 (times 2^8 of a lagging maximum, below 2^14)
   float fv = 0.f;
 
-  // ---- keys: the warp's steps are its 16 tokens of every block i0 .. i1 - 1;
-  // page ids for 32 steps at a time, one per lane
-  const int steps = i1 > i0 ? i1 - i0 : 0;
-  int page_lane = -1;
-  auto tok_of = [&](int i) { return (i < sp.sb ? i : sp.lb + i - sp.sb) * BLK + 16 * warp; };
-  auto fetch_pages = [&](int st) {
-    const int i = i0 + st + lane;
-    page_lane = -1;
-    if (st + lane < steps) {
-      const int j = tok_of(i);
-      if (j < any_hi) {
-        page_lane = a.b.table[u.b * a.b.table_ld + (j >> a.cache.lgP)];
-        if (page_lane < 0 || page_lane >= a.cache.pages) {
-          const bool seen = j + 16 > any_lo || j < a.sinks;
-          if (seen) kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
-          page_lane = -1;
-        }
-      }
-    }
-  };
-  // the step's codes, zeros where it has no page
-  auto fetch = [&](Step<D>& d, int st) -> bool {
-    if ((st & 31) == 0) fetch_pages(st);
-    const int pg = __shfl_sync(0xffffffffu, page_lane, st & 31);
-    if (pg < 0) return false;
-    const uint8_t* blk = a.cache.base + ((int64_t)pg * a.cache.heads + head) * a.cache.block_bytes;
-    load_step<D>(d, a, blk, tok_of(i0 + st) & (a.cache.P - 1), gr, t);
-    return true;
-  };
-
-  Step<D> cur, nxt;
-  bool have = steps > 0 && fetch(nxt, 0);
+  int koff[SG::KLOADS], voff[4];
+#pragma unroll
+  for (int i = 0; i < SG::KLOADS; ++i) koff[i] = SG::key_lane(gr, t, i);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) voff[i] = SG::value_lane(gr, t, i);
+  const int woff = 2 * SG::CODES + 4 * (4 * (gr >> 1) + (gr & 1));
+  int unflushed = 0;
   for (int st = 0; st < steps; ++st) {
-    cur = nxt;
-    const bool valid = have;
-    have = st + 1 < steps && fetch(nxt, st + 1);
+    copy_wait<RING - 2>();
+    __syncwarp();
+    const bool valid = (present >> (st % RING)) & 1;
+    fetch(st + RING - 1);                // into the stage that the last step has left
     if (!valid) continue;
+    const uint32_t stage = ring + (st % RING) * SG::BYTES;
+    uint32_t kc[2][KW], vc[4][VW], kw[2], vw[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int i = 0; i < SG::KLOADS; ++i)
+        lds_words<KW / SG::KLOADS>(kc[k] + 4 * i, stage + second_key<D>(koff[i], k));
+      lds_words<1>(&kw[k], stage + woff + 8 * k);
+      lds_words<1>(&vw[k], stage + woff + 64 + 8 * k);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lds_words<VW>(vc[i], stage + voff[i]);
     const int j0 = tok_of(i0 + st);
     const int ja = j0 + 4 * (gr >> 1) + (gr & 1);        // this lane's two tokens: ja, ja + 2
     const bool masked = !(j0 + 16 <= all_hi && (j0 >= all_lo || j0 + 16 <= a.sinks));
@@ -271,16 +341,16 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int j = ja + 2 * k;
-        if (!(j < any_hi && (j >= any_lo || j < a.sinks))) cur.kw[k] = cur.vw[k] = 0;
+        if (!(j < any_hi && (j >= any_lo || j < a.sinks))) kw[k] = vw[k] = 0;
       }
     }
     float sk[2], zk[2], sv[2], zv[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      sk[k] = word_scale(cur.kw[k]);
-      zk[k] = word_zero(cur.kw[k]);
-      sv[k] = word_scale(cur.vw[k]);
-      zv[k] = word_zero(cur.vw[k]);
+      sk[k] = word_scale(kw[k]);
+      zk[k] = word_zero(kw[k]);
+      sv[k] = word_scale(vw[k]);
+      zv[k] = word_zero(vw[k]);
     }
     float x[NT][4];
 #pragma unroll
@@ -291,7 +361,7 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
         for (int c = 0; c < 2; ++c) x[nt][2 * k + c] = -zk[k] * qsum[nt][c];
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
-        const uint32_t ua = cur.k[0][w], ub = cur.k[1][w];
+        const uint32_t ua = kc[0][w], ub = kc[1][w];
         mma16816(x[nt], ua & 0x000f000fu, ub & 0x000f000fu, ua & 0x00f000f0u, ub & 0x00f000f0u,
                  qf[nt][w][0], qf[nt][w][1]);
         const uint32_t va = ua >> 8, vb = ub >> 8;
@@ -373,10 +443,10 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
       }
 #pragma unroll
     for (int w = 0; w < VW; ++w) {
-      uint32_t lo01 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x5410);
-      uint32_t hi01 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x7632);
-      uint32_t lo23 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x5410);
-      uint32_t hi23 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x7632);
+      uint32_t lo01 = __byte_perm(vc[0][w], vc[1][w], 0x5410);
+      uint32_t hi01 = __byte_perm(vc[0][w], vc[1][w], 0x7632);
+      uint32_t lo23 = __byte_perm(vc[2][w], vc[3][w], 0x5410);
+      uint32_t hi23 = __byte_perm(vc[2][w], vc[3][w], 0x7632);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint32_t p01 = q == 0 ? lo01 : q == 1 ? lo01 >> 8 : q == 2 ? hi01 : hi01 >> 8;
@@ -387,7 +457,29 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
         for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][4 * w + q], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
       }
     }
+    // the sums of codes and of zero points nearly cancel (values are centred), and
+    // the tensor core rounds its sum towards zero: keep the difference small
+    if (++unflushed == FLUSH) {
+      unflushed = 0;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float z = zs[nt][c];
+          zs[nt][c] = 0.f;
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+          const float ze = z * 0x1p-24f, zo = z * 0x1p-20f;
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            o[nt][i][c] -= ze;
+            o[nt][i][2 + c] -= zo;
+          }
+        }
+    }
   }
+  copy_wait<0>();
+  __syncthreads();                       // the rings become the joining buffer
 
   // ---- join the warps
 #pragma unroll
@@ -456,10 +548,11 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
 }
 
 // Joins the splits of the rows that have some: a block per token and `hpb` query
-// heads, its warps one row each at a time.
+// heads, one row at a time; warp w takes the splits w, w + 4, ..
 template <int D>
 __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, int R, int hpb) {
   constexpr int E = D / 32;
+  __shared__ float sum_o[WARPS][D], sum_l[WARPS];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = blockIdx.x;
@@ -470,7 +563,7 @@ __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, 
   const int2 mt = a.meta[b];
   const int ns = mt.y;
   if (ns <= 1) return;
-  for (int h = warp; h < hpb; h += WARPS) {
+  for (int h = 0; h < hpb; ++h) {
     const int hq = blockIdx.y * hpb + h;
     if (hq >= a.Hq) return;
     const int head = hq / a.g, r = (i - s.row0) * a.g + hq - head * a.g;
@@ -485,55 +578,57 @@ __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, 
     float l = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int k0 = 0; k0 < ns; k0 += 32) {
-      float w = 0.f;
-      if (k0 + lane < ns) {
-        const Part p = a.part_ml[s0 + (k0 + lane) * stride];
-        // a split without a key (m = -inf, l = 0) counts nothing; a NaN stays
-        w = p.m == -INFINITY ? (p.l == 0.f ? 0.f : NAN) : exp2_approx(p.m - m);
-        l += w == 0.f ? 0.f : p.l * w;
-      }
-      const int kn = min(32, ns - k0);
 #pragma unroll 4
-      for (int k = 0; k < kn; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const float* p = a.part_o + (s0 + (k0 + k) * stride) * D + lane * E;
-        float v[E];
-        if constexpr (E == 2) {
-          const float2 x = *reinterpret_cast<const float2*>(p);
-          v[0] = x.x;
-          v[1] = x.y;
-        } else {
+    for (int k = warp; k < ns; k += WARPS) {
+      const Part q = a.part_ml[s0 + k * stride];
+      const float* p = a.part_o + (s0 + k * stride) * D + lane * E;
+      float v[E];
+      if constexpr (E == 2) {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        v[0] = x.x;
+        v[1] = x.y;
+      } else {
 #pragma unroll
-          for (int e = 0; e < E; e += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(p + e);
-            v[e] = x.x;
-            v[e + 1] = x.y;
-            v[e + 2] = x.z;
-            v[e + 3] = x.w;
-          }
+        for (int e = 0; e < E; e += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(p + e);
+          v[e] = x.x;
+          v[e + 1] = x.y;
+          v[e + 2] = x.z;
+          v[e + 3] = x.w;
         }
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(wk, v[e], o[e]);
       }
+      // a split without a key (m = -inf, l = 0) counts nothing; a NaN stays
+      const float w = q.m == -INFINITY ? (q.l == 0.f ? 0.f : NAN) : exp2_approx(q.m - m);
+      l += q.l * w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[e], o[e]);
     }
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if constexpr (E == 2) {
-      const float x = __shfl_down_sync(0xffffffffu, o[0], 1), y = __shfl_down_sync(0xffffffffu, o[1], 1);
-      if (!(lane & 1)) store_row(a, i, hq, 2 * lane, make_float4(o[0], o[1], x, y), m, l);
-    } else {
+    for (int e = 0; e < E; ++e) sum_o[warp][lane * E + e] = o[e];
+    if (lane == 0) sum_l[warp] = l;
+    __syncthreads();
+    if (threadIdx.x < D / 4) {
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+      float ls = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; e += 4)
-        store_row(a, i, hq, lane * E + e, make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]), m, l);
+      for (int w = 0; w < WARPS; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(&sum_o[w][4 * threadIdx.x]);
+        t.x += x.x;
+        t.y += x.y;
+        t.z += x.z;
+        t.w += x.w;
+        ls += sum_l[w];
+      }
+      store_row(a, i, hq, 4 * threadIdx.x, t, m, ls);
     }
+    __syncthreads();
   }
 }
 
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 constexpr unsigned long long TARGET = 148ull * 12;   // units over all heads
-constexpr int MIN_CHUNK = 2;                         // 128 keys
+constexpr int MIN_CHUNK = 4;                         // 256 keys
 
 struct Layout {
   size_t meta, ml, o, total;
@@ -555,12 +650,16 @@ int launch(AttendArgs& a, cudaStream_t st) {
   const long long ux = max_units(a.T, a.g, a.b.B, R, a.cache.heads, a.target);
   if (ux > INT32_MAX) return KRONQ_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)ux, (unsigned)a.cache.heads);
-  kv4_attend_kernel<D, NT><<<grid, THREADS, (size_t)WARPS * R * D * sizeof(float), st>>>(a);
+  constexpr int rings = WARPS * RING * Stage<D>::BYTES, join = WARPS * R * D * (int)sizeof(float);
+  constexpr int smem = rings > join ? rings : join;
+  static kqh::PerDevice attr;
+  if (kqh::smem_attr_once(attr, kv4_attend_kernel<D, NT>, smem) <= 0) return KRONQ_ERR_CUDA;
+  kv4_attend_kernel<D, NT><<<grid, THREADS, smem, st>>>(a);
   KQ_CHECK_LAUNCH();
   // no sequence can be split when the longest one the table holds is one chunk
   const long long most = (((long long)a.b.max_pages << a.cache.lgP) + BLK - 1) / BLK;
   if (most <= a.min_chunk) return KRONQ_OK;
-  const int hpb = (long long)a.T * a.Hq <= 16384 ? WARPS : a.Hq;
+  const int hpb = (long long)a.T * a.Hq <= 16384 ? 1 : a.Hq;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.T, (unsigned)((a.Hq + hpb - 1) / hpb));
   cfg.blockDim = dim3(THREADS);
@@ -605,6 +704,7 @@ int kq_kv4_attention(const void* q, int64_t q_st, int64_t q_sh, int dtype, int64
   a.q = static_cast<const uint16_t*>(q);
   a.q_st = q_st;
   a.q_sh = q_sh;
+  a.q_vec = kqh::aligned(q, 16) && q_st % 8 == 0 && q_sh % 8 == 0;
   a.out = out;
   a.o_st = o_st;
   a.o_sh = o_sh;

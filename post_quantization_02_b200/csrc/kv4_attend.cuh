@@ -25,6 +25,7 @@ struct Part {            // one (row, split): unnormalised sum relative to 2^m
 struct AttendArgs {
   const uint16_t* q;
   int64_t q_st, q_sh;
+  int q_vec;             // 16-byte loads fit
   void* out;
   int64_t o_st, o_sh;
   float* lse;            // T x Hq, or null

@@ -29,51 +29,6 @@ using namespace kv4;
 constexpr int TPB = 128;
 constexpr int ITEMS = TPB / 8;      // vectors per block
 
-KQ_DEV float to_f32(uint16_t h, int dt) {
-  return dt == BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
-}
-
-KQ_DEV void unpack8(const uint4& u, int dt, float (&x)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (dt == BF16) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
-  }
-}
-
-KQ_DEV uint4 pack8(const float (&x)[8], int dt) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (dt == BF16) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&b);
-    } else {
-      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// 8 consecutive elements at p: one 16-byte load, or element loads where the
-// tensor's address or strides are not multiples of 16 bytes.
-KQ_DEV void load8(const uint16_t* p, bool vec, int dt, float (&x)[8]) {
-  if (vec) {
-    unpack8(__ldg(reinterpret_cast<const uint4*>(p)), dt, x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_f32(__ldg(p + i), dt);
-  }
-}
-
 struct Rows {
   const uint16_t* p;
   int64_t st, sh;     // strides of the token and of the head (elements)

@@ -19,7 +19,7 @@ given are allocated on the current stream.
 
 from __future__ import annotations
 
-import contextlib
+import functools
 
 import torch
 
@@ -42,19 +42,18 @@ def rope_table(rows: int, rot: int, base: float = 10000.0, device=None) -> torch
     return torch.cat([ang.cos(), ang.sin()], 1).float()
 
 
-def _on(stream):
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
-
-
 def append(q, k, v, cache, block_table, q_start, kv_len, rope=None, interleaved: bool = False,
            positions=None, signs=None, q_out=None, info=None, stream=None):
     """Puts the batch's new keys and values into the cache; returns the rotated
     queries (None when q is None)."""
-    with _on(stream):
-        if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        abi.kronq_kv4_append(q, k, v, cache, block_table, q_start, kv_len, q_out, rope, interleaved,
-                             positions, signs, info, stream)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return append(q, k, v, cache, block_table, q_start, kv_len, rope, interleaved, positions, signs,
+                          q_out, info)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    abi.kronq_kv4_append(q, k, v, cache, block_table, q_start, kv_len, q_out, rope, interleaved, positions,
+                         signs, info)
     return q_out
 
 
@@ -62,12 +61,15 @@ def gather(cache, block_table, q_start, kv_len, tokens: int, head_dim: int, dtyp
            info=None, stream=None):
     """(keys, values) of the batch's new tokens as the cache holds them, tokens x
     heads x head_dim; rows that are no sequence's are left unset."""
-    with _on(stream):
-        shape = (tokens, cache.shape[1], head_dim)
-        k = torch.empty(shape, dtype=dtype, device=cache.device)
-        v = torch.empty(shape, dtype=dtype, device=cache.device)
-        abi.kronq_kv4_gather(cache, block_table, q_start, kv_len, k, v, info, stream)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gather(cache, block_table, q_start, kv_len, tokens, head_dim, dtype, info)
+    k, v = torch.empty((2, tokens, cache.shape[1], head_dim), dtype=dtype, device=cache.device)
+    abi.kronq_kv4_gather(cache, block_table, q_start, kv_len, k, v, info)
     return k, v
+
+
+_workspace_size = functools.lru_cache(maxsize=1024)(abi.kronq_kv4_attention_workspace_size)
 
 
 def attend(q, cache, block_table, q_start, kv_len, scale: float | None = None, causal: bool = True,
@@ -75,13 +77,15 @@ def attend(q, cache, block_table, q_start, kv_len, scale: float | None = None, c
     """Attention of q (tokens x q_heads x head_dim) over the cache; scale defaults
     to head_dim^-1/2.  Rows that are no sequence's are left as they were (unset in a
     fresh output)."""
-    with _on(stream):
-        T, Hq, D = q.shape
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if ws is None:
-            ws = abi.kv4_workspace(T, Hq, cache.shape[1], D, kv_len.shape[0], q.device)
-        abi.kronq_kv4_attention(q, cache, block_table, q_start, kv_len, out, ws,
-                                D ** -0.5 if scale is None else scale, causal, window, sinks, lse, info,
-                                stream)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return attend(q, cache, block_table, q_start, kv_len, scale, causal, window, sinks, out, lse, ws, info)
+    T, Hq, D = q.shape
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if ws is None:
+        nbytes = _workspace_size(T, Hq, cache.shape[1], D, kv_len.shape[0])
+        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+    abi.kronq_kv4_attention(q, cache, block_table, q_start, kv_len, out, ws, D ** -0.5 if scale is None else scale,
+                            causal, window, sinks, lse, info)
     return out
