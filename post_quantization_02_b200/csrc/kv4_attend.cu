@@ -21,8 +21,8 @@
 // of probabilities are turned with movmatrix.
 //
 // One block = one (sequence, tile of 8 NT rows, split of its keys) of one
-// key/value head; warp w takes keys 16 w .. of every 64 through a ring of its
-// own in shared memory, filled by cp.async three steps ahead: no barrier
+// key/value head; warp w takes keys 32 w .. of every 128 through a ring of its
+// own in shared memory, filled by cp.async two steps ahead: no barrier
 // between warps, and some 100 KB in flight per SM.  (Bulk copies cannot place
 // the swizzle that keeps the value reads, four tokens apart, off each other's
 // banks.)  The running maximum is only moved when a score passes it by 2^8
@@ -33,7 +33,7 @@
 namespace kv4 {
 namespace {
 
-constexpr int THREADS = 128, WARPS = 4, BLK = 64;
+constexpr int THREADS = 128, WARPS = 4, BLK = 128, STEP = BLK / WARPS;
 
 KQ_DEV void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                      uint32_t b1) {
@@ -81,16 +81,16 @@ KQ_DEV void lds_words(uint32_t* w, uint32_t p) {
                  : "r"(p));
 }
 
-// A step's 16 tokens in shared memory: key codes, value codes (16 x D/2 bytes
-// each, in 128-byte lines whose 16-byte chunks are swizzled by the token),
-// key words, value words.
+// 16 tokens in shared memory (a step has two such halves): key codes, value
+// codes (16 x D/2 bytes each, in 128-byte lines whose 16-byte chunks are
+// swizzled by the token), key words, value words.
 //
 // Key rows of the MMA: row r of block k (0: rows 0-7, 1: rows 8-15) is token
 // 4 (r >> 1) + 2 k + (r & 1), the order in which the turned probabilities come
 // out as pairs of neighbouring tokens.  Lane (gr, t) reads D/4 dims of the two
 // tokens of row gr, and D/8 dims of the tokens 4t .. 4t + 3 of the values.
 template <int D>
-struct Stage {
+struct Half {
   static constexpr int TOK = D / 2;                 // bytes of a token's codes
   static constexpr int CODES = 16 * TOK;
   static constexpr int BYTES = 2 * CODES + 128;
@@ -116,6 +116,10 @@ struct Stage {
     const int at = tok * TOK + byte;
     return key_at(at / 16) + at % 16;
   }
+  KQ_DEV static int second_key(int off) {
+    if constexpr (D == 64) return off ^ 64;         // 2 tokens of 32 bytes: the line's other half
+    return off + 2 * TOK;
+  }
   KQ_DEV static int value_lane(int gr, int t, int i) {
     const int at = (4 * t + i) * TOK + gr * (D / 16);
     return value_at(at / 16) + at % 16;
@@ -126,23 +130,19 @@ struct Stage {
   }
 };
 
-// the lane's second key token lies 2 tokens behind the first; within a line that
-// may cross the swizzle
-template <int D>
-KQ_DEV int second_key(int off, int k) {
-  if (!k) return off;
-  if constexpr (D == 64) return off ^ 64;       // 2 tokens of 32 bytes: the line's other half
-  return off + 2 * (D / 2);
-}
+// chunk c (4 floats) of row r of the joining buffer is stored at c ^ this: a
+// store's 8 lanes of a phase have 2 values of gr (chunks D/32 apart) and 4 of
+// t (rows 2 apart, all on the same banks otherwise)
+KQ_DEV int join_swizzle(int c, int r) { return (r >> 1) & 3; }
 
-constexpr int RING = 4;
-constexpr int FLUSH = 8;      // steps between subtractions of the zero points' part
+constexpr int RING = 3;
+constexpr int FLUSH = 4;      // steps between subtractions of the zero points' part
 
 template <int D, int NT>
-__global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_attend_kernel(const AttendArgs a) {
   constexpr int R = 8 * NT;
-  using SG = Stage<D>;
-  constexpr int KW = SG::KW, VW = SG::VW, MT = D / 16;
+  using HF = Half<D>;
+  constexpr int KW = HF::KW, VW = HF::VW, MT = D / 16;
   extern __shared__ __align__(128) uint8_t smem[];   // the warps' rings; then [WARPS][R][D] floats
   float* merge_o = reinterpret_cast<float*>(smem);
   __shared__ float merge_ml[WARPS][R][2];
@@ -161,81 +161,79 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gr = lane >> 2, t = lane & 3;
   const int rows = s.n * a.g, r0 = u.tile * R;
-  const int q0 = r0 / a.g, q1 = (min(rows, r0 + R) - 1) / a.g;
+  const int last = min(rows, r0 + R) - 1;
+  int qi[NT];                                       // query of this lane's row (rows behind: the last)
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) qi[nt] = min(last, r0 + 8 * nt + gr) / a.g;
+  const int q0 = __shfl_sync(0xffffffffu, qi[0], 0), q1 = __shfl_sync(0xffffffffu, qi[NT - 1], 28);
   const Span sp = span_of<BLK>(a, s, q0, q1);
   const int per = ceil_div(sp.nb, u.nsplit);
   const int i0 = u.split * per, i1 = min(sp.nb, i0 + per);
 
-  // the keys each column's row sees: j < chi and (j >= clo or j < sinks)
+  // the keys each column's row sees: j < chi and (j >= clo or j < sinks); what all
+  // of the tile's rows see, and what one of them sees (rows are in order)
   int clo[NT][2], chi[NT][2];
-  int all_lo = 0, all_hi = INT32_MAX, any_lo = INT32_MAX, any_hi = 0;
+  auto lo_of = [&](int q) { return a.window ? max(0, s.L - s.n + q - a.window + 1) : 0; };
+  auto hi_of = [&](int q) { return max(0, a.causal ? min(s.L, s.L - s.n + q + 1) : s.L); };
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int r = r0 + 8 * nt + 2 * t + c;
-      const int p = s.L - s.n + (r < rows ? r : rows - 1) / a.g;
-      chi[nt][c] = max(0, a.causal ? min(s.L, p + 1) : s.L);
-      clo[nt][c] = a.window ? max(0, p - a.window + 1) : 0;
-      all_lo = max(all_lo, clo[nt][c]);
-      all_hi = min(all_hi, chi[nt][c]);
-      any_lo = min(any_lo, clo[nt][c]);
-      any_hi = max(any_hi, chi[nt][c]);
+      const int q = __shfl_sync(0xffffffffu, qi[nt], (2 * t + c) * 4);
+      chi[nt][c] = hi_of(q);
+      clo[nt][c] = lo_of(q);
     }
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
-    all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
-    any_lo = min(any_lo, __shfl_xor_sync(0xffffffffu, any_lo, o));
-    any_hi = max(any_hi, __shfl_xor_sync(0xffffffffu, any_hi, o));
-  }
+  const int all_lo = lo_of(q1), all_hi = hi_of(q0), any_lo = lo_of(q0), any_hi = hi_of(q1);
 
-  // ---- keys: the warp's steps are its 16 tokens of every block i0 .. i1 - 1;
-  // page ids for 32 steps at a time, one per lane
+  // ---- keys: the warp's steps are its 32 tokens of every block i0 .. i1 - 1;
+  // page numbers of the next 32 halves, one per lane
   const int steps = i1 > i0 ? i1 - i0 : 0;
-  const uint32_t ring = kq::smem_u32(smem) + warp * (RING * SG::BYTES);
+  const uint32_t ring = kq::smem_u32(smem) + warp * (RING * 2 * HF::BYTES);
   int page_lane = -1;
-  uint32_t present = 0;                  // bit k: the ring's stage k holds tokens
-  auto tok_of = [&](int i) { return (i < sp.sb ? i : sp.lb + i - sp.sb) * BLK + 16 * warp; };
-  auto fetch = [&](int st) {
+  uint32_t present = 0;                  // bits 2k, 2k + 1: the halves of stage k hold tokens
+  auto tok_of = [&](int i) { return (i < sp.sb ? i : sp.lb + i - sp.sb) * BLK + STEP * warp; };
+  auto fetch = [&](int st, int k) {      // step st into stage k
     if (st < steps) {
-      if ((st & 31) == 0) {
+      if ((st & 15) == 0) {
         page_lane = -1;
-        if (st + lane < steps) {
-          const int j = tok_of(i0 + st + lane);
-          if (j < any_hi) {
+        const int s1 = st + (lane >> 1);
+        if (s1 < steps) {
+          const int j = tok_of(i0 + s1) + 16 * (lane & 1);
+          if (j < any_hi && (j + 16 > any_lo || j < a.sinks)) {
             page_lane = a.b.table[u.b * a.b.table_ld + (j >> a.cache.lgP)];
             if (page_lane < 0 || page_lane >= a.cache.pages) {
-              if (j + 16 > any_lo || j < a.sinks) kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
+              kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
               page_lane = -1;
             }
           }
         }
       }
-      const int pg = __shfl_sync(0xffffffffu, page_lane, st & 31);
-      const int k = st % RING;
-      present &= ~(1u << k);
-      if (pg >= 0) {
-        present |= 1u << k;
-        const int slot0 = tok_of(i0 + st) & (a.cache.P - 1);
-        const uint8_t* blk = a.cache.base + ((int64_t)pg * a.cache.heads + head) * a.cache.block_bytes;
-        const uint8_t* kp = blk + slot0 * SG::TOK + lane * 16;
-        const uint8_t* vp = kp + a.cache.P * SG::TOK;
-        const uint32_t dst = ring + k * SG::BYTES;
+      const int slot0 = tok_of(i0 + st) & (a.cache.P - 1);
+      present &= ~(3u << (2 * k));
 #pragma unroll
-        for (int c = 0; c < SG::CODES / 16; c += 32) {
-          copy16(dst + SG::key_at(c + lane), kp + c * 16);
-          copy16(dst + SG::value_at(c + lane), vp + c * 16);
+      for (int h = 0; h < 2; ++h) {
+        const int pg = __shfl_sync(0xffffffffu, page_lane, 2 * (st & 15) + h);
+        if (pg < 0) continue;
+        present |= 1u << (2 * k + h);
+        const int slot = (slot0 + 16 * h) & (a.cache.P - 1);
+        const uint8_t* blk = a.cache.base + ((int64_t)pg * a.cache.heads + head) * a.cache.block_bytes;
+        const uint8_t* kp = blk + slot * HF::TOK + lane * 16;
+        const uint8_t* vp = kp + a.cache.P * HF::TOK;
+        const uint32_t dst = ring + (2 * k + h) * HF::BYTES;
+#pragma unroll
+        for (int c = 0; c < HF::CODES / 16; c += 32) {
+          copy16(dst + HF::key_at(c + lane), kp + c * 16);
+          copy16(dst + HF::value_at(c + lane), vp + c * 16);
         }
         if (lane < 8)
-          copy16(dst + 2 * SG::CODES + lane * 16,
-                 blk + a.cache.P * D + ((lane & 4) ? a.cache.P * 4 : 0) + slot0 * 4 + (lane & 3) * 16);
+          copy16(dst + 2 * HF::CODES + lane * 16,
+                 blk + a.cache.P * D + ((lane & 4) ? a.cache.P * 4 : 0) + slot * 4 + (lane & 3) * 16);
       }
     }
     copy_commit();
   };
 #pragma unroll
-  for (int k = 0; k < RING - 1; ++k) fetch(k);
+  for (int k = 0; k < RING - 1; ++k) fetch(k, k);
 
   // ---- queries: fp16 fragments of q 2^e (e per row: the largest becomes about
   // 2^10, so bf16's range is kept and so are 20 binades below the row's largest)
@@ -247,11 +245,10 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
     float x[KW][8];
     float big = 0.f, sum = 0.f;
     if (r < rows) {
-      const int qi = r / a.g;
-      const uint16_t* p = a.q + (int64_t)(s.row0 + qi) * a.q_st +
-                          (int64_t)(head * a.g + r - qi * a.g) * a.q_sh;
+      const uint16_t* p = a.q + (int64_t)(s.row0 + qi[nt]) * a.q_st +
+                          (int64_t)(head * a.g + r - qi[nt] * a.g) * a.q_sh;
 #pragma unroll
-      for (int w = 0; w < KW; ++w) load8(p + SG::key_dim(t, w), a.q_vec, a.dt, x[w]);
+      for (int w = 0; w < KW; ++w) load8(p + HF::key_dim(t, w), a.q_vec, a.dt, x[w]);
 #pragma unroll
       for (int w = 0; w < KW; ++w)
 #pragma unroll
@@ -281,7 +278,7 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
     }
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    sum *= 0x1p-24f;
+    sum *= -0x1p-24f;
     const float mul = a.scale_log2 * down * 0x1p24f;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -289,8 +286,11 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
       qmul[nt][c] = __shfl_sync(0xffffffffu, mul, (2 * t + c) * 4);
     }
   }
-  float o[NT][MT][4];
-  float m[NT][2], me[NT][2], l[NT][2], zs[NT][2];
+
+  // o: even tiles' sums of p s' c over dims e, odd halves' sums of p s' (c_e + 16 c_(e+1))
+  // (a byte of codes taken whole saves a mask); z: sums of p s' z'
+  float o[NT][MT][4], z[NT][4];
+  float m[NT][2], me[NT][2], l[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -298,111 +298,138 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
 #pragma unroll
+    for (int j = 0; j < 4; ++j) z[nt][j] = 0.f;
+#pragma unroll
     for (int c = 0; c < 2; ++c) {
       m[nt][c] = -INFINITY;     // the running maximum
       me[nt][c] = 0.f;          // the same, 0 while there is none
-      l[nt][c] = zs[nt][c] = 0.f;
+      l[nt][c] = 0.f;
     }
   }
-  // values' scales are taken relative to 2^-ve so that p s' fits fp16: the
-  // largest so far lies below 2^6 (times 2^8 of a lagging maximum, below 2^14)
-  float fv = 0.f;
-
-  int koff[SG::KLOADS], voff[4];
-#pragma unroll
-  for (int i = 0; i < SG::KLOADS; ++i) koff[i] = SG::key_lane(gr, t, i);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) voff[i] = SG::value_lane(gr, t, i);
-  const int woff = 2 * SG::CODES + 4 * (4 * (gr >> 1) + (gr & 1));
-  int unflushed = 0;
-  for (int st = 0; st < steps; ++st) {
-    copy_wait<RING - 2>();
-    __syncwarp();
-    const bool valid = (present >> (st % RING)) & 1;
-    fetch(st + RING - 1);                // into the stage that the last step has left
-    if (!valid) continue;
-    const uint32_t stage = ring + (st % RING) * SG::BYTES;
-    uint32_t kc[2][KW], vc[4][VW], kw[2], vw[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-      for (int i = 0; i < SG::KLOADS; ++i)
-        lds_words<KW / SG::KLOADS>(kc[k] + 4 * i, stage + second_key<D>(koff[i], k));
-      lds_words<1>(&kw[k], stage + woff + 8 * k);
-      lds_words<1>(&vw[k], stage + woff + 64 + 8 * k);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) lds_words<VW>(vc[i], stage + voff[i]);
-    const int j0 = tok_of(i0 + st);
-    const int ja = j0 + 4 * (gr >> 1) + (gr & 1);        // this lane's two tokens: ja, ja + 2
-    const bool masked = !(j0 + 16 <= all_hi && (j0 >= all_lo || j0 + 16 <= a.sinks));
-    if (masked) {
-      // what no row sees may be memory that was never written
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int j = ja + 2 * k;
-        if (!(j < any_hi && (j >= any_lo || j < a.sinks))) kw[k] = vw[k] = 0;
-      }
-    }
-    float sk[2], zk[2], sv[2], zv[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      sk[k] = word_scale(kw[k]);
-      zk[k] = word_zero(kw[k]);
-      sv[k] = word_scale(vw[k]);
-      zv[k] = word_zero(vw[k]);
-    }
-    float x[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) x[nt][2 * k + c] = -zk[k] * qsum[nt][c];
-#pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        const uint32_t ua = kc[0][w], ub = kc[1][w];
-        mma16816(x[nt], ua & 0x000f000fu, ub & 0x000f000fu, ua & 0x00f000f0u, ub & 0x00f000f0u,
-                 qf[nt][w][0], qf[nt][w][1]);
-        const uint32_t va = ua >> 8, vb = ub >> 8;
-        mma16816(x[nt], va & 0x000f000fu, vb & 0x000f000fu, va & 0x00f000f0u, vb & 0x00f000f0u,
-                 qf[nt][w][2], qf[nt][w][3]);
-      }
-    }
-    bool move = sv[0] * fv > 64.f || sv[1] * fv > 64.f || fv == 0.f;
+  // the sums of codes and of zero points nearly cancel (values are centred), and
+  // the tensor core rounds its sum towards zero: keep the difference small
+  auto flush = [&]() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int c = 0; c < 2; ++c) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float& y = x[nt][2 * k + c];
-          y *= sk[k] * qmul[nt][c];
-          if (masked) {
-            const int j = ja + 2 * k;
-            if (!(j < chi[nt][c] && (j >= clo[nt][c] || j < a.sinks))) y = -INFINITY;
-          }
-          move |= y > m[nt][c] + 8.f;
+        for (int i = 0; i < MT; ++i) {
+          o[nt][i][c] -= z[nt][c];
+          o[nt][i][2 + c] = fmaf(z[nt][c], -17.f, o[nt][i][2 + c]);
         }
+        z[nt][c] = 0.f;
+      }
+  };
+  // values' scales are taken times fv, a power of two, so that p s' fits fp16: the
+  // largest so far lies below 2^6 (times 2^8 of a lagging maximum, below 2^14)
+  float fv = 0.f, sv_max = -1.f;
+
+  int koff[HF::KLOADS], voff[4];
+#pragma unroll
+  for (int i = 0; i < HF::KLOADS; ++i) koff[i] = HF::key_lane(gr, t, i);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) voff[i] = HF::value_lane(gr, t, i);
+  const int woff = 2 * HF::CODES + 4 * (4 * (gr >> 1) + (gr & 1));
+  const int zoff = 2 * HF::CODES + 64 + 16 * t;
+  int unflushed = 0, k_now = 0, k_new = RING - 1;
+  for (int st = 0; st < steps; ++st) {
+    copy_wait<RING - 2>();
+    __syncwarp();
+    const uint32_t here = (present >> (2 * k_now)) & 3u;
+    const uint32_t stage = ring + k_now * (2 * HF::BYTES);
+    fetch(st + RING - 1, k_new);         // into the stage that the last step has left
+    k_now = k_now == RING - 1 ? 0 : k_now + 1;
+    k_new = k_new == RING - 1 ? 0 : k_new + 1;
+    if (!here) continue;
+    const int j0 = tok_of(i0 + st);
+    const int ja = j0 + 4 * (gr >> 1) + (gr & 1);        // this lane's tokens: ja + 16 h + 2 k
+    const bool masked =
+        here != 3u || !(j0 + STEP <= all_hi && (j0 >= all_lo || j0 + STEP <= a.sinks));
+    float x[NT][2][4], sv[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t base = stage + h * HF::BYTES;
+      uint32_t kc[2][KW], kw[2], vw[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int i = 0; i < HF::KLOADS; ++i)
+          lds_words<KW / HF::KLOADS>(kc[k] + 4 * i, base + (k ? HF::second_key(koff[i]) : koff[i]));
+        lds_words<1>(&kw[k], base + woff + 8 * k);
+        lds_words<1>(&vw[k], base + woff + 64 + 8 * k);
+        if (masked) {
+          // what no row sees may be memory that was never written
+          const int j = ja + 16 * h + 2 * k;
+          if (!((here >> h) & 1) || !(j < any_hi && (j >= any_lo || j < a.sinks))) kw[k] = vw[k] = 0;
+        }
+        sv[h][k] = word_scale(vw[k]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) x[nt][h][2 * k + c] = word_zero(kw[k]) * qsum[nt][c];
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          const uint32_t ua = kc[0][w], ub = kc[1][w];
+          mma16816(x[nt][h], ua & 0x000f000fu, ub & 0x000f000fu, ua & 0x00f000f0u, ub & 0x00f000f0u,
+                   qf[nt][w][0], qf[nt][w][1]);
+          const uint32_t va = ua >> 8, vb = ub >> 8;
+          mma16816(x[nt][h], va & 0x000f000fu, vb & 0x000f000fu, va & 0x00f000f0u, vb & 0x00f000f0u,
+                   qf[nt][w][2], qf[nt][w][3]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float sk = word_scale(kw[k]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) x[nt][h][2 * k + c] *= sk * qmul[nt][c];
+        }
+      }
+    }
+    if (masked) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int j = ja + 16 * h + 2 * k;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              if (!((here >> h) & 1) || !(j < chi[nt][c] && (j >= clo[nt][c] || j < a.sinks)))
+                x[nt][h][2 * k + c] = -INFINITY;
+        }
+    }
+    const float sv_big = fmaxf(fmaxf(sv[0][0], sv[0][1]), fmaxf(sv[1][0], sv[1][1]));
+    bool move = sv_big > sv_max;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float y = fmaxf(fmaxf(x[nt][0][c], x[nt][0][2 + c]), fmaxf(x[nt][1][c], x[nt][1][2 + c]));
+        move |= y > m[nt][c] + 8.f;
+      }
     if (__any_sync(0xffffffffu, move)) {
       // new maxima (per column, over the lanes of equal t) and value scale
-      float big = fmaxf(sv[0], sv[1]);
+      float big = sv_big;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
       float turn = 1.f;
-      if (big * fv > 64.f || (fv == 0.f && big > 0.f)) {
+      if (big > sv_max && big > 0.f) {
         const int e = min(max(127 - (int)(__float_as_uint(big) >> 23), -100), 100);
         const float nf = __uint_as_float((uint32_t)(127 + e) << 23);
-        // (kept finite when the scale is infinite or NaN: those rows are NaN)
         turn = fv == 0.f ? 1.f : nf / fv;
         fv = nf;
+        sv_max = 64.f / nf;
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float al[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float y = fmaxf(x[nt][c], x[nt][2 + c]);
+          float y = fmaxf(fmaxf(x[nt][0][c], x[nt][0][2 + c]), fmaxf(x[nt][1][c], x[nt][1][2 + c]));
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
           const float nm = fmaxf(m[nt][c], y);
@@ -411,73 +438,66 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
           me[nt][c] = nm == -INFINITY ? 0.f : nm;
           l[nt][c] *= al[c];
           al[c] *= turn;
-          zs[nt][c] *= al[c];
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[nt][j] *= al[j & 1];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[nt][i][j] *= al[j & 1];
       }
     }
-    const float svf[2] = {sv[0] * fv, sv[1] * fv};
-    uint32_t pf[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t base = stage + h * HF::BYTES;
+      uint32_t vc[4][VW], zw[4], pf[NT][2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float pp[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float y = x[nt][2 * k + c];
-          const float p = exp2_approx(y - me[nt][c]);
-          l[nt][c] += p;
-          pp[c] = p * svf[k];
-          if (masked && y == -INFINITY) pp[c] = 0.f;     // (0 times a NaN scale)
-        }
-        const uint32_t h = pack_half2(pp[0], pp[1]);
-        // the zero points' part from the same rounded probabilities
-        const float2 rp = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        zs[nt][0] += rp.x * zv[k];
-        zs[nt][1] += rp.y * zv[k];
-        pf[nt][k] = turn8x8(h);
-      }
-#pragma unroll
-    for (int w = 0; w < VW; ++w) {
-      uint32_t lo01 = __byte_perm(vc[0][w], vc[1][w], 0x5410);
-      uint32_t hi01 = __byte_perm(vc[0][w], vc[1][w], 0x7632);
-      uint32_t lo23 = __byte_perm(vc[2][w], vc[3][w], 0x5410);
-      uint32_t hi23 = __byte_perm(vc[2][w], vc[3][w], 0x7632);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t p01 = q == 0 ? lo01 : q == 1 ? lo01 >> 8 : q == 2 ? hi01 : hi01 >> 8;
-        const uint32_t p23 = q == 0 ? lo23 : q == 1 ? lo23 >> 8 : q == 2 ? hi23 : hi23 >> 8;
-        const uint32_t a0 = p01 & 0x000f000fu, a1 = p01 & 0x00f000f0u, a2 = p23 & 0x000f000fu,
-                       a3 = p23 & 0x00f000f0u;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][4 * w + q], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-      }
-    }
-    // the sums of codes and of zero points nearly cancel (values are centred), and
-    // the tensor core rounds its sum towards zero: keep the difference small
-    if (++unflushed == FLUSH) {
-      unflushed = 0;
+      for (int i = 0; i < 4; ++i) lds_words<VW>(vc[i], base + voff[i]);
+      lds_words<4>(zw, base + zoff);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float z = zs[nt][c];
-          zs[nt][c] = 0.f;
+        for (int k = 0; k < 2; ++k) {
+          const float svf = sv[h][k] * fv;
+          float pp[2];
 #pragma unroll
-          for (int d = 4; d < 32; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-          const float ze = z * 0x1p-24f, zo = z * 0x1p-20f;
+          for (int c = 0; c < 2; ++c) {
+            const float y = x[nt][h][2 * k + c];
+            const float p = exp2_approx(y - me[nt][c]);
+            l[nt][c] += p;
+            pp[c] = p * svf;
+            if (masked && y == -INFINITY) pp[c] = 0.f;     // (0 times a NaN scale)
+          }
+          pf[nt][k] = turn8x8(pack_half2(pp[0], pp[1]));
+        }
+      {
+        const uint32_t z01 = __byte_perm(zw[0], zw[1], 0x5410) & 0x000f000fu;
+        const uint32_t z23 = __byte_perm(zw[2], zw[3], 0x5410) & 0x000f000fu;
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            o[nt][i][c] -= ze;
-            o[nt][i][2 + c] -= zo;
+        for (int nt = 0; nt < NT; ++nt) mma16816(z[nt], z01, z01, z23, z23, pf[nt][0], pf[nt][1]);
+      }
+#pragma unroll
+      for (int w = 0; w < VW; ++w)
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          const uint32_t p01 = __byte_perm(vc[0][w], vc[1][w], q ? 0x7632 : 0x5410);
+          const uint32_t p23 = __byte_perm(vc[2][w], vc[3][w], q ? 0x7632 : 0x5410);
+          const uint32_t b01 = __byte_perm(p01, 0, 0x4341), b23 = __byte_perm(p23, 0, 0x4341);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816(o[nt][4 * w + q], p01 & 0x000f000fu, p01 & 0x00ff00ffu, p23 & 0x000f000fu,
+                     p23 & 0x00ff00ffu, pf[nt][0], pf[nt][1]);
+            mma16816(o[nt][4 * w + q + 1], b01 & 0x000f000fu, b01, b23 & 0x000f000fu, b23, pf[nt][0],
+                     pf[nt][1]);
           }
         }
     }
+    if (++unflushed == FLUSH) {
+      unflushed = 0;
+      flush();
+    }
   }
+  flush();
   copy_wait<0>();
   __syncthreads();                       // the rings become the joining buffer
 
@@ -487,10 +507,7 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int d = 4; d < 32; d <<= 1) {
-        l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], d);
-        zs[nt][c] += __shfl_xor_sync(0xffffffffu, zs[nt][c], d);
-      }
+      for (int d = 4; d < 32; d <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], d);
       if (gr == 0) {
         merge_ml[warp][8 * nt + 2 * t + c][0] = m[nt][c];
         merge_ml[warp][8 * nt + 2 * t + c][1] = l[nt][c];
@@ -508,19 +525,22 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
       for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, merge_ml[w][r][0]);
       const float f = m[nt][c] == -INFINITY ? (l[nt][c] == 0.f ? 0.f : NAN)
                                             : exp2_approx(m[nt][c] - mx) * rfv;
+      const float fe = f * 0x1p24f, fo = f * 0x1p20f;
+      // tile 4 w + q: dims gr (D / 8) + 8 w + 2 q and the next; two tiles to a
+      // 16-byte store, chunks swizzled by the lane's dims
       float* row = merge_o + (warp * R + r) * D;
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        // tile 4 w + q: dims gr (D / 8) + 8 w + 2 q and the next
+      for (int i = 0; i < MT; i += 2) {
         const int d = gr * (D / 8) + 8 * (i >> 2) + 2 * (i & 3);
-        row[d] = (o[nt][i][c] * 0x1p24f - zs[nt][c]) * f;
-        row[d + 1] = (o[nt][i][2 + c] * 0x1p20f - zs[nt][c]) * f;
+        const float4 v = make_float4(o[nt][i][c] * fe, (o[nt][i][2 + c] - o[nt][i][c]) * fo,
+                                     o[nt][i + 1][c] * fe, (o[nt][i + 1][2 + c] - o[nt][i + 1][c]) * fo);
+        *reinterpret_cast<float4*>(row + 4 * ((d >> 2) ^ join_swizzle(d >> 2, r))) = v;
       }
     }
   __syncthreads();
   const int64_t slot = ((int64_t)(u.slot0 + (int)blockIdx.x - u.base) * a.cache.heads + head) * R;
   for (int e = threadIdx.x; e < R * (D / 4); e += THREADS) {
-    const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
+    const int r = e / (D / 4), d4 = e - r * (D / 4);
     if (r0 + r >= rows) break;
     float mx = merge_ml[0][r][0];
 #pragma unroll
@@ -531,19 +551,20 @@ __global__ void __launch_bounds__(THREADS) kv4_attend_kernel(const AttendArgs a)
     for (int w = 0; w < WARPS; ++w) {
       const float mw = merge_ml[w][r][0], lw = merge_ml[w][r][1];
       ls += mw == -INFINITY ? lw : lw * exp2_approx(mw - mx);
-      const float4 v = *reinterpret_cast<const float4*>(merge_o + (w * R + r) * D + d);
+      const float4 v =
+          *reinterpret_cast<const float4*>(merge_o + (w * R + r) * D + 4 * (d4 ^ join_swizzle(d4, r)));
       acc.x += v.x;
       acc.y += v.y;
       acc.z += v.z;
       acc.w += v.w;
     }
     if (u.nsplit > 1) {
-      *reinterpret_cast<float4*>(a.part_o + (slot + r) * D + d) = acc;
-      if (d == 0) a.part_ml[slot + r] = {mx, ls};
+      *reinterpret_cast<float4*>(a.part_o + (slot + r) * D + 4 * d4) = acc;
+      if (d4 == 0) a.part_ml[slot + r] = {mx, ls};
       continue;
     }
-    const int qi = (r0 + r) / a.g, hq = head * a.g + (r0 + r) - qi * a.g;
-    store_row(a, s.row0 + qi, hq, d, acc, mx, ls);
+    const int q = (r0 + r) / a.g, hq = head * a.g + (r0 + r) - q * a.g;
+    store_row(a, s.row0 + q, hq, 4 * d4, acc, mx, ls);
   }
 }
 
@@ -628,7 +649,7 @@ __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, 
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 constexpr unsigned long long TARGET = 148ull * 12;   // units over all heads
-constexpr int MIN_CHUNK = 4;                         // 256 keys
+constexpr int MIN_CHUNK = 2;                         // 256 keys
 
 struct Layout {
   size_t meta, ml, o, total;
@@ -650,7 +671,7 @@ int launch(AttendArgs& a, cudaStream_t st) {
   const long long ux = max_units(a.T, a.g, a.b.B, R, a.cache.heads, a.target);
   if (ux > INT32_MAX) return KRONQ_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)ux, (unsigned)a.cache.heads);
-  constexpr int rings = WARPS * RING * Stage<D>::BYTES, join = WARPS * R * D * (int)sizeof(float);
+  constexpr int rings = WARPS * RING * 2 * Half<D>::BYTES, join = WARPS * R * D * (int)sizeof(float);
   constexpr int smem = rings > join ? rings : join;
   static kqh::PerDevice attr;
   if (kqh::smem_attr_once(attr, kv4_attend_kernel<D, NT>, smem) <= 0) return KRONQ_ERR_CUDA;
