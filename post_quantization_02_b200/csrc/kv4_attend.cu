@@ -22,12 +22,13 @@
 //
 // One block = one (sequence, tile of 8 NT rows, split of its keys) of one
 // key/value head; warp w takes keys 32 w .. of every 128 through a ring of its
-// own in shared memory, filled by cp.async two steps ahead: no barrier
-// between warps, and some 100 KB in flight per SM.  (Bulk copies cannot place
-// the swizzle that keeps the value reads, four tokens apart, off each other's
-// banks.)  The running maximum is only moved when a score passes it by 2^8
-// (all lanes of a column agree by vote), so most steps have no cross-lane
+// own in shared memory, filled by cp.async two steps ahead: no barrier between
+// warps, and some 130 KB in flight per SM.  (Bulk copies from one lane cost
+// more: 89 against 20 issued instructions per 16 tokens.)  The running maximum is only moved when a score passes it by
+// 2^8 (all lanes of a column agree by vote), so most steps have no cross-lane
 // reduction.
+#include <type_traits>
+
 #include "kv4_attend.cuh"
 
 namespace kv4 {
@@ -81,49 +82,27 @@ KQ_DEV void lds_words(uint32_t* w, uint32_t p) {
                  : "r"(p));
 }
 
-// 16 tokens in shared memory (a step has two such halves): key codes, value
-// codes (16 x D/2 bytes each, in 128-byte lines whose 16-byte chunks are
-// swizzled by the token), key words, value words.
+// A step's 32 tokens in shared memory, as they lie in a page: key codes, value
+// codes (32 x D/2 bytes each), key words, value words.  They are multiplied as
+// two halves of 16.
 //
-// Key rows of the MMA: row r of block k (0: rows 0-7, 1: rows 8-15) is token
-// 4 (r >> 1) + 2 k + (r & 1), the order in which the turned probabilities come
-// out as pairs of neighbouring tokens.  Lane (gr, t) reads D/4 dims of the two
-// tokens of row gr, and D/8 dims of the tokens 4t .. 4t + 3 of the values.
+// Lane (gr, t) reads D/8 dims of the values of four tokens T(t, 0 .. 3) of a
+// half, T(t, i) = 4 t + (i ^ (t & 1)): tokens of neighbouring t then differ in
+// parity, which halves the bank conflicts of these reads (to two-way at
+// D = 128; the copies cannot swizzle).  Probabilities come out of the turn as
+// pairs of neighbouring rows of S, so row r of its first 8 is the key
+// T(r >> 1, r & 1) and row r of its second 8 the key T(r >> 1, 2 + (r & 1)),
+// two tokens on; lane (gr, t) reads D/4 dims of these two keys for row gr.
 template <int D>
-struct Half {
+struct Step {
   static constexpr int TOK = D / 2;                 // bytes of a token's codes
-  static constexpr int CODES = 16 * TOK;
-  static constexpr int BYTES = 2 * CODES + 128;
+  static constexpr int V = STEP * TOK, KWORDS = 2 * V, VWORDS = KWORDS + 4 * STEP;
+  static constexpr int BYTES = VWORDS + 4 * STEP;
   static constexpr int KW = D / 32;                 // key words per lane and token
   static constexpr int VW = D / 64;                 // value words per lane and token
-  static constexpr int KLOADS = KW > 4 ? 2 : 1;
+  static constexpr int KLOADS = KW > 4 ? 2 : 1;     // 64 bytes apart: a quad reads 64 at once
 
-  // byte offset of 16-byte chunk c of the keys (values): lines of 8 chunks
-  KQ_DEV static int key_at(int c) {
-    const int tok = c / (TOK / 16);
-    const int x = D == 256 ? 4 * (tok & 1) : D == 128 ? 0 : 4 * ((tok >> 2) & 1);
-    return (c ^ x) * 16;
-  }
-  KQ_DEV static int value_at(int c) {
-    const int tok = c / (TOK / 16);
-    return CODES + (c ^ (2 * ((tok >> 2) & 3))) * 16;
-  }
-  // where lane (gr, t) reads: keys of its first token (load i of KLOADS) and
-  // values of token 4 t + i.  Its second key token is 2 tokens on.
-  KQ_DEV static int key_lane(int gr, int t, int i) {
-    const int tok = 4 * (gr >> 1) + (gr & 1);
-    const int byte = KLOADS == 2 ? 16 * (t + 4 * i) : t * (D / 8);
-    const int at = tok * TOK + byte;
-    return key_at(at / 16) + at % 16;
-  }
-  KQ_DEV static int second_key(int off) {
-    if constexpr (D == 64) return off ^ 64;         // 2 tokens of 32 bytes: the line's other half
-    return off + 2 * TOK;
-  }
-  KQ_DEV static int value_lane(int gr, int t, int i) {
-    const int at = (4 * t + i) * TOK + gr * (D / 16);
-    return value_at(at / 16) + at % 16;
-  }
+  KQ_DEV static int token(int t, int i) { return 4 * t + (i ^ (t & 1)); }
   // dims of word w of lane t's keys
   KQ_DEV static int key_dim(int t, int w) {
     return KLOADS == 2 ? 32 * (t + 4 * (w >> 2)) + 8 * (w & 3) : t * (D / 4) + 8 * w;
@@ -135,14 +114,18 @@ struct Half {
 // t (rows 2 apart, all on the same banks otherwise)
 KQ_DEV int join_swizzle(int c, int r) { return (r >> 1) & 3; }
 
+// The running maximum before there is one: finite, so that a row that has seen no
+// key has sums of 0 and weights of 2^(NO_MAX - max) = 0 or 1, never a NaN.
+constexpr float NO_MAX = -0x1p127f;
+
 constexpr int RING = 3;
 constexpr int FLUSH = 4;      // steps between subtractions of the zero points' part
 
 template <int D, int NT>
 __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_attend_kernel(const AttendArgs a) {
   constexpr int R = 8 * NT;
-  using HF = Half<D>;
-  constexpr int KW = HF::KW, VW = HF::VW, MT = D / 16;
+  using SP = Step<D>;
+  constexpr int KW = SP::KW, VW = SP::VW, MT = D / 16;
   extern __shared__ __align__(128) uint8_t smem[];   // the warps' rings; then [WARPS][R][D] floats
   float* merge_o = reinterpret_cast<float*>(smem);
   __shared__ float merge_ml[WARPS][R][2];
@@ -188,7 +171,15 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
   // ---- keys: the warp's steps are its 32 tokens of every block i0 .. i1 - 1;
   // page numbers of the next 32 halves, one per lane
   const int steps = i1 > i0 ? i1 - i0 : 0;
-  const uint32_t ring = kq::smem_u32(smem) + warp * (RING * 2 * HF::BYTES);
+  const uint32_t ring = kq::smem_u32(smem) + warp * (RING * SP::BYTES);
+  const int P = a.cache.P, Pm = P - 1;
+  const int64_t page_bytes = (int64_t)a.cache.heads * a.cache.block_bytes;
+  const uint8_t* head_base = a.cache.base + (int64_t)head * a.cache.block_bytes + lane * 16;
+  const int vrel = P * SP::TOK;                         // value codes behind key codes
+  // of the words, lane 8 i + 4 h + c copies chunk c of half h of the keys' (i = 0)
+  // or values' (i = 1)
+  const int wrel = P * D + ((lane >> 3) & 1) * P * 4 + (lane & 3) * 16 - lane * 16;
+  const uint32_t ring_lane = ring + lane * 16;
   int page_lane = -1;
   uint32_t present = 0;                  // bits 2k, 2k + 1: the halves of stage k hold tokens
   auto tok_of = [&](int i) { return (i < sp.sb ? i : sp.lb + i - sp.sb) * BLK + STEP * warp; };
@@ -208,27 +199,36 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
           }
         }
       }
-      const int slot0 = tok_of(i0 + st) & (a.cache.P - 1);
+      const int pg0 = __shfl_sync(0xffffffffu, page_lane, 2 * (st & 15));
+      const int pg1 = __shfl_sync(0xffffffffu, page_lane, 2 * (st & 15) + 1);
+      const int slot0 = tok_of(i0 + st) & Pm, slot1 = (slot0 + 16) & Pm;
+      const uint32_t dst = ring_lane + k * SP::BYTES;
+      const uint8_t* b0 = head_base + pg0 * page_bytes;
+      const uint8_t* b1 = head_base + pg1 * page_bytes;
       present &= ~(3u << (2 * k));
+      if (pg0 >= 0) {
+        present |= 1u << (2 * k);
+        const uint8_t* kp = b0 + slot0 * SP::TOK;
+        const uint8_t* vp = kp + vrel;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int pg = __shfl_sync(0xffffffffu, page_lane, 2 * (st & 15) + h);
-        if (pg < 0) continue;
-        present |= 1u << (2 * k + h);
-        const int slot = (slot0 + 16 * h) & (a.cache.P - 1);
-        const uint8_t* blk = a.cache.base + ((int64_t)pg * a.cache.heads + head) * a.cache.block_bytes;
-        const uint8_t* kp = blk + slot * HF::TOK + lane * 16;
-        const uint8_t* vp = kp + a.cache.P * HF::TOK;
-        const uint32_t dst = ring + (2 * k + h) * HF::BYTES;
-#pragma unroll
-        for (int c = 0; c < HF::CODES / 16; c += 32) {
-          copy16(dst + HF::key_at(c + lane), kp + c * 16);
-          copy16(dst + HF::value_at(c + lane), vp + c * 16);
+        for (int c = 0; c < 16 * SP::TOK; c += 512) {
+          copy16(dst + c, kp + c);
+          copy16(dst + SP::V + c, vp + c);
         }
-        if (lane < 8)
-          copy16(dst + 2 * HF::CODES + lane * 16,
-                 blk + a.cache.P * D + ((lane & 4) ? a.cache.P * 4 : 0) + slot * 4 + (lane & 3) * 16);
       }
+      if (pg1 >= 0) {
+        present |= 2u << (2 * k);
+        const uint8_t* kp = b1 + slot1 * SP::TOK;
+        const uint8_t* vp = kp + vrel;
+#pragma unroll
+        for (int c = 0; c < 16 * SP::TOK; c += 512) {
+          copy16(dst + 16 * SP::TOK + c, kp + c);
+          copy16(dst + SP::V + 16 * SP::TOK + c, vp + c);
+        }
+      }
+      const bool h1 = lane & 4;
+      if (lane < 16 && (h1 ? pg1 : pg0) >= 0)
+        copy16(dst + SP::KWORDS, (h1 ? b1 : b0) + wrel + 4 * (h1 ? slot1 : slot0));
     }
     copy_commit();
   };
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
       const uint16_t* p = a.q + (int64_t)(s.row0 + qi[nt]) * a.q_st +
                           (int64_t)(head * a.g + r - qi[nt] * a.g) * a.q_sh;
 #pragma unroll
-      for (int w = 0; w < KW; ++w) load8(p + HF::key_dim(t, w), a.q_vec, a.dt, x[w]);
+      for (int w = 0; w < KW; ++w) load8(p + SP::key_dim(t, w), a.q_vec, a.dt, x[w]);
 #pragma unroll
       for (int w = 0; w < KW; ++w)
 #pragma unroll
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
   // o: even tiles' sums of p s' c over dims e, odd halves' sums of p s' (c_e + 16 c_(e+1))
   // (a byte of codes taken whole saves a mask); z: sums of p s' z'
   float o[NT][MT][4], z[NT][4];
-  float m[NT][2], me[NT][2], l[NT][2];
+  float m[NT][2], l[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -301,8 +301,7 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
     for (int j = 0; j < 4; ++j) z[nt][j] = 0.f;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      m[nt][c] = -INFINITY;     // the running maximum
-      me[nt][c] = 0.f;          // the same, 0 while there is none
+      m[nt][c] = NO_MAX;        // the running maximum
       l[nt][c] = 0.f;
     }
   }
@@ -325,52 +324,42 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
   // largest so far lies below 2^6 (times 2^8 of a lagging maximum, below 2^14)
   float fv = 0.f, sv_max = -1.f;
 
-  int koff[HF::KLOADS], voff[4];
-#pragma unroll
-  for (int i = 0; i < HF::KLOADS; ++i) koff[i] = HF::key_lane(gr, t, i);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) voff[i] = HF::value_lane(gr, t, i);
-  const int woff = 2 * HF::CODES + 4 * (4 * (gr >> 1) + (gr & 1));
-  const int zoff = 2 * HF::CODES + 64 + 16 * t;
-  int unflushed = 0, k_now = 0, k_new = RING - 1;
-  for (int st = 0; st < steps; ++st) {
-    copy_wait<RING - 2>();
-    __syncwarp();
-    const uint32_t here = (present >> (2 * k_now)) & 3u;
-    const uint32_t stage = ring + k_now * (2 * HF::BYTES);
-    fetch(st + RING - 1, k_new);         // into the stage that the last step has left
-    k_now = k_now == RING - 1 ? 0 : k_now + 1;
-    k_new = k_new == RING - 1 ? 0 : k_new + 1;
-    if (!here) continue;
-    const int j0 = tok_of(i0 + st);
-    const int ja = j0 + 4 * (gr >> 1) + (gr & 1);        // this lane's tokens: ja + 16 h + 2 k
-    const bool masked =
-        here != 3u || !(j0 + STEP <= all_hi && (j0 >= all_lo || j0 + STEP <= a.sinks));
-    float x[NT][2][4], sv[2][2];
+  // byte offsets within a stage of what this lane reads
+  const int tok = SP::token(gr >> 1, gr & 1);       // its keys: tok + 16 h + 2 k
+  const int koff = tok * SP::TOK + t * (SP::KLOADS == 2 ? 16 : D / 8);
+  const int voff0 = SP::V + SP::token(t, 0) * SP::TOK + gr * (D / 16);
+  const int voff1 = SP::V + SP::token(t, 1) * SP::TOK + gr * (D / 16);
+  const uint32_t zpick = t & 1 ? 0x1054 : 0x5410;   // T(t, i), i = 0, 1, out of tokens 4t, 4t + 1
+  // one step: two copies of the code, so that steps with every key seen by every
+  // row (all but those at the ends) carry no selections
+  auto multiply = [&](auto is_masked, uint32_t stage, uint32_t here, int j0) {
+    constexpr bool masked = decltype(is_masked)::value;
+    const uint32_t kp = stage + koff, wp = stage + SP::KWORDS + 4 * tok;
+    const uint32_t vp0 = stage + voff0, vp1 = stage + voff1, zp = stage + SP::VWORDS + 16 * t;
+    // x: scores, after their scale relative to the running maximum
+    float x[NT][2][4], sk[2][2], sv[2][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t base = stage + h * HF::BYTES;
-      uint32_t kc[2][KW], kw[2], vw[2];
+      uint32_t kc[2][KW];
+      float kz[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
+        uint32_t kw, vw;
 #pragma unroll
-        for (int i = 0; i < HF::KLOADS; ++i)
-          lds_words<KW / HF::KLOADS>(kc[k] + 4 * i, base + (k ? HF::second_key(koff[i]) : koff[i]));
-        lds_words<1>(&kw[k], base + woff + 8 * k);
-        lds_words<1>(&vw[k], base + woff + 64 + 8 * k);
-        if (masked) {
-          // what no row sees may be memory that was never written
-          const int j = ja + 16 * h + 2 * k;
-          if (!((here >> h) & 1) || !(j < any_hi && (j >= any_lo || j < a.sinks))) kw[k] = vw[k] = 0;
-        }
-        sv[h][k] = word_scale(vw[k]);
+        for (int i = 0; i < SP::KLOADS; ++i)
+          lds_words<KW / SP::KLOADS>(kc[k] + 4 * i, kp + (16 * h + 2 * k) * SP::TOK + 64 * i);
+        lds_words<1>(&kw, wp + 64 * h + 8 * k);
+        lds_words<1>(&vw, wp + 4 * STEP + 64 * h + 8 * k);
+        sk[h][k] = word_scale(kw);
+        kz[k] = word_zero(kw);
+        sv[h][k] = word_scale(vw);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) x[nt][h][2 * k + c] = word_zero(kw[k]) * qsum[nt][c];
+          for (int c = 0; c < 2; ++c) x[nt][h][2 * k + c] = kz[k] * qsum[nt][c];
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
           const uint32_t ua = kc[0][w], ub = kc[1][w];
@@ -380,38 +369,43 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
           mma16816(x[nt][h], va & 0x000f000fu, vb & 0x000f000fu, va & 0x00f000f0u, vb & 0x00f000f0u,
                    qf[nt][w][2], qf[nt][w][3]);
         }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float sk = word_scale(kw[k]);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) x[nt][h][2 * k + c] *= sk * qmul[nt][c];
-        }
       }
     }
-    if (masked) {
+    if constexpr (masked) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int j = ja + 16 * h + 2 * k;
+          const int j = j0 + tok + 16 * h + 2 * k;
+          // what no row sees may be memory that was never written
+          if (!((here >> h) & 1) || !(j < any_hi && (j >= any_lo || j < a.sinks))) sv[h][k] = 0.f;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-              if (!((here >> h) & 1) || !(j < chi[nt][c] && (j >= clo[nt][c] || j < a.sinks)))
-                x[nt][h][2 * k + c] = -INFINITY;
+            for (int c = 0; c < 2; ++c) {
+              const bool seen = ((here >> h) & 1) && j < chi[nt][c] && (j >= clo[nt][c] || j < a.sinks);
+              float& y = x[nt][h][2 * k + c];
+              y = seen ? y * (sk[h][k] * qmul[nt][c]) : -INFINITY;
+            }
+          sk[h][k] = 1.f;                // (applied)
         }
     }
     const float sv_big = fmaxf(fmaxf(sv[0][0], sv[0][1]), fmaxf(sv[1][0], sv[1][1]));
-    bool move = sv_big > sv_max;
+    float top = -INFINITY;
+    float y[NT][2][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float y = fmaxf(fmaxf(x[nt][0][c], x[nt][0][2 + c]), fmaxf(x[nt][1][c], x[nt][1][2 + c]));
-        move |= y > m[nt][c] + 8.f;
-      }
-    if (__any_sync(0xffffffffu, move)) {
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float f = masked ? 1.f : sk[h][k] * qmul[nt][c];
+            y[nt][h][2 * k + c] = fmaf(x[nt][h][2 * k + c], f, -m[nt][c]);
+            top = fmaxf(top, y[nt][h][2 * k + c]);
+          }
+    if (__any_sync(0xffffffffu, top > 8.f || sv_big > sv_max)) {
       // new maxima (per column, over the lanes of equal t) and value scale
       float big = sv_big;
 #pragma unroll
@@ -429,13 +423,23 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
         float al[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float y = fmaxf(fmaxf(x[nt][0][c], x[nt][0][2 + c]), fmaxf(x[nt][1][c], x[nt][1][2 + c]));
+          float nm = m[nt][c];
 #pragma unroll
-          for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
-          const float nm = fmaxf(m[nt][c], y);
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float& v = y[nt][h][2 * k + c];
+              v = x[nt][h][2 * k + c] * (masked ? 1.f : sk[h][k] * qmul[nt][c]);
+              nm = fmaxf(nm, v);
+            }
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, d));
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) y[nt][h][2 * k + c] -= nm;
           al[c] = m[nt][c] == nm ? 1.f : exp2_approx(m[nt][c] - nm);
           m[nt][c] = nm;
-          me[nt][c] = nm == -INFINITY ? 0.f : nm;
           l[nt][c] *= al[c];
           al[c] *= turn;
         }
@@ -449,30 +453,29 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t base = stage + h * HF::BYTES;
       uint32_t vc[4][VW], zw[4], pf[NT][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) lds_words<VW>(vc[i], base + voff[i]);
-      lds_words<4>(zw, base + zoff);
+      for (int i = 0; i < 4; ++i)
+        lds_words<VW>(vc[i], (i & 1 ? vp1 : vp0) + (16 * h + (i & 2)) * SP::TOK);
+      lds_words<4>(zw, zp + 64 * h);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float svf = sv[h][k] * fv;
-          float pp[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float y = x[nt][h][2 * k + c];
-            const float p = exp2_approx(y - me[nt][c]);
-            l[nt][c] += p;
-            pp[c] = p * svf;
-            if (masked && y == -INFINITY) pp[c] = 0.f;     // (0 times a NaN scale)
+          const float p0 = exp2_approx(y[nt][h][2 * k]), p1 = exp2_approx(y[nt][h][2 * k + 1]);
+          l[nt][0] += p0;
+          l[nt][1] += p1;
+          float w0 = p0 * svf, w1 = p1 * svf;
+          if constexpr (masked) {        // (0 times a NaN scale)
+            if (x[nt][h][2 * k] == -INFINITY) w0 = 0.f;
+            if (x[nt][h][2 * k + 1] == -INFINITY) w1 = 0.f;
           }
-          pf[nt][k] = turn8x8(pack_half2(pp[0], pp[1]));
+          pf[nt][k] = turn8x8(pack_half2(w0, w1));
         }
       {
-        const uint32_t z01 = __byte_perm(zw[0], zw[1], 0x5410) & 0x000f000fu;
-        const uint32_t z23 = __byte_perm(zw[2], zw[3], 0x5410) & 0x000f000fu;
+        const uint32_t z01 = __byte_perm(zw[0], zw[1], zpick) & 0x000f000fu;
+        const uint32_t z23 = __byte_perm(zw[2], zw[3], zpick) & 0x000f000fu;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma16816(z[nt], z01, z01, z23, z23, pf[nt][0], pf[nt][1]);
       }
@@ -492,13 +495,31 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
           }
         }
     }
+  };
+  int unflushed = 0, k_now = 0, k_new = RING - 1;
+  for (int st = 0; st < steps; ++st) {
+    const uint32_t here = (present >> (2 * k_now)) & 3u;
+    const uint32_t stage = ring + k_now * SP::BYTES;
+    copy_wait<RING - 2>();
+    __syncwarp();
+    fetch(st + RING - 1, k_new);         // into the stage that the last step has left
+    k_now = k_now == RING - 1 ? 0 : k_now + 1;
+    k_new = k_new == RING - 1 ? 0 : k_new + 1;
+    if (!here) continue;
+    const int j0 = tok_of(i0 + st);
+    const bool masked =
+        here != 3u || !(j0 + STEP <= all_hi && (j0 >= all_lo || j0 + STEP <= a.sinks));
+    if (masked)
+      multiply(std::true_type{}, stage, here, j0);
+    else
+      multiply(std::false_type{}, stage, here, j0);
     if (++unflushed == FLUSH) {
       unflushed = 0;
       flush();
     }
   }
-  flush();
   copy_wait<0>();
+  flush();
   __syncthreads();                       // the rings become the joining buffer
 
   // ---- join the warps
@@ -523,8 +544,7 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
       float mx = merge_ml[0][r][0];
 #pragma unroll
       for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, merge_ml[w][r][0]);
-      const float f = m[nt][c] == -INFINITY ? (l[nt][c] == 0.f ? 0.f : NAN)
-                                            : exp2_approx(m[nt][c] - mx) * rfv;
+      const float f = exp2_approx(m[nt][c] - mx) * rfv;
       const float fe = f * 0x1p24f, fo = f * 0x1p20f;
       // tile 4 w + q: dims gr (D / 8) + 8 w + 2 q and the next; two tiles to a
       // 16-byte store, chunks swizzled by the lane's dims
@@ -550,7 +570,7 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
       const float mw = merge_ml[w][r][0], lw = merge_ml[w][r][1];
-      ls += mw == -INFINITY ? lw : lw * exp2_approx(mw - mx);
+      ls += lw * exp2_approx(mw - mx);
       const float4 v =
           *reinterpret_cast<const float4*>(merge_o + (w * R + r) * D + 4 * (d4 ^ join_swizzle(d4, r)));
       acc.x += v.x;
@@ -618,8 +638,7 @@ __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, 
           v[e + 3] = x.w;
         }
       }
-      // a split without a key (m = -inf, l = 0) counts nothing; a NaN stays
-      const float w = q.m == -INFINITY ? (q.l == 0.f ? 0.f : NAN) : exp2_approx(q.m - m);
+      const float w = exp2_approx(q.m - m);
       l += q.l * w;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[e], o[e]);
@@ -671,7 +690,7 @@ int launch(AttendArgs& a, cudaStream_t st) {
   const long long ux = max_units(a.T, a.g, a.b.B, R, a.cache.heads, a.target);
   if (ux > INT32_MAX) return KRONQ_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)ux, (unsigned)a.cache.heads);
-  constexpr int rings = WARPS * RING * 2 * Half<D>::BYTES, join = WARPS * R * D * (int)sizeof(float);
+  constexpr int rings = WARPS * RING * Step<D>::BYTES, join = WARPS * R * D * (int)sizeof(float);
   constexpr int smem = rings > join ? rings : join;
   static kqh::PerDevice attr;
   if (kqh::smem_attr_once(attr, kv4_attend_kernel<D, NT>, smem) <= 0) return KRONQ_ERR_CUDA;
