@@ -6,27 +6,35 @@
 //
 // (s, z, c: scale, zero point and codes of key j; primed of value j).  Scales
 // and zero points are per token, so they are taken out of both products: the
-// tensor cores multiply the bare codes, and 128 codes of a token cost one
-// scale.  A code in the low bits of a half is the subnormal c 2^-24 (and
-// c 2^-20 four bits up), exact in fp16 x fp16 -> fp32 products: unpacking is
-// one AND per two codes and one shift per four pairs; the factors 16 go into
-// the queries (keys) and into the epilogue (values).
+// tensor cores multiply the bare codes, and 128 codes of a token cost one scale.
 //
-// S^T = K Q^T and O^T = V^T P^T with mma.m16n8k16: keys (or dims) are the 16
-// rows and the query rows of one key/value head the 8 columns, so a group of 8
-// or fewer query heads wastes none of the code operand.  (A tensor-memory
-// accumulator of 128 lanes would be filled the same way, but its operand has
-// to be written to shared or tensor memory after unpacking; with mma.sync the
-// unpacked words are the fragment.)  Between the two products the 8 x 8 blocks
-// of probabilities are turned with movmatrix.
+// What bounds it is not the copy but the integer instructions that turn 4-bit codes
+// into operands.  A code in the low bits of a half is the subnormal c 2^-24 (c 2^-20
+// four bits up), exact in fp16 x fp16 -> fp32 products, so:
+//   keys    unpacking is one AND per two codes and one shift per four pairs; the
+//           factors 16 of every other pair go into the queries' fragments;
+//   values  the tokens of a dim come together by ldmatrix.trans on bytes (two dims);
+//           a byte taken whole is c_even + 16 c_odd, which saves a mask: the odd
+//           dim is the difference, taken once at the end.
+// (8-bit operands would halve the unpacking: 0000cccc is an e4m3 number and a u8.
+// mma.sync on e4m3 is two fp16 MMAs and conversions on this machine, measured 1.6
+// times slower over all; on s8 it runs at the fp16 instruction rate, with queries in
+// two terms and two sums to convert.)
+//
+// S^T = K Q^T and O^T = V^T P^T: keys (or dims) are the 16 rows of the MMA and the
+// query rows of one key/value head the 8 columns, so a group of 8 or fewer query
+// heads wastes none of the code operand.  (A tensor-memory accumulator of 128 lanes
+// would be filled the same way, but its operand has to be written to shared or
+// tensor memory after unpacking; here the unpacked words are the fragment.)  Between
+// the two products the 8 x 8 blocks of probabilities are turned with movmatrix.
 //
 // One block = one (sequence, tile of 8 NT rows, split of its keys) of one
 // key/value head; warp w takes keys 32 w .. of every 128 through a ring of its
 // own in shared memory, filled by cp.async two steps ahead: no barrier between
 // warps, and some 130 KB in flight per SM.  (Bulk copies from one lane cost
-// more: 89 against 20 issued instructions per 16 tokens.)  The running maximum is only moved when a score passes it by
-// 2^8 (all lanes of a column agree by vote), so most steps have no cross-lane
-// reduction.
+// more: 89 against 20 issued instructions per 16 tokens.)  The running maximum
+// is only moved when a score passes it by 2^8 (all lanes of a column agree by
+// vote), so most steps have no cross-lane reduction.
 #include <type_traits>
 
 #include "kv4_attend.cuh"
@@ -42,6 +50,14 @@ KQ_DEV void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint3
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two 16 x 16 byte blocks (lane l: row l % 16 of block l / 16), turned: register
+// 2 i + j of lane (gr, t) holds column 8 j + gr, rows 4t .. 4t + 3 of block i.
+KQ_DEV void ldmatrix_turned(uint32_t (&r)[4], uint32_t p) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(p));
 }
 
 KQ_DEV uint32_t turn8x8(uint32_t x) {
@@ -82,37 +98,61 @@ KQ_DEV void lds_words(uint32_t* w, uint32_t p) {
                  : "r"(p));
 }
 
-// A step's 32 tokens in shared memory, as they lie in a page: key codes, value
-// codes (32 x D/2 bytes each), key words, value words.  They are multiplied as
-// two halves of 16.
+// A step's 32 tokens in shared memory: key codes, value codes (32 x D/2 bytes
+// each, in 128-byte lines whose 16-byte chunks are swizzled by the token so that
+// neither read has bank conflicts), key words, value words.  They are multiplied
+// as two halves of 16.
 //
-// Lane (gr, t) reads D/8 dims of the values of four tokens T(t, 0 .. 3) of a
-// half, T(t, i) = 4 t + (i ^ (t & 1)): tokens of neighbouring t then differ in
-// parity, which halves the bank conflicts of these reads (to two-way at
-// D = 128; the copies cannot swizzle).  Probabilities come out of the turn as
-// pairs of neighbouring rows of S, so row r of its first 8 is the key
-// T(r >> 1, r & 1) and row r of its second 8 the key T(r >> 1, 2 + (r & 1)),
-// two tokens on; lane (gr, t) reads D/4 dims of these two keys for row gr.
+// Probabilities come out of the turn as pairs of neighbouring rows of S and meet
+// the values' tokens 4t .. 4t + 3 in lane (gr, t), so row r of the first 8 rows of S
+// is the key 4 (r >> 1) + (r & 1), row r of the second 8 the key two tokens on.
+// Lane (gr, t) reads D/4 dims of these two keys for row gr.
 template <int D>
 struct Step {
   static constexpr int TOK = D / 2;                 // bytes of a token's codes
   static constexpr int V = STEP * TOK, KWORDS = 2 * V, VWORDS = KWORDS + 4 * STEP;
   static constexpr int BYTES = VWORDS + 4 * STEP;
   static constexpr int KW = D / 32;                 // key words per lane and token
-  static constexpr int VW = D / 64;                 // value words per lane and token
+  static constexpr int VC = D / 32;                 // 16-byte chunks of a token's values
   static constexpr int KLOADS = KW > 4 ? 2 : 1;     // 64 bytes apart: a quad reads 64 at once
 
-  KQ_DEV static int token(int t, int i) { return 4 * t + (i ^ (t & 1)); }
+  // byte offsets of 16-byte chunk c of the keys, of the values
+  KQ_DEV static int key_at(int c) {
+    const int tok = c / VC;
+    const int x = D == 256 ? 4 * (tok & 1) : D == 128 ? 0 : 4 * ((tok >> 2) & 1);
+    return (c ^ x) * 16;
+  }
+  KQ_DEV static int value_at(int c) {
+    const int tok = c / VC;
+    const int x = D == 256 ? tok & 7 : D == 128 ? (tok >> 1) & 3 : (tok >> 2) & 1;
+    return V + (c ^ x) * 16;
+  }
+  // where lane (gr, t) reads its first key token (load i of KLOADS); the second
+  KQ_DEV static int key_lane(int gr, int t, int i) {
+    const int tok = 4 * (gr >> 1) + (gr & 1);
+    const int at = tok * TOK + (KLOADS == 2 ? 16 * (t + 4 * i) : t * (D / 8));
+    return key_at(at / 16) + at % 16;
+  }
+  KQ_DEV static int second_key(int off) {
+    if constexpr (D == 64) return off ^ 64;         // 2 tokens of 32 bytes: the line's other half
+    return off + 2 * TOK;
+  }
   // dims of word w of lane t's keys
   KQ_DEV static int key_dim(int t, int w) {
     return KLOADS == 2 ? 32 * (t + 4 * (w >> 2)) + 8 * (w & 3) : t * (D / 4) + 8 * w;
   }
 };
 
-// chunk c (4 floats) of row r of the joining buffer is stored at c ^ this: a
-// store's 8 lanes of a phase have 2 values of gr (chunks D/32 apart) and 4 of
-// t (rows 2 apart, all on the same banks otherwise)
-KQ_DEV int join_swizzle(int c, int r) { return (r >> 1) & 3; }
+// The next 16 steps of a warp: where their halves lie (0: nowhere), and for the last
+// 32 steps the first token with flags in its low bits.
+struct Plan {
+  uint64_t codes[16][2], words[16][2];
+  uint32_t first[32];      // token | halves present (1, 2) | some row does not see some key (4)
+};
+
+// chunk c (4 floats) of row r of the joining buffer is stored at c ^ this: the 16
+// lanes of a phase store 8 floats to each of 4 rows, 2 rows apart
+KQ_DEV int join_swizzle(int r) { return 2 * ((r >> 1) & 3); }
 
 // The running maximum before there is one: finite, so that a row that has seen no
 // key has sums of 0 and weights of 2^(NO_MAX - max) = 0 or 1, never a NaN.
@@ -125,10 +165,11 @@ template <int D, int NT>
 __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_attend_kernel(const AttendArgs a) {
   constexpr int R = 8 * NT;
   using SP = Step<D>;
-  constexpr int KW = SP::KW, VW = SP::VW, MT = D / 16;
+  constexpr int KW = SP::KW, MT = D / 16;
   extern __shared__ __align__(128) uint8_t smem[];   // the warps' rings; then [WARPS][R][D] floats
   float* merge_o = reinterpret_cast<float*>(smem);
   __shared__ float merge_ml[WARPS][R][2];
+  __shared__ __align__(16) Plan plans[WARPS];
 
   Unit u;
   if (!find_unit<R, BLK, THREADS>(a, blockIdx.x, &u)) return;
@@ -168,72 +209,63 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
     }
   const int all_lo = lo_of(q1), all_hi = hi_of(q0), any_lo = lo_of(q0), any_hi = hi_of(q1);
 
-  // ---- keys: the warp's steps are its 32 tokens of every block i0 .. i1 - 1;
-  // page numbers of the next 32 halves, one per lane
+  // ---- keys: the warp's steps are its 32 tokens of every block i0 .. i1 - 1
   const int steps = i1 > i0 ? i1 - i0 : 0;
   const uint32_t ring = kq::smem_u32(smem) + warp * (RING * SP::BYTES);
-  const int P = a.cache.P, Pm = P - 1;
-  const int64_t page_bytes = (int64_t)a.cache.heads * a.cache.block_bytes;
-  const uint8_t* head_base = a.cache.base + (int64_t)head * a.cache.block_bytes + lane * 16;
-  const int vrel = P * SP::TOK;                         // value codes behind key codes
+  Plan& plan = plans[warp];
+  auto look_ahead = [&](int st) {        // plans steps st .. st + 15, a half per lane
+    const int s1 = st + (lane >> 1);
+    const int i = i0 + s1;
+    const int j0 = (i < sp.sb ? i : sp.lb + i - sp.sb) * BLK + STEP * warp;
+    const int j = j0 + 16 * (lane & 1);
+    int64_t page = -1;
+    if (s1 < steps && j < any_hi && (j + 16 > any_lo || j < a.sinks)) {
+      page = a.b.table[u.b * a.b.table_ld + (j >> a.cache.lgP)];
+      if (page < 0 || page >= a.cache.pages) {
+        kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
+        page = -1;
+      }
+    }
+    const int P = a.cache.P, slot = j & (P - 1);
+    const uint8_t* blk = a.cache.base + (page * a.cache.heads + head) * a.cache.block_bytes;
+    const uint32_t both = __ballot_sync(0xffffffffu, page >= 0);
+    const uint32_t here = (both >> (lane & ~1)) & 3u;
+    plan.codes[s1 & 15][lane & 1] = page >= 0 ? (uint64_t)(blk + slot * SP::TOK) : 0;
+    plan.words[s1 & 15][lane & 1] = page >= 0 ? (uint64_t)(blk + P * D + slot * 4) : 0;
+    const bool masked = here != 3u || !(j0 + STEP <= all_hi && (j0 >= all_lo || j0 + STEP <= a.sinks));
+    if (!(lane & 1)) plan.first[s1 & 31] = (uint32_t)j0 | here | (masked ? 4u : 0u);
+    __syncwarp();
+  };
+  const int vrel = a.cache.P * SP::TOK;                 // value codes behind key codes
   // of the words, lane 8 i + 4 h + c copies chunk c of half h of the keys' (i = 0)
   // or values' (i = 1)
-  const int wrel = P * D + ((lane >> 3) & 1) * P * 4 + (lane & 3) * 16 - lane * 16;
-  const uint32_t ring_lane = ring + lane * 16;
-  int page_lane = -1;
-  uint32_t present = 0;                  // bits 2k, 2k + 1: the halves of stage k hold tokens
-  auto tok_of = [&](int i) { return (i < sp.sb ? i : sp.lb + i - sp.sb) * BLK + STEP * warp; };
-  auto fetch = [&](int st, int k) {      // step st into stage k
+  const int word_half = (lane >> 2) & 1;
+  const int wrel = ((lane >> 3) & 1) * a.cache.P * 4 + (lane & 3) * 16;
+  auto fetch = [&](int st, uint32_t dst) {      // step st into the stage at dst
     if (st < steps) {
-      if ((st & 15) == 0) {
-        page_lane = -1;
-        const int s1 = st + (lane >> 1);
-        if (s1 < steps) {
-          const int j = tok_of(i0 + s1) + 16 * (lane & 1);
-          if (j < any_hi && (j + 16 > any_lo || j < a.sinks)) {
-            page_lane = a.b.table[u.b * a.b.table_ld + (j >> a.cache.lgP)];
-            if (page_lane < 0 || page_lane >= a.cache.pages) {
-              kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
-              page_lane = -1;
-            }
+      if ((st & 15) == 0) look_ahead(st);
+      const ulonglong2 at = *reinterpret_cast<const ulonglong2*>(plan.codes[st & 15]);
+      const uint64_t w = plan.words[st & 15][word_half];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint64_t p = h ? at.y : at.x;
+        if (p) {
+          const uint8_t* kp = reinterpret_cast<const uint8_t*>(p) + lane * 16;
+          const uint8_t* vp = kp + vrel;
+#pragma unroll
+          for (int c = 0; c < 16 * SP::TOK; c += 512) {
+            const int chunk = h * SP::TOK + c / 16 + lane;
+            copy16(dst + SP::key_at(chunk), kp + c);
+            copy16(dst + SP::value_at(chunk), vp + c);
           }
         }
       }
-      const int pg0 = __shfl_sync(0xffffffffu, page_lane, 2 * (st & 15));
-      const int pg1 = __shfl_sync(0xffffffffu, page_lane, 2 * (st & 15) + 1);
-      const int slot0 = tok_of(i0 + st) & Pm, slot1 = (slot0 + 16) & Pm;
-      const uint32_t dst = ring_lane + k * SP::BYTES;
-      const uint8_t* b0 = head_base + pg0 * page_bytes;
-      const uint8_t* b1 = head_base + pg1 * page_bytes;
-      present &= ~(3u << (2 * k));
-      if (pg0 >= 0) {
-        present |= 1u << (2 * k);
-        const uint8_t* kp = b0 + slot0 * SP::TOK;
-        const uint8_t* vp = kp + vrel;
-#pragma unroll
-        for (int c = 0; c < 16 * SP::TOK; c += 512) {
-          copy16(dst + c, kp + c);
-          copy16(dst + SP::V + c, vp + c);
-        }
-      }
-      if (pg1 >= 0) {
-        present |= 2u << (2 * k);
-        const uint8_t* kp = b1 + slot1 * SP::TOK;
-        const uint8_t* vp = kp + vrel;
-#pragma unroll
-        for (int c = 0; c < 16 * SP::TOK; c += 512) {
-          copy16(dst + 16 * SP::TOK + c, kp + c);
-          copy16(dst + SP::V + 16 * SP::TOK + c, vp + c);
-        }
-      }
-      const bool h1 = lane & 4;
-      if (lane < 16 && (h1 ? pg1 : pg0) >= 0)
-        copy16(dst + SP::KWORDS, (h1 ? b1 : b0) + wrel + 4 * (h1 ? slot1 : slot0));
+      if (lane < 16 && w) copy16(dst + SP::KWORDS + lane * 16, reinterpret_cast<const uint8_t*>(w) + wrel);
     }
     copy_commit();
   };
 #pragma unroll
-  for (int k = 0; k < RING - 1; ++k) fetch(k, k);
+  for (int k = 0; k < RING - 1; ++k) fetch(k, ring + k * SP::BYTES);
 
   // ---- queries: fp16 fragments of q 2^e (e per row: the largest becomes about
   // 2^10, so bf16's range is kept and so are 20 binades below the row's largest)
@@ -287,8 +319,8 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
     }
   }
 
-  // o: even tiles' sums of p s' c over dims e, odd halves' sums of p s' (c_e + 16 c_(e+1))
-  // (a byte of codes taken whole saves a mask); z: sums of p s' z'
+  // o: tile i's sums of p s' c over dim 16 i + 2 gr (0, 1) and of p s' (c + 16 c of the next
+  // dim) (2, 3), for columns 2t, 2t + 1; z: sums of p s' z'
   float o[NT][MT][4], z[NT][4];
   float m[NT][2], l[NT][2];
 #pragma unroll
@@ -325,17 +357,16 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
   float fv = 0.f, sv_max = -1.f;
 
   // byte offsets within a stage of what this lane reads
-  const int tok = SP::token(gr >> 1, gr & 1);       // its keys: tok + 16 h + 2 k
-  const int koff = tok * SP::TOK + t * (SP::KLOADS == 2 ? 16 : D / 8);
-  const int voff0 = SP::V + SP::token(t, 0) * SP::TOK + gr * (D / 16);
-  const int voff1 = SP::V + SP::token(t, 1) * SP::TOK + gr * (D / 16);
-  const uint32_t zpick = t & 1 ? 0x1054 : 0x5410;   // T(t, i), i = 0, 1, out of tokens 4t, 4t + 1
+  const int tok = 4 * (gr >> 1) + (gr & 1);         // its keys: tok + 16 h + 2 k
+  int koff[SP::KLOADS];
+#pragma unroll
+  for (int i = 0; i < SP::KLOADS; ++i) koff[i] = SP::key_lane(gr, t, i);
+  const int voff = SP::value_at((lane & 15) * SP::VC + (lane >> 4));
   // one step: two copies of the code, so that steps with every key seen by every
   // row (all but those at the ends) carry no selections
   auto multiply = [&](auto is_masked, uint32_t stage, uint32_t here, int j0) {
     constexpr bool masked = decltype(is_masked)::value;
-    const uint32_t kp = stage + koff, wp = stage + SP::KWORDS + 4 * tok;
-    const uint32_t vp0 = stage + voff0, vp1 = stage + voff1, zp = stage + SP::VWORDS + 16 * t;
+    const uint32_t wp = stage + SP::KWORDS + 4 * tok, zp = stage + SP::VWORDS + 16 * t;
     // x: scores, after their scale relative to the running maximum
     float x[NT][2][4], sk[2][2], sv[2][2];
 #pragma unroll
@@ -347,7 +378,8 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
         uint32_t kw, vw;
 #pragma unroll
         for (int i = 0; i < SP::KLOADS; ++i)
-          lds_words<KW / SP::KLOADS>(kc[k] + 4 * i, kp + (16 * h + 2 * k) * SP::TOK + 64 * i);
+          lds_words<KW / SP::KLOADS>(
+              kc[k] + 4 * i, stage + (k ? SP::second_key(koff[i]) : koff[i]) + 16 * h * SP::TOK);
         lds_words<1>(&kw, wp + 64 * h + 8 * k);
         lds_words<1>(&vw, wp + 4 * STEP + 64 * h + 8 * k);
         sk[h][k] = word_scale(kw);
@@ -453,10 +485,7 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t vc[4][VW], zw[4], pf[NT][2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        lds_words<VW>(vc[i], (i & 1 ? vp1 : vp0) + (16 * h + (i & 2)) * SP::TOK);
+      uint32_t zw[4], pf[NT][2];
       lds_words<4>(zw, zp + 64 * h);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -474,45 +503,41 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
           pf[nt][k] = turn8x8(pack_half2(w0, w1));
         }
       {
-        const uint32_t z01 = __byte_perm(zw[0], zw[1], zpick) & 0x000f000fu;
-        const uint32_t z23 = __byte_perm(zw[2], zw[3], zpick) & 0x000f000fu;
+        const uint32_t z01 = __byte_perm(zw[0], zw[1], 0x5410) & 0x000f000fu;
+        const uint32_t z23 = __byte_perm(zw[2], zw[3], 0x5410) & 0x000f000fu;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma16816(z[nt], z01, z01, z23, z23, pf[nt][0], pf[nt][1]);
       }
 #pragma unroll
-      for (int w = 0; w < VW; ++w)
+      for (int c = 0; c < SP::VC; c += 2) {
+        uint32_t v[4];
+        ldmatrix_turned(v, ((stage + voff) ^ (16 * c)) + 16 * h * SP::TOK);
 #pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-          const uint32_t p01 = __byte_perm(vc[0][w], vc[1][w], q ? 0x7632 : 0x5410);
-          const uint32_t p23 = __byte_perm(vc[2][w], vc[3][w], q ? 0x7632 : 0x5410);
-          const uint32_t b01 = __byte_perm(p01, 0, 0x4341), b23 = __byte_perm(p23, 0, 0x4341);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t b01 = __byte_perm(v[i], 0, 0x4140), b23 = __byte_perm(v[i], 0, 0x4342);
+          const uint32_t c01 = b01 & 0x000f000fu, c23 = b23 & 0x000f000fu;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma16816(o[nt][4 * w + q], p01 & 0x000f000fu, p01 & 0x00ff00ffu, p23 & 0x000f000fu,
-                     p23 & 0x00ff00ffu, pf[nt][0], pf[nt][1]);
-            mma16816(o[nt][4 * w + q + 1], b01 & 0x000f000fu, b01, b23 & 0x000f000fu, b23, pf[nt][0],
-                     pf[nt][1]);
-          }
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(o[nt][2 * c + i], c01, b01, c23, b23, pf[nt][0], pf[nt][1]);
         }
+      }
     }
   };
-  int unflushed = 0, k_now = 0, k_new = RING - 1;
+  int unflushed = 0;
+  uint32_t now = ring, next = ring + (RING - 1) * SP::BYTES;
+  const uint32_t ring_end = ring + RING * SP::BYTES;
   for (int st = 0; st < steps; ++st) {
-    const uint32_t here = (present >> (2 * k_now)) & 3u;
-    const uint32_t stage = ring + k_now * SP::BYTES;
     copy_wait<RING - 2>();
     __syncwarp();
-    fetch(st + RING - 1, k_new);         // into the stage that the last step has left
-    k_now = k_now == RING - 1 ? 0 : k_now + 1;
-    k_new = k_new == RING - 1 ? 0 : k_new + 1;
-    if (!here) continue;
-    const int j0 = tok_of(i0 + st);
-    const bool masked =
-        here != 3u || !(j0 + STEP <= all_hi && (j0 >= all_lo || j0 + STEP <= a.sinks));
-    if (masked)
-      multiply(std::true_type{}, stage, here, j0);
+    const uint32_t first = plan.first[st & 31], stage = now;
+    fetch(st + RING - 1, next);          // into the stage that the last step has left
+    now = now + SP::BYTES == ring_end ? ring : now + SP::BYTES;
+    next = next + SP::BYTES == ring_end ? ring : next + SP::BYTES;
+    if (!(first & 3u)) continue;
+    if (first & 4u)
+      multiply(std::true_type{}, stage, first & 3u, (int)(first & ~7u));
     else
-      multiply(std::false_type{}, stage, here, j0);
+      multiply(std::false_type{}, stage, 3u, (int)(first & ~7u));
     if (++unflushed == FLUSH) {
       unflushed = 0;
       flush();
@@ -546,15 +571,12 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
       for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, merge_ml[w][r][0]);
       const float f = exp2_approx(m[nt][c] - mx) * rfv;
       const float fe = f * 0x1p24f, fo = f * 0x1p20f;
-      // tile 4 w + q: dims gr (D / 8) + 8 w + 2 q and the next; two tiles to a
-      // 16-byte store, chunks swizzled by the lane's dims
       float* row = merge_o + (warp * R + r) * D;
 #pragma unroll
-      for (int i = 0; i < MT; i += 2) {
-        const int d = gr * (D / 8) + 8 * (i >> 2) + 2 * (i & 3);
-        const float4 v = make_float4(o[nt][i][c] * fe, (o[nt][i][2 + c] - o[nt][i][c]) * fo,
-                                     o[nt][i + 1][c] * fe, (o[nt][i + 1][2 + c] - o[nt][i + 1][c]) * fo);
-        *reinterpret_cast<float4*>(row + 4 * ((d >> 2) ^ join_swizzle(d >> 2, r))) = v;
+      for (int i = 0; i < MT; ++i) {
+        const int d = 16 * i + 2 * gr;
+        *reinterpret_cast<float2*>(row + 4 * ((d >> 2) ^ join_swizzle(r)) + (d & 3)) =
+            make_float2(o[nt][i][c] * fe, (o[nt][i][2 + c] - o[nt][i][c]) * fo);
       }
     }
   __syncthreads();
@@ -572,7 +594,7 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
       const float mw = merge_ml[w][r][0], lw = merge_ml[w][r][1];
       ls += lw * exp2_approx(mw - mx);
       const float4 v =
-          *reinterpret_cast<const float4*>(merge_o + (w * R + r) * D + 4 * (d4 ^ join_swizzle(d4, r)));
+          *reinterpret_cast<const float4*>(merge_o + (w * R + r) * D + 4 * (d4 ^ join_swizzle(r)));
       acc.x += v.x;
       acc.y += v.y;
       acc.z += v.z;
