@@ -691,19 +691,37 @@ size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 constexpr unsigned long long TARGET = 148ull * 12;   // units over all heads
 constexpr int MIN_CHUNK = 2;                         // 256 keys
+constexpr int64_t PROMPT_ROWS = 16;
+constexpr unsigned long long PROMPT_TARGET = 148ull * 4;
+constexpr int PROMPT_MIN_KEYS = 512;
+
+// How a call is run.  Rows per sequence and key/value head decide (on average:
+// lengths are on the device): the tensor-memory kernel fills 128 rows whatever
+// there are.
+struct Way {
+  bool prompt;
+  int R, BLK, min_chunk;
+  unsigned long long target;
+};
+
+Way way_of(int64_t T, int g, int D, int64_t B) {
+  if (T * g > PROMPT_ROWS * B)
+    return {true, prompt_rows(D), prompt_block(D), PROMPT_MIN_KEYS / prompt_block(D), PROMPT_TARGET};
+  return {false, D == 256 || T * g <= 8 * B ? 8 : 16, BLK, MIN_CHUNK, TARGET};
+}
 
 struct Layout {
   size_t meta, ml, o, total;
 };
 
-Layout layout_of(int R, int D, int heads, int64_t B) {
-  const size_t rows = (size_t)max_slots(heads, TARGET) * heads * R;
-  Layout w;
-  w.meta = 0;
-  w.ml = up256((size_t)B * sizeof(int2));
-  w.o = w.ml + up256(rows * sizeof(Part));
-  w.total = w.o + up256(rows * D * sizeof(float));
-  return w;
+Layout layout_of(const Way& w, int D, int heads, int64_t B) {
+  const size_t rows = (size_t)max_slots(heads, w.target) * heads * w.R;
+  Layout l;
+  l.meta = 0;
+  l.ml = up256((size_t)B * sizeof(int2));
+  l.o = l.ml + up256(rows * sizeof(Part));
+  l.total = l.o + up256(rows * D * sizeof(float));
+  return l;
 }
 
 template <int D, int NT>
@@ -718,9 +736,11 @@ int launch(AttendArgs& a, cudaStream_t st) {
   if (kqh::smem_attr_once(attr, kv4_attend_kernel<D, NT>, smem) <= 0) return KRONQ_ERR_CUDA;
   kv4_attend_kernel<D, NT><<<grid, THREADS, smem, st>>>(a);
   KQ_CHECK_LAUNCH();
-  // no sequence can be split when the longest one the table holds is one chunk
-  const long long most = (((long long)a.b.max_pages << a.cache.lgP) + BLK - 1) / BLK;
-  if (most <= a.min_chunk) return KRONQ_OK;
+  return KRONQ_OK;
+}
+
+template <int D>
+int launch_merge(const AttendArgs& a, int R, cudaStream_t st) {
   const int hpb = (long long)a.T * a.Hq <= 16384 ? 1 : a.Hq;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.T, (unsigned)((a.Hq + hpb - 1) / hpb));
@@ -731,10 +751,24 @@ int launch(AttendArgs& a, cudaStream_t st) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D>, (const AttendArgs)a, R, hpb) != cudaSuccess)
-    return KRONQ_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D>, a, R, hpb) != cudaSuccess) return KRONQ_ERR_CUDA;
   KQ_CHECK_LAUNCH();
   return KRONQ_OK;
+}
+
+template <int D>
+int run(AttendArgs& a, const Way& w, cudaStream_t st) {
+  int s;
+  if (w.prompt)
+    s = launch_prompt(a, D, st);
+  else if (D == 256 || w.R == 8)
+    s = launch<D, 1>(a, st);
+  else
+    s = launch<D, D == 256 ? 1 : 2>(a, st);
+  if (s != KRONQ_OK) return s;
+  // no sequence can be split when the longest one the table holds is one chunk
+  const long long most = (((long long)a.b.max_pages << a.cache.lgP) + w.BLK - 1) / w.BLK;
+  return most <= a.min_chunk ? KRONQ_OK : launch_merge<D>(a, w.R, st);
 }
 
 }  // namespace
@@ -742,7 +776,7 @@ int launch(AttendArgs& a, cudaStream_t st) {
 
 size_t kq_kv4_attention_ws(int64_t T, int Hq, int heads, int D, int64_t B) {
   if (T < 0 || Hq <= 0 || heads <= 0 || Hq % heads || B <= 0 || (D != 64 && D != 128 && D != 256)) return 0;
-  return kv4::layout_of(16, D, heads, B).total;
+  return kv4::layout_of(kv4::way_of(T, Hq / heads, D, B), D, heads, B).total;
 }
 
 int kq_kv4_attention(const void* q, int64_t q_st, int64_t q_sh, int dtype, int64_t T, int Hq, int D,
@@ -781,17 +815,15 @@ int kq_kv4_attention(const void* q, int64_t q_st, int64_t q_sh, int dtype, int64
   a.window = window > (1 << 30) ? 0 : window;    // wider than any sequence
   a.sinks = !a.window ? 0 : sinks > (1 << 30) ? 1 << 30 : sinks;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.min_chunk = MIN_CHUNK;
-  a.target = TARGET;
-  a.slots = (int)max_slots(c.heads, TARGET);
+  const Way way = way_of(T, g, D, b.B);
+  a.min_chunk = way.min_chunk;
+  a.target = way.target;
+  a.slots = (int)max_slots(c.heads, way.target);
   a.info = info;
-  const int NT = D == 256 || T * g <= 8 * (long long)b.B ? 1 : 2;
-  const Layout w = layout_of(8 * NT, D, c.heads, b.B);
+  const Layout w = layout_of(way, D, c.heads, b.B);
   uint8_t* base = static_cast<uint8_t*>(ws);
   a.meta = reinterpret_cast<int2*>(base + w.meta);
   a.part_ml = reinterpret_cast<Part*>(base + w.ml);
   a.part_o = reinterpret_cast<float*>(base + w.o);
-  if (D == 64) return NT == 1 ? launch<64, 1>(a, st) : launch<64, 2>(a, st);
-  if (D == 128) return NT == 1 ? launch<128, 1>(a, st) : launch<128, 2>(a, st);
-  return launch<256, 1>(a, st);
+  return D == 64 ? run<64>(a, way, st) : D == 128 ? run<128>(a, way, st) : run<256>(a, way, st);
 }

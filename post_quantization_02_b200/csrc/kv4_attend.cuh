@@ -187,6 +187,11 @@ KQ_DEV void store_row(const AttendArgs& a, int row, int hq, int d, float4 o, flo
     a.lse[(int64_t)row * a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
+// kv4_prompt.cu: its rows per tile, keys per block, launch.
+int prompt_rows(int D);
+int prompt_block(int D);
+int launch_prompt(const AttendArgs& a, int D, cudaStream_t st);
+
 // Bounds of what find_unit hands out: a sequence with t tiles and w key blocks
 // has t ceil(w / chunk) <= t + t w / chunk units, and at most twice t w / chunk
 // when it is split.
