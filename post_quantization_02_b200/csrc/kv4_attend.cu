@@ -615,7 +615,8 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
 template <int D>
 __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, int R, int hpb) {
   constexpr int E = D / 32;
-  __shared__ float sum_o[WARPS][D], sum_l[WARPS];
+  __shared__ __align__(16) float sum_o[WARPS][D];
+  __shared__ float sum_l[WARPS];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = blockIdx.x;

@@ -10,14 +10,16 @@
 // then scaled by a power of two.
 //
 // One block = up to 256 rows (two tiles of 128; one at head_dim 256) of one
-// sequence and key/value head, over its keys in steps of BN (128; 64 at head_dim
-// 256).  Warps:
-//   0-3, 4-7  softmax of tile 0, of tile 1: a thread owns a row, reads S 32 columns
-//             at a time and writes P over it, so no reduction crosses lanes
-//   8-11      unpacking: codes of the next step are in registers while this one waits
-//             for its stage; rows of 128 bytes, 128-byte swizzled, for both operands
-//             (keys K-major, values MN-major)
-//   12        issues the MMAs: S of one tile runs beside the softmax of the other
+// sequence and key/value head, over its keys 64 at a time.  Warps:
+//   0-3, 4-7  softmax of tile 0, of tile 1: a thread owns a row, reads its 64 scores and
+//             writes the probabilities over them, so no reduction crosses lanes
+//   8-11      unpacking, 16 tokens of a step each: codes are in registers a step ahead;
+//             rows of 128 bytes, 128-byte swizzled, for both operands (keys K-major,
+//             values MN-major), two stages of each
+//   12        issues the MMAs.  Every tile has two S buffers and S runs two steps ahead
+//             (S of step j + 2 goes over P of step j behind P V of step j), so the softmax
+//             never waits for a product: with 128 keys and one buffer (all of tensor
+//             memory) it did, and a step took twice as long.
 // Dims stay in the order unpacking yields within each 8 (0 4 1 5 2 6 3 7): queries
 // are stored that way and the output is put right when it leaves.
 //
@@ -30,35 +32,52 @@ namespace kv4 {
 namespace {
 
 constexpr int UNPACK_WARP0 = 8, MMA_WARP = 12, THREADS = 416;
-constexpr float NO_MAX = -0x1p100f;     // a whole number; see kv4_attend.cu
+constexpr int BN = 64, TPW = BN / 4;    // keys per step, per unpacking warp
+constexpr float NO_MAX = -0x1p127f;     // a split's maximum where it saw no key
 constexpr float LAG = 8.f;
 
 template <int D>
 struct Shape {
   static constexpr int NT = D == 256 ? 1 : 2;        // tiles of 128 rows
-  static constexpr int BN = D == 256 ? 64 : 128;     // keys per step
   static constexpr int R = 128 * NT;
   static constexpr int ATOMS = D / 64;               // 128-byte columns of an operand row
   static constexpr int Q_BYTES = R * D * 2;
   static constexpr int KV_BYTES = BN * D * 2;        // keys or values of a stage
   static constexpr int STAGE = 2 * KV_BYTES;
-  static constexpr int TPW = BN / 4;                 // tokens per unpacking warp
   static constexpr int CH = D / 32;                  // 16-byte chunks of a token's codes
-  static constexpr int LOADS = TPW * CH / 32;        // chunks per lane (keys; values)
-  static constexpr int S_COLS = D == 256 ? 64 : 128;
-  static constexpr int O_COL = 256;
-  static constexpr int SMEM = Q_BYTES + 2 * STAGE + 1024;
+  static constexpr int TPL = 32 / CH;                // tokens per load of a warp
+  static constexpr int LOADS = TPW / TPL;            // chunks per lane (keys; values)
+  static constexpr int O_COL = 256;                  // tensor memory: S buffers, 64 columns each, then O
+  static constexpr int STAGES = D == 256 ? 2 : 4;    // of keys and values: what fits
+  static constexpr int LG = D == 256 ? 1 : 2;
+  static constexpr int SMEM = Q_BYTES + STAGES * STAGE + 1024;
 };
 
-struct Ctl {
-  uint64_t kv_full[2], kv_empty[2], s_full[2], p_ready[2], scales, pv_done, o_full;
-  float fk[2][128], sv[2][128];          // per key: score factor; value scale x fv
-  uint32_t absent[2][4];                 // bit per key: no page
-  float turn[2], fv[2];                  // fv of the stage over fv of the step before; fv
+// Numbers of a step's keys live in a ring of 8: a step's are written when its keys are
+// unpacked, which is after S of at least two steps before (four with four stages), so after
+// the softmax of four (six) steps before, and up to four steps ahead.
+struct alignas(16) Ctl {                 // (fk and sv are read 16 bytes at a time)
+  float fk[8][BN], sv[8][BN];            // per key: score factor; value scale x fv
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[2][2], p_ready[2][2];  // per tile and buffer
+  uint64_t pv_done[2], scales, o_full;
+  uint32_t absent[8];                    // bit per 16 keys: no page
+  float turn[8], fv[8];                  // fv over fv of the step before; fv
   float sv_warp[2][4];                   // per step's parity and warp: its largest value scale
+  int here_warp[2][4];                   // and whether it has a page
   uint32_t tmem;
   int abort;
 };
+
+// One lane of a converged warp, the same one every time.  The operands of what it issues
+// are computed by the whole warp, so that they live in uniform registers; from one lane's
+// registers each would be moved there first (some 100 cycles per MMA).
+KQ_DEV bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e != 0;
+}
+KQ_DEV uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 KQ_DEV void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -95,6 +114,51 @@ KQ_DEV uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// (volatile: a load stays in front of the waits it is to pass the time of)
+KQ_DEV void load16(uint4& v, const uint4* p) {
+  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+}
+KQ_DEV uint32_t load4(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
+// Two fp32 in one 64-bit register: one instruction for both.
+using f32x2 = unsigned long long;
+KQ_DEV f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+KQ_DEV float2 halves(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+KQ_DEV f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+KQ_DEV f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+KQ_DEV f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+KQ_DEV float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // 8 codes less their zero point, as 8 halves in the order 0 4 1 5 2 6 3 7.
 // z1: 1024 + z in both halves, z2: -(64 + z); exact: 1024 + c and 1024 + 16 c are.
 KQ_DEV uint4 codes_f16(uint32_t w, uint32_t z1, uint32_t z2) {
@@ -128,7 +192,7 @@ KQ_DEV uint4 codes_bf16(uint32_t w, uint32_t z1) {
 template <int D, bool BF>
 __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs a) {
   using SH = Shape<D>;
-  constexpr int NT = SH::NT, BN = SH::BN, R = SH::R, ATOMS = SH::ATOMS;
+  constexpr int NT = SH::NT, R = SH::R, ATOMS = SH::ATOMS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl ctl;
   uint8_t* q_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -160,15 +224,22 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
   auto key_of = [&](int i) { return (i < sp.sb ? i : sp.lb + i - sp.sb) * BN; };   // first key of block i
 
   volatile int* abort = &ctl.abort;
+  constexpr int STAGES = SH::STAGES, LG = SH::LG, SM = STAGES - 1;    // stage of step j: j & SM, its phase j >> LG
   if (threadIdx.x == 0) {
+    for (int i = 0; i < SH::STAGES; ++i) {
+      kq::mbar_init(&ctl.k_full[i], 4);
+      kq::mbar_init(&ctl.k_empty[i], 1);
+      kq::mbar_init(&ctl.v_full[i], 4);
+      kq::mbar_init(&ctl.v_empty[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
-      kq::mbar_init(&ctl.kv_full[i], 4);
-      kq::mbar_init(&ctl.kv_empty[i], 1);
-      kq::mbar_init(&ctl.s_full[i], 1);
-      kq::mbar_init(&ctl.p_ready[i], 4);
+      for (int k = 0; k < 2; ++k) {
+        kq::mbar_init(&ctl.s_full[i][k], 2);   // S itself, and that its keys' numbers are there
+        kq::mbar_init(&ctl.p_ready[i][k], 4);
+      }
+      kq::mbar_init(&ctl.pv_done[i], 1);
     }
     kq::mbar_init(&ctl.scales, 4);
-    kq::mbar_init(&ctl.pv_done, 1);
     kq::mbar_init(&ctl.o_full, 1);
     ctl.abort = 0;
     kq::fence_barrier_init();
@@ -203,142 +274,164 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
   kq::tc_fence_after();
   const uint32_t tmem = ctl.tmem;
 
+  // a wait of the whole warp: all lanes agree on its outcome
+  auto wait = [&](uint64_t* bar, int parity) -> bool {
+    return __all_sync(0xffffffffu, kq::mbar_wait(bar, (uint32_t)parity & 1u, abort, a.info));
+  };
+
   if (warp == MMA_WARP) {
-    // ------------------------------------------------------------- MMAs
-    if (lane == 0 && steps > 0) {
-      constexpr uint32_t idesc_qk = kq::idesc_f16(128, BN, BF ? 1 : 0, 0, 0);
-      constexpr uint32_t idesc_pv = kq::idesc_f16(128, D, 0, 0, 1);
-      const uint32_t qa = kq::smem_u32(q_smem), kv = kq::smem_u32(kv_smem);
-      auto issue_s = [&](int tile, int buf, int j) {
-        const uint32_t ka = kv + (j & 1) * SH::STAGE;
+    // -------------------------------------------------------------- MMAs
+    const uint32_t tm = uniform(tmem), qa = uniform(kq::smem_u32(q_smem)), kv = uniform(kq::smem_u32(kv_smem));
+    auto issue_s = [&](int tile, int j) {
+      constexpr uint32_t idesc = kq::idesc_f16(128, BN, BF ? 1 : 0, 0, 0);
+      const uint32_t d = tm + (2 * tile + (j & 1)) * BN;
+      const uint64_t qd = kq::smem_desc(qa + tile * (ATOMS * 16384), 16, 1024, kq::kLayoutSwizzle128B);
+      const uint64_t kd = kq::smem_desc(kv + (j & SM) * SH::STAGE, 16, 1024, kq::kLayoutSwizzle128B);
 #pragma unroll
-        for (int at = 0; at < ATOMS; ++at)
+      for (int at = 0; at < ATOMS; ++at)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            kq::mma_f16(tmem + buf * SH::S_COLS,
-                        kq::smem_desc(qa + (tile * ATOMS + at) * 16384 + kk * 32, 16, 1024, kq::kLayoutSwizzle128B),
-                        kq::smem_desc(ka + at * (BN * 128) + kk * 32, 16, 1024, kq::kLayoutSwizzle128B), idesc_qk,
+        for (int kk = 0; kk < 4; ++kk)
+          if (elect_one())
+            kq::mma_f16(d, qd + ((at * 16384 + kk * 32) >> 4), kd + ((at * (BN * 128) + kk * 32) >> 4), idesc,
                         at || kk);
-        kq::mma_commit(&ctl.s_full[buf]);
-      };
-      auto issue_pv = [&](int tile, int buf, int j) {
-        const uint32_t va = kv + (j & 1) * SH::STAGE + SH::KV_BYTES;
+      if (elect_one()) {
+        if (tile == tiles - 1) kq::mma_commit(&ctl.k_empty[j & SM]);
+        kq::mma_commit(&ctl.s_full[tile][j & 1]);
+        kq::mbar_arrive(&ctl.s_full[tile][j & 1]);
+      }
+    };
+    auto issue_pv = [&](int tile, int j) {
+      constexpr uint32_t idesc = kq::idesc_f16(128, D, 0, 0, 1);
+      const uint32_t d = tm + SH::O_COL + tile * D, p = tm + (2 * tile + (j & 1)) * BN;
+      const uint64_t vd =
+          kq::smem_desc(kv + (j & SM) * SH::STAGE + SH::KV_BYTES, BN * 128, 1024, kq::kLayoutSwizzle128B);
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          mma_f16_ts(tmem + SH::O_COL + tile * D, tmem + buf * SH::S_COLS + kk * 8,
-                     kq::smem_desc(va + kk * 2048, BN * 128, 1024, kq::kLayoutSwizzle128B), idesc_pv,
-                     j > 0 || kk > 0);
-      };
-      bool ok = kq::mbar_wait(&ctl.kv_full[0], 0, abort, a.info);
-      if (ok) {
-        kq::tc_fence_after();
-        for (int i = 0; i < (NT == 2 ? tiles : 1); ++i) issue_s(i, i, 0);
+      for (int kk = 0; kk < BN / 16; ++kk)
+        if (elect_one()) mma_f16_ts(d, p + kk * 8, vd + ((kk * 2048) >> 4), idesc, kk > 0 || j > 0);
+      if (elect_one()) {
+        if (tile == tiles - 1) kq::mma_commit(&ctl.v_empty[j & SM]);
+        kq::mma_commit(&ctl.pv_done[tile]);
       }
-      for (int j = 0; j < steps && ok; ++j) {
-        const bool more = j + 1 < steps;
-        if (more) {
-          ok = kq::mbar_wait(&ctl.kv_full[(j + 1) & 1], ((j + 1) >> 1) & 1, abort, a.info);
-          if (!ok) break;
-          kq::tc_fence_after();
-        }
-        if (NT == 2) {
-          for (int i = 0; i < tiles && ok; ++i) {
-            ok = kq::mbar_wait(&ctl.p_ready[i], j & 1, abort, a.info);
-            if (!ok) break;
-            kq::tc_fence_after();
-            issue_pv(i, i, j);
-            if (i == tiles - 1) kq::mma_commit(&ctl.kv_empty[j & 1]);
-            // (over P, in issue order behind the MMAs that read it)
-            if (more) issue_s(i, i, j + 1);
-          }
-        } else {
-          if (more) issue_s(0, (j + 1) & 1, j + 1);
-          ok = kq::mbar_wait(&ctl.p_ready[j & 1], (j >> 1) & 1, abort, a.info);
-          if (!ok) break;
-          kq::tc_fence_after();
-          issue_pv(0, j & 1, j);
-          kq::mma_commit(&ctl.kv_empty[j & 1]);
-          kq::mma_commit(&ctl.pv_done);
-        }
-      }
-      // (also after a wait that gave up: nothing is in flight when the block ends)
-      kq::mma_commit(&ctl.o_full);
-      volatile int none = 0;
-      kq::mbar_wait(&ctl.o_full, 0, &none, a.info);
+    };
+    bool ok = true;
+    for (int j = 0; j < min(steps, 2) && ok; ++j) {
+      ok = wait(&ctl.k_full[j], 0);
+      if (!ok) break;
+      kq::tc_fence_after();
+      for (int i = 0; i < tiles; ++i) issue_s(i, j);
     }
+    for (int j = 0; j < steps && ok; ++j) {
+      ok = wait(&ctl.v_full[j & SM], j >> LG);
+      for (int i = 0; i < tiles && ok; ++i) {
+        ok = wait(&ctl.p_ready[i][j & 1], j >> 1);
+        if (!ok) break;
+        kq::tc_fence_after();
+        issue_pv(i, j);
+      }
+      if (ok && j + 2 < steps) {
+        ok = wait(&ctl.k_full[(j + 2) & SM], (j + 2) >> LG);
+        if (!ok) break;
+        kq::tc_fence_after();
+        // (over P, in issue order behind the MMAs that read it)
+        for (int i = 0; i < tiles; ++i) issue_s(i, j + 2);
+      }
+    }
+    // (also after a wait that gave up: nothing is in flight when the block ends)
+    if (elect_one()) kq::mma_commit(&ctl.o_full);
+    __syncwarp();
+    volatile int none = 0;
+    kq::mbar_wait(&ctl.o_full, 0, &none, a.info);
     __syncwarp();
   } else if (warp >= UNPACK_WARP0) {
     // -------------------------------------------------------- unpacking
     const int w = warp - UNPACK_WARP0;
     const int any_lo = lo_of(q_first), any_hi = hi_of(q_last);
-    const int c = lane % SH::CH, ct = lane / SH::CH;        // chunk, token within a load
-    constexpr int TPL = 32 / SH::CH;                        // tokens per load
-    const int at = c >> 1;
-    const int x = D == 256 ? at : D == 128 ? 2 * at : 0;    // order in which words are stored
-    uint4 kreg[SH::LOADS], vreg[SH::LOADS];
-    uint32_t kword = 0, vword = 0;                          // of token TPW w + lane
-    bool here = false;
-    auto load = [&](int j) {
-      const int tok0 = key_of(i0 + j) + SH::TPW * w;
-      const int tl = tok0 + (lane & (SH::TPW - 1));
-      int64_t page = -1;
-      if (tl < any_hi && (tl >= any_lo || tl < a.sinks)) {
-        page = a.b.table[u.b * a.b.table_ld + (tl >> a.cache.lgP)];
-        if (page < 0 || page >= a.cache.pages) {
-          kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
-          page = -1;
-        }
-      }
-      const int P = a.cache.P;
-      const uint8_t* blk = a.cache.base + (page * a.cache.heads + head) * (int64_t)a.cache.block_bytes;
-      here = page >= 0;
-      kword = vword = 0;
-      if (here) {
-        const uint32_t* wp = reinterpret_cast<const uint32_t*>(blk + P * D) + (tl & (P - 1));
-        kword = __ldg(wp);
-        vword = __ldg(wp + P);
-      }
-      const uint32_t seen = __ballot_sync(0xffffffffu, here);
-      // the base address of this token's codes
-      const uint64_t codes = here ? (uint64_t)(blk + (tl & (P - 1)) * (D / 2)) : 0;
-#pragma unroll
-      for (int i = 0; i < SH::LOADS; ++i) {
-        const int tk = i * TPL + ct;
-        const uint64_t p = __shfl_sync(0xffffffffu, codes, tk);
-        kreg[i] = vreg[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (p) {
-          const uint8_t* kp = reinterpret_cast<const uint8_t*>(p) + 16 * c;
-          asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(kreg[i].x), "=r"(kreg[i].y), "=r"(kreg[i].z), "=r"(kreg[i].w)
-                       : "l"(kp));
-          asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(vreg[i].x), "=r"(vreg[i].y), "=r"(vreg[i].z), "=r"(vreg[i].w)
-                       : "l"(kp + (int64_t)P * (D / 2)));
-        }
-      }
-      return seen;
+    constexpr int TPL = SH::TPL;
+    // Lane to (16-byte chunk, token of the load): the 8 lanes of a phase write the two
+    // halves of one 128-byte line of 4 tokens, on 8 different chunks of banks.
+    const int c = (lane & 1) | (((lane >> 3) & (SH::CH / 2 - 1)) << 1);
+    const int ct = ((lane >> 1) & 3) | ((lane / (4 * SH::CH)) << 2);
+    constexpr int NOT_SEEN = INT32_MIN;       // (a table entry of this value is taken for keys not seen)
+    struct Codes {
+      uint4 k[SH::LOADS], v[SH::LOADS];
+      uint32_t kword, vword;                  // of token lane % 16
+      bool here;                              // the 16 tokens have a page (they lie in one)
     };
-    uint32_t seen = 0;
-    if (steps > 0) seen = load(0);
+    // A step's page number is asked for two steps ahead, its codes one step ahead: both
+    // latencies pass while earlier steps are unpacked.
+    auto page_of_step = [&](int j) -> int {
+      const int t0 = key_of(i0 + j) + TPW * w;
+      if (j >= steps || !(t0 < any_hi && (t0 + TPW > any_lo || t0 < a.sinks))) return NOT_SEEN;
+      return (int)load4(reinterpret_cast<const uint32_t*>(a.b.table + u.b * a.b.table_ld + (t0 >> a.cache.lgP)));
+    };
+    auto load = [&](Codes& q, int j, int page) {
+      q.here = page >= 0 && page < a.cache.pages;
+      if (!q.here && page != NOT_SEEN) kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
+      const int P = a.cache.P, t0 = key_of(i0 + j) + TPW * w, slot = t0 & (P - 1);
+      const uint8_t* blk = a.cache.base + ((int64_t)page * a.cache.heads + head) * (int64_t)a.cache.block_bytes;
+      q.kword = q.vword = 0;
+      if (q.here) {
+        const uint4* kp = reinterpret_cast<const uint4*>(blk + (slot + ct) * (D / 2)) + c;
+#pragma unroll
+        for (int i = 0; i < SH::LOADS; ++i) {
+          load16(q.k[i], kp + i * (TPL * SH::CH));
+          load16(q.v[i], kp + i * (TPL * SH::CH) + P * SH::CH);
+        }
+        // what no row sees may be memory that was never written: its scales count as 0
+        const int t = t0 + (lane & (TPW - 1));
+        if (t < any_hi && (t >= any_lo || t < a.sinks)) {
+          const uint32_t* wp = reinterpret_cast<const uint32_t*>(blk + P * D) + (t & (P - 1));
+          q.kword = load4(wp);
+          q.vword = load4(wp + P);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < SH::LOADS; ++i) q.k[i] = q.v[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    // where word k of load i goes: (at ^ 16 k) + i (128 TPL), swizzled by the token
+    const uint32_t at = kq::smem_u32(kv_smem) + (c >> 1) * (BN * 128) + (TPW * w + ct) * 128 +
+                        (((4 * (c & 1)) ^ (ct & 7)) << 4);
+    static_assert(TPL % 8 == 0 || TPL == 4, "the swizzle of a load's tokens");
+    auto put = [&](uint32_t base, int i, int k, uint4 v) {
+      // (with 4 tokens to a load, every other load's tokens are 4 .. 7 of a line of 8)
+      const uint32_t p = ((base ^ (16u * k)) ^ (TPL == 4 && (i & 1) ? 64u : 0u)) + i * (128 * TPL);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                   : "memory");
+    };
+    auto announce = [&](const Codes& q, int j) {            // this warp's largest value scale
+      // (scales are not negative: their bits are in the numbers' order; a NaN counts as 0)
+      const uint32_t bits = q.vword & ~15u;
+      const uint32_t big = __reduce_max_sync(0xffffffffu, bits > 0x7f800000u ? 0u : bits);
+      if (lane == 0) {
+        ctl.sv_warp[j & 1][w] = __uint_as_float(big);
+        ctl.here_warp[j & 1][w] = q.here;
+        kq::mbar_arrive(&ctl.scales);
+      }
+    };
+    Codes cur, nxt;
+    int page = page_of_step(0);
+    if (steps > 0) {
+      load(nxt, 0, page);
+      announce(nxt, 0);
+    }
+    page = page_of_step(1);
     float fv = 0.f;
     bool ok = true;
     for (int j = 0; j < steps; ++j) {
-      const int st = j & 1;
-      if (j >= 2) {
-        ok = kq::mbar_wait(&ctl.kv_empty[st], ((j >> 1) + 1) & 1, abort, a.info);
-        if (!__all_sync(0xffffffffu, ok)) break;
+      const int st = j & SM, ring = j & 7;
+      cur = nxt;
+      if (j + 1 < steps) {
+        load(nxt, j + 1, page);
+        page = page_of_step(j + 2);
       }
+      // ---- keys, and the numbers of this step
+      if (j >= STAGES) ok = wait(&ctl.k_empty[st], (j >> LG) + 1);
+      ok = ok && wait(&ctl.scales, j);
+      if (!ok) break;
       // fv: a power of two that keeps value scales below 2^6 (see kv4_attend.cu)
-      float sv = word_scale(vword), big = sv;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-      if (lane == 0) {
-        ctl.sv_warp[st][w] = big;
-        kq::mbar_arrive(&ctl.scales);
-      }
-      ok = kq::mbar_wait(&ctl.scales, j & 1, abort, a.info);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      big = fmaxf(fmaxf(ctl.sv_warp[st][0], ctl.sv_warp[st][1]), fmaxf(ctl.sv_warp[st][2], ctl.sv_warp[st][3]));
+      const float big =
+          fmaxf(fmaxf(ctl.sv_warp[j & 1][0], ctl.sv_warp[j & 1][1]), fmaxf(ctl.sv_warp[j & 1][2], ctl.sv_warp[j & 1][3]));
       float turn = 1.f;
       if (big > 0.f && (fv == 0.f || big * fv > 64.f)) {
         const int e = min(max(127 - (int)(__float_as_uint(big) >> 23), -100), 100);
@@ -346,60 +439,50 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         if (fv != 0.f) turn = nf / fv;
         fv = nf;
       }
-      if (lane < SH::TPW) {
-        ctl.fk[st][SH::TPW * w + lane] = word_scale(kword) * a.scale_log2;
-        ctl.sv[st][SH::TPW * w + lane] = sv * fv;
-      }
-      if (lane == 0) {
-        if (SH::TPW == 32)
-          ctl.absent[st][w] = ~seen;
-        else
-          reinterpret_cast<uint16_t*>(ctl.absent[st])[w] = (uint16_t)~seen;
+      if (lane < TPW) {
+        ctl.fk[ring][TPW * w + lane] = word_scale(cur.kword) * a.scale_log2;
+        ctl.sv[ring][TPW * w + lane] = word_scale(cur.vword) * fv;
       }
       if (w == 0 && lane == 0) {
-        ctl.turn[st] = turn;
-        ctl.fv[st] = fv;
+        uint32_t gone = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) gone |= (ctl.here_warp[j & 1][i] ? 0u : 1u) << i;
+        ctl.absent[ring] = gone;
+        ctl.turn[ring] = turn;
+        ctl.fv[ring] = fv;
       }
-      const uint32_t kz = kword & 15u, vz = vword & 15u;
-      uint8_t* kd = kv_smem + st * SH::STAGE + at * (BN * 128);
+      const uint32_t kd = at + st * SH::STAGE, vd = kd + SH::KV_BYTES;
+      uint32_t zeros[SH::LOADS];               // of the tokens this lane unpacks
+#pragma unroll
+      for (int i = 0; i < SH::LOADS; ++i)
+        zeros[i] = __shfl_sync(0xffffffffu, (cur.kword & 15u) | ((cur.vword & 15u) << 4), i * TPL + ct);
 #pragma unroll
       for (int i = 0; i < SH::LOADS; ++i) {
-        const int tk = i * TPL + ct, row = SH::TPW * w + tk;
-        const uint32_t z = __shfl_sync(0xffffffffu, kz, tk), zv = __shfl_sync(0xffffffffu, vz, tk);
+        const uint32_t z = zeros[i] & 15u;
         const uint32_t z1 = (BF ? 0x43004300u : 0x64006400u) + z * 0x00010001u;
         const uint32_t z2 = 0xd400d400u + z * 0x00100010u;
-        const uint32_t y1 = 0x64006400u + zv * 0x00010001u, y2 = 0xd400d400u + zv * 0x00100010u;
-        uint32_t kw[4] = {kreg[i].x, kreg[i].y, kreg[i].z, kreg[i].w};
-        uint32_t vw[4] = {vreg[i].x, vreg[i].y, vreg[i].z, vreg[i].w};
-        auto swap = [](uint32_t& p, uint32_t& q, bool yes) {
-          const uint32_t t = p;
-          p = yes ? q : p;
-          q = yes ? t : q;
-        };
-        if (D >= 128) {
-          // lanes of a phase that write the same lines start with other words
-          swap(kw[0], kw[2], x & 2);
-          swap(kw[1], kw[3], x & 2);
-          swap(vw[0], vw[2], x & 2);
-          swap(vw[1], vw[3], x & 2);
-        }
-        if (D == 256) {
-          swap(kw[0], kw[1], x & 1);
-          swap(kw[2], kw[3], x & 1);
-          swap(vw[0], vw[1], x & 1);
-          swap(vw[2], vw[3], x & 1);
-        }
+        const uint32_t kw[4] = {cur.k[i].x, cur.k[i].y, cur.k[i].z, cur.k[i].w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint8_t* d = kd + row * 128 + (((4 * (c & 1) + (k ^ x)) ^ (row & 7)) << 4);
-          *reinterpret_cast<uint4*>(d) = BF ? codes_bf16(kw[k], z1) : codes_f16(kw[k], z1, z2);
-          *reinterpret_cast<uint4*>(d + SH::KV_BYTES) = codes_f16(vw[k], y1, y2);
-        }
+        for (int k = 0; k < 4; ++k) put(kd, i, k, BF ? codes_bf16(kw[k], z1) : codes_f16(kw[k], z1, z2));
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) kq::mbar_arrive(&ctl.kv_full[st]);
-      if (j + 1 < steps) seen = load(j + 1);
+      if (lane == 0) kq::mbar_arrive(&ctl.k_full[st]);
+      // ---- values
+      if (j >= STAGES) ok = wait(&ctl.v_empty[st], (j >> LG) + 1);
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < SH::LOADS; ++i) {
+        const uint32_t z = zeros[i] >> 4;
+        const uint32_t z1 = 0x64006400u + z * 0x00010001u, z2 = 0xd400d400u + z * 0x00100010u;
+        const uint32_t vw[4] = {cur.v[i].x, cur.v[i].y, cur.v[i].z, cur.v[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) put(vd, i, k, codes_f16(vw[k], z1, z2));
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) kq::mbar_arrive(&ctl.v_full[st]);
+      if (j + 1 < steps) announce(nxt, j + 1);
     }
   } else if (warp < 4 * tiles || (NT == 1 && warp < 4)) {
     // ---------------------------------------------------------- softmax
@@ -412,126 +495,117 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     const int lo = lo_of(qi), hi = hi_of(qi);
     // what all rows of the warp see (rows are in order)
     const int all_lo = lo_of(__shfl_sync(0xffffffffu, qi, 31)), all_hi = hi_of(__shfl_sync(0xffffffffu, qi, 0));
-    float m = NO_MAX, l = 0.f;
+    // the running maximum, a whole number, and how far scores may pass it; 0 and -infinity's
+    // neighbour until the row has seen a key
+    float m = 0.f, lag = -0x1.fffffep127f;
+    f32x2 l2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
     bool ok = true;
     auto step = [&](auto is_masked, int j, int key0) {
       constexpr bool masked = decltype(is_masked)::value;
-      const int st = j & 1, buf = NT == 2 ? tile : j & 1;
-      const uint32_t s_at = tbase + buf * SH::S_COLS;
-      float turn = ctl.turn[st];
-#pragma unroll 1
-      for (int ch = 0; ch < BN / 32; ++ch) {
+      const int st = j & 7;
+      const uint32_t s_at = tbase + (2 * tile + (j & 1)) * BN;
+      const float turn = ctl.turn[st];
+      const uint32_t gone = masked ? ctl.absent[st] : 0u;
+      f32x2 t[BN / 2];             // scores relative to the running maximum
+      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      const f32x2 neg_m = pair(-m, -m);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
         float x[32];
-        kq::tmem_ld32(s_at + 32 * ch, x);
-        const float4* fk4 = reinterpret_cast<const float4*>(&ctl.fk[st][32 * ch]);
-        const float4* sv4 = reinterpret_cast<const float4*>(&ctl.sv[st][32 * ch]);
-        const uint32_t gone = masked ? ctl.absent[st][ch] : 0u;
+        kq::tmem_ld32(s_at + 32 * h, x);
         kq::tmem_wait_ld();
-        float top = -INFINITY;
+        const ulonglong2* fk = reinterpret_cast<const ulonglong2*>(&ctl.fk[st][32 * h]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float4 f = fk4[i];
-          x[4 * i] *= f.x;
-          x[4 * i + 1] *= f.y;
-          x[4 * i + 2] *= f.z;
-          x[4 * i + 3] *= f.w;
-          if constexpr (masked) {
+          const ulonglong2 f = fk[i];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int key = key0 + 32 * ch + 4 * i + k;
-              const bool seen = !((gone >> (4 * i + k)) & 1u) && key < hi && (key >= lo || key < a.sinks);
-              if (!seen) x[4 * i + k] = -INFINITY;
+          for (int k = 0; k < 2; ++k) {
+            const int e = 4 * i + 2 * k;
+            f32x2& tc = t[16 * h + 2 * i + k];
+            tc = fma2(pair(x[e], x[e + 1]), k ? f.y : f.x, neg_m);
+            float2 v = halves(tc);
+            if constexpr (masked) {
+              const int key = key0 + 32 * h + e;
+              const bool page = !((gone >> (2 * h + (e >> 4))) & 1u);
+              if (!(page && key < hi && (key >= lo || key < a.sinks))) v.x = -INFINITY;
+              if (!(page && key + 1 < hi && (key + 1 >= lo || key + 1 < a.sinks))) v.y = -INFINITY;
+              tc = pair(v.x, v.y);
             }
+            top[i & 3] = max3(top[i & 3], v.x, v.y);
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) top = fmaxf(top, x[4 * i + k]);
         }
-        const bool up = top > m + LAG;
-        if (__any_sync(0xffffffffu, up || turn != 1.f)) {
-          // the maximum moves to the next whole number: sums and the probabilities of
-          // this step's earlier columns turn by a power of two
-          const float nm = up ? (top < INFINITY ? ceilf(top) : top) : m;
-          const float al = nm == m ? 1.f : exp2_approx(m - nm);
-          m = nm;
-          l *= al;
-          if (j > 0) {
-            if (NT == 1) ok = kq::mbar_wait(&ctl.pv_done, (j - 1) & 1, abort, a.info) && ok;
-            __syncwarp();
-            kq::tc_fence_after();
-            const float f = al * turn;
-#pragma unroll 1
-            for (int d = 0; d < D; d += 16) {
-              uint32_t o[16];
-              tmem_ld16(o_at + d, o);
-              kq::tmem_wait_ld();
+      }
+      const float high = max3(max3(top[0], top[1], top[2]), top[3], top[3]);
+      if (__any_sync(0xffffffffu, high > lag || turn != 1.f)) {
+        // the maximum moves by a whole number; what was summed before turns by a power of two
+        const bool up = high > lag;
+        const float by = up ? (high < INFINITY ? ceilf(high) : high) : 0.f;
+        const float al = up && lag == LAG ? exp2_approx(-by) : 1.f;
+        if (up) lag = LAG;
+        m += by;
+        const f32x2 down = pair(-by, -by), al2 = pair(al, al);
+        l2[0] = mul2(l2[0], al2);
+        l2[1] = mul2(l2[1], al2);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st16(o_at + d, o);
-            }
-          }
-          turn = 1.f;
-          kq::tmem_wait_st();
-          const __half2 ah = __float2half2_rn(al);
+        for (int k = 0; k < BN / 2; ++k) t[k] = add2(t[k], down);
+        if (j > 0) {
+          ok = wait(&ctl.pv_done[tile], j - 1) && ok;
+          kq::tc_fence_after();
+          const float f = al * turn;
 #pragma unroll 1
-          for (int d = 0; d < 16 * ch; d += 16) {
-            uint32_t p[16];
-            tmem_ld16(s_at + d, p);
+          for (int d = 0; d < D; d += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_at + d, o);
             kq::tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&p[k]), ah);
-              p[k] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            tmem_st16(s_at + d, p);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st16(o_at + d, o);
           }
         }
+      }
+      const ulonglong2* sv = reinterpret_cast<const ulonglong2*>(ctl.sv[st]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
         uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float4 sv = sv4[i];
-          const float p0 = exp2_approx(x[4 * i] - m), p1 = exp2_approx(x[4 * i + 1] - m);
-          const float p2 = exp2_approx(x[4 * i + 2] - m), p3 = exp2_approx(x[4 * i + 3] - m);
-          l += (p0 + p1) + (p2 + p3);
-          float v0 = p0 * sv.x, v1 = p1 * sv.y, v2 = p2 * sv.z, v3 = p3 * sv.w;
-          if constexpr (masked) {                       // (0 times a NaN scale)
-            if (x[4 * i] == -INFINITY) v0 = 0.f;
-            if (x[4 * i + 1] == -INFINITY) v1 = 0.f;
-            if (x[4 * i + 2] == -INFINITY) v2 = 0.f;
-            if (x[4 * i + 3] == -INFINITY) v3 = 0.f;
+          const ulonglong2 f = sv[8 * h + i];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 v = halves(t[16 * h + 2 * i + k]);
+            const f32x2 p = pair(exp2_approx(v.x), exp2_approx(v.y));
+            l2[k] = add2(l2[k], p);
+            float2 w = halves(mul2(p, k ? f.y : f.x));
+            if constexpr (masked) {                     // (0 times a NaN scale)
+              if (v.x == -INFINITY) w.x = 0.f;
+              if (v.y == -INFINITY) w.y = 0.f;
+            }
+            pk[2 * i + k] = pack_half2(w.x, w.y);
           }
-          pk[2 * i] = pack_half2(v0, v1);
-          pk[2 * i + 1] = pack_half2(v2, v3);
         }
-        tmem_st16(s_at + 16 * ch, pk);
+        tmem_st16(s_at + 16 * h, pk);
       }
     };
     for (int j = 0; j < steps; ++j) {
-      const int st = j & 1, buf = NT == 2 ? tile : j & 1;
-      ok = kq::mbar_wait(&ctl.kv_full[st], (j >> 1) & 1, abort, a.info) && ok;
-      ok = ok && kq::mbar_wait(&ctl.s_full[buf], NT == 2 ? j & 1 : (j >> 1) & 1, abort, a.info);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
+      ok = ok && wait(&ctl.s_full[tile][j & 1], j >> 1);
+      if (!ok) break;
       kq::tc_fence_after();
       const int key0 = key_of(i0 + j);
-      uint32_t gone = 0;
-#pragma unroll
-      for (int i = 0; i < BN / 32; ++i) gone |= ctl.absent[st][i];
-      if (gone || !(key0 + BN <= all_hi && (key0 >= all_lo || key0 + BN <= a.sinks)))
+      if (ctl.absent[j & 7] || !(key0 + BN <= all_hi && (key0 >= all_lo || key0 + BN <= a.sinks)))
         step(std::true_type{}, j, key0);
       else
         step(std::false_type{}, j, key0);
       kq::tmem_wait_st();
       kq::tc_fence_before();
       __syncwarp();
-      if (lane == 0) kq::mbar_arrive(&ctl.p_ready[buf]);
+      if (lane == 0) kq::mbar_arrive(&ctl.p_ready[tile][j & 1]);
     }
     // ---- output
-    if (steps > 0) ok = ok && kq::mbar_wait(&ctl.o_full, 0, abort, a.info);
-    ok = __all_sync(0xffffffffu, ok);
+    const float2 ls = halves(add2(l2[0], l2[1]));
+    const float l = ls.x + ls.y;
+    if (steps > 0) ok = ok && wait(&ctl.o_full, 0);
     kq::tc_fence_after();
-    const float rfv = steps > 0 && ctl.fv[(steps - 1) & 1] != 0.f ? 1.f / ctl.fv[(steps - 1) & 1] : 0.f;
+    const float rfv = steps > 0 && ctl.fv[(steps - 1) & 7] != 0.f ? 1.f / ctl.fv[(steps - 1) & 7] : 0.f;
     const int rr = 128 * tile + tr;
     const bool mine = r0 + rr < rows;
     const int64_t slot = ((int64_t)(u.slot0 + (int)blockIdx.x - u.base) * a.cache.heads + head) * R + rr;
@@ -556,7 +630,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
                                        __uint_as_float(o[b + 4]) * rfv, __uint_as_float(o[b + 6]) * rfv);
           if (u.nsplit > 1) {
             *reinterpret_cast<float4*>(a.part_o + slot * D + d + k) = v;
-            if (d + k == 0) a.part_ml[slot] = {m, l};
+            if (d + k == 0) a.part_ml[slot] = {lag == LAG ? m : NO_MAX, l};
           } else {
             store_row(a, s.row0 + qi, hq, d + k, v, m, l);
           }
@@ -589,7 +663,7 @@ int launch(const AttendArgs& a, cudaStream_t st) {
 }  // namespace
 
 int prompt_rows(int D) { return D == 256 ? Shape<256>::R : Shape<128>::R; }
-int prompt_block(int D) { return D == 256 ? Shape<256>::BN : Shape<128>::BN; }
+int prompt_block(int D) { return BN; }
 
 int launch_prompt(const AttendArgs& a, int D, cudaStream_t st) {
   if (D == 64) return a.dt == BF16 ? launch<64, true>(a, st) : launch<64, false>(a, st);
