@@ -13,13 +13,15 @@
 // sequence and key/value head, over its keys 64 at a time.  Warps:
 //   0-3, 4-7  softmax of tile 0, of tile 1: a thread owns a row, reads its 64 scores and
 //             writes the probabilities over them, so no reduction crosses lanes
-//   8-11      unpacking, 16 tokens of a step each: codes are in registers a step ahead;
-//             rows of 128 bytes, 128-byte swizzled, for both operands (keys K-major,
-//             values MN-major), two stages of each
-//   12        issues the MMAs.  Every tile has two S buffers and S runs two steps ahead
+//   8         issues the MMAs.  Every tile has two S buffers and S runs two steps ahead
 //             (S of step j + 2 goes over P of step j behind P V of step j), so the softmax
 //             never waits for a product: with 128 keys and one buffer (all of tensor
 //             memory) it did, and a step took twice as long.
+//   9         numbers: looks up the pages, turns the keys' words into factors, up to 8
+//             steps ahead
+//   10-15     unpacking: 16 tokens' keys or values at a time, in turn (eight such jobs to
+//             a step), the next one's codes on their way; rows of 128 bytes, 128-byte
+//             swizzled, for both operands (keys K-major, values MN-major)
 // Dims stay in the order unpacking yields within each 8 (0 4 1 5 2 6 3 7): queries
 // are stored that way and the output is put right when it leaves.
 //
@@ -31,8 +33,8 @@
 namespace kv4 {
 namespace {
 
-constexpr int UNPACK_WARP0 = 8, MMA_WARP = 12, THREADS = 416;
-constexpr int BN = 64, TPW = BN / 4;    // keys per step, per unpacking warp
+constexpr int MMA_WARP = 8, NUM_WARP = 9, UNPACK_WARP0 = 10, UNPACKERS = 6, THREADS = 512;
+constexpr int BN = 64, GROUP = 16, GROUPS = BN / GROUP;    // keys per step, per unpacking job
 constexpr float NO_MAX = -0x1p127f;     // a split's maximum where it saw no key
 constexpr float LAG = 8.f;
 
@@ -46,25 +48,28 @@ struct Shape {
   static constexpr int STAGE = 2 * KV_BYTES;
   static constexpr int CH = D / 32;                  // 16-byte chunks of a token's codes
   static constexpr int TPL = 32 / CH;                // tokens per load of a warp
-  static constexpr int LOADS = TPW / TPL;            // chunks per lane (keys; values)
+  static constexpr int LOADS = GROUP / TPL;          // chunks per lane
   static constexpr int O_COL = 256;                  // tensor memory: S buffers, 64 columns each, then O
   static constexpr int STAGES = D == 256 ? 2 : 4;    // of keys and values: what fits
   static constexpr int LG = D == 256 ? 1 : 2;
   static constexpr int SMEM = Q_BYTES + STAGES * STAGE + 1024;
 };
 
-// Numbers of a step's keys live in a ring of 8: a step's are written when its keys are
-// unpacked, which is after S of at least two steps before (four with four stages), so after
-// the softmax of four (six) steps before, and up to four steps ahead.
-struct alignas(16) Ctl {                 // (fk and sv are read 16 bytes at a time)
-  float fk[8][BN], sv[8][BN];            // per key: score factor; value scale x fv
+// What the other warps need to know of a step's keys.
+struct alignas(16) Numbers {
+  float fk[BN], sv[BN];      // score factor; value scale x fv
+  uint8_t zeros[BN];         // key's zero point | value's << 4
+  uint64_t codes[GROUPS];    // address of the group's first key's codes, 0: no page
+  uint32_t absent;           // bit per group: no page
+  float turn, fv;            // fv over fv of the step before; fv
+};
+
+struct alignas(16) Ctl {
+  Numbers num[8];            // step j: num[j & 7]
+  uint64_t num_full[8], num_free[8];
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2][2], p_ready[2][2];  // per tile and buffer
-  uint64_t pv_done[2], scales, o_full;
-  uint32_t absent[8];                    // bit per 16 keys: no page
-  float turn[8], fv[8];                  // fv over fv of the step before; fv
-  float sv_warp[2][4];                   // per step's parity and warp: its largest value scale
-  int here_warp[2][4];                   // and whether it has a page
+  uint64_t pv_done[2], o_full;
   uint32_t tmem;
   int abort;
 };
@@ -239,7 +244,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       }
       kq::mbar_init(&ctl.pv_done[i], 1);
     }
-    kq::mbar_init(&ctl.scales, 4);
+    for (int i = 0; i < 8; ++i) {
+      kq::mbar_init(&ctl.num_full[i], 1);
+      kq::mbar_init(&ctl.num_free[i], 4 * tiles + GROUPS);   // softmax warps, unpackers of the values
+    }
     kq::mbar_init(&ctl.o_full, 1);
     ctl.abort = 0;
     kq::fence_barrier_init();
@@ -287,14 +295,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       const uint32_t d = tm + (2 * tile + (j & 1)) * BN;
       const uint64_t qd = kq::smem_desc(qa + tile * (ATOMS * 16384), 16, 1024, kq::kLayoutSwizzle128B);
       const uint64_t kd = kq::smem_desc(kv + (j & SM) * SH::STAGE, 16, 1024, kq::kLayoutSwizzle128B);
+      if (elect_one()) {
 #pragma unroll
-      for (int at = 0; at < ATOMS; ++at)
+        for (int at = 0; at < ATOMS; ++at)
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          if (elect_one())
+          for (int kk = 0; kk < 4; ++kk)
             kq::mma_f16(d, qd + ((at * 16384 + kk * 32) >> 4), kd + ((at * (BN * 128) + kk * 32) >> 4), idesc,
                         at || kk);
-      if (elect_one()) {
         if (tile == tiles - 1) kq::mma_commit(&ctl.k_empty[j & SM]);
         kq::mma_commit(&ctl.s_full[tile][j & 1]);
         kq::mbar_arrive(&ctl.s_full[tile][j & 1]);
@@ -305,10 +312,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       const uint32_t d = tm + SH::O_COL + tile * D, p = tm + (2 * tile + (j & 1)) * BN;
       const uint64_t vd =
           kq::smem_desc(kv + (j & SM) * SH::STAGE + SH::KV_BYTES, BN * 128, 1024, kq::kLayoutSwizzle128B);
-#pragma unroll
-      for (int kk = 0; kk < BN / 16; ++kk)
-        if (elect_one()) mma_f16_ts(d, p + kk * 8, vd + ((kk * 2048) >> 4), idesc, kk > 0 || j > 0);
       if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk) mma_f16_ts(d, p + kk * 8, vd + ((kk * 2048) >> 4), idesc, kk > 0 || j > 0);
         if (tile == tiles - 1) kq::mma_commit(&ctl.v_empty[j & SM]);
         kq::mma_commit(&ctl.pv_done[tile]);
       }
@@ -342,55 +348,93 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     volatile int none = 0;
     kq::mbar_wait(&ctl.o_full, 0, &none, a.info);
     __syncwarp();
-  } else if (warp >= UNPACK_WARP0) {
-    // -------------------------------------------------------- unpacking
-    const int w = warp - UNPACK_WARP0;
+  } else if (warp == NUM_WARP) {
+    // ----------------------------------------------------------- numbers
+    // Page numbers are asked for two steps ahead (lane g: group g), words one step ahead
+    // (keys lane and lane + 32): their latencies pass while earlier steps are written.
     const int any_lo = lo_of(q_first), any_hi = hi_of(q_last);
+    const int P = a.cache.P;
+    auto seen = [&](int t) { return t < any_hi && (t >= any_lo || t < a.sinks); };
+    auto ask_page = [&](int j) -> int {
+      const int t0 = key_of(i0 + j) + GROUP * lane;
+      // (a table entry of INT32_MIN is taken for keys that are not seen)
+      if (j >= steps || lane >= GROUPS || !(t0 < any_hi && (t0 + GROUP > any_lo || t0 < a.sinks))) return INT32_MIN;
+      return (int)load4(reinterpret_cast<const uint32_t*>(a.b.table + u.b * a.b.table_ld + (t0 >> a.cache.lgP)));
+    };
+    struct Words {
+      uint32_t k[2], v[2];
+      uint64_t codes;          // lane g: of group g
+    };
+    auto ask_words = [&](Words& q, int j, int page) {
+      const bool here = page >= 0 && page < a.cache.pages;
+      if (!here && page != INT32_MIN) kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
+      const int key0 = key_of(i0 + j);
+      const uint8_t* blk = a.cache.base + ((int64_t)page * a.cache.heads + head) * (int64_t)a.cache.block_bytes;
+      const uint64_t b64 = here ? (uint64_t)blk : 0;
+      q.codes = here ? b64 + ((key0 + GROUP * lane) & (P - 1)) * (D / 2) : 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = key0 + lane + 32 * i;
+        const uint64_t b = __shfl_sync(0xffffffffu, b64, (lane >> 4) + 2 * i);
+        q.k[i] = q.v[i] = 0;
+        // what no row sees may be memory that was never written: its scales count as 0
+        if (b && seen(t)) {
+          const uint32_t* wp = reinterpret_cast<const uint32_t*>(b + (uint64_t)P * D) + (t & (P - 1));
+          q.k[i] = load4(wp);
+          q.v[i] = load4(wp + P);
+        }
+      }
+    };
+    Words cur, nxt;
+    int page = ask_page(0);
+    if (steps > 0) ask_words(nxt, 0, page);
+    page = ask_page(1);
+    float fv = 0.f;
+    for (int j = 0; j < steps; ++j) {
+      cur = nxt;
+      if (j + 1 < steps) {
+        ask_words(nxt, j + 1, page);
+        page = ask_page(j + 2);
+      }
+      if (j >= 8 && !wait(&ctl.num_free[j & 7], (j >> 3) + 1)) break;
+      // fv: a power of two that keeps value scales below 2^6 (see kv4_attend.cu).  Scales
+      // are not negative: their bits are in the numbers' order; a NaN counts as 0.
+      const uint32_t s0 = cur.v[0] & ~15u, s1 = cur.v[1] & ~15u;
+      const float big = __uint_as_float(__reduce_max_sync(
+          0xffffffffu, max(s0 > 0x7f800000u ? 0u : s0, s1 > 0x7f800000u ? 0u : s1)));
+      float turn = 1.f;
+      if (big > 0.f && (fv == 0.f || big * fv > 64.f)) {
+        const int e = min(max(127 - (int)(__float_as_uint(big) >> 23), -100), 100);
+        const float nf = __uint_as_float((uint32_t)(127 + e) << 23);
+        if (fv != 0.f) turn = nf / fv;
+        fv = nf;
+      }
+      Numbers& n = ctl.num[j & 7];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        n.fk[lane + 32 * i] = word_scale(cur.k[i]) * a.scale_log2;
+        n.sv[lane + 32 * i] = word_scale(cur.v[i]) * fv;
+        n.zeros[lane + 32 * i] = (uint8_t)((cur.k[i] & 15u) | ((cur.v[i] & 15u) << 4));
+      }
+      const uint32_t there = __ballot_sync(0xffffffffu, cur.codes != 0);
+      if (lane < GROUPS) n.codes[lane] = cur.codes;
+      if (lane == 0) {
+        n.absent = ~there & ((1u << GROUPS) - 1);
+        n.turn = turn;
+        n.fv = fv;
+      }
+      __syncwarp();
+      if (lane == 0) kq::mbar_arrive(&ctl.num_full[j & 7]);
+    }
+  } else if (warp >= UNPACK_WARP0) {
+    // --------------------------------------------------------- unpacking
     constexpr int TPL = SH::TPL;
     // Lane to (16-byte chunk, token of the load): the 8 lanes of a phase write the two
     // halves of one 128-byte line of 4 tokens, on 8 different chunks of banks.
     const int c = (lane & 1) | (((lane >> 3) & (SH::CH / 2 - 1)) << 1);
     const int ct = ((lane >> 1) & 3) | ((lane / (4 * SH::CH)) << 2);
-    constexpr int NOT_SEEN = INT32_MIN;       // (a table entry of this value is taken for keys not seen)
-    struct Codes {
-      uint4 k[SH::LOADS], v[SH::LOADS];
-      uint32_t kword, vword;                  // of token lane % 16
-      bool here;                              // the 16 tokens have a page (they lie in one)
-    };
-    // A step's page number is asked for two steps ahead, its codes one step ahead: both
-    // latencies pass while earlier steps are unpacked.
-    auto page_of_step = [&](int j) -> int {
-      const int t0 = key_of(i0 + j) + TPW * w;
-      if (j >= steps || !(t0 < any_hi && (t0 + TPW > any_lo || t0 < a.sinks))) return NOT_SEEN;
-      return (int)load4(reinterpret_cast<const uint32_t*>(a.b.table + u.b * a.b.table_ld + (t0 >> a.cache.lgP)));
-    };
-    auto load = [&](Codes& q, int j, int page) {
-      q.here = page >= 0 && page < a.cache.pages;
-      if (!q.here && page != NOT_SEEN) kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
-      const int P = a.cache.P, t0 = key_of(i0 + j) + TPW * w, slot = t0 & (P - 1);
-      const uint8_t* blk = a.cache.base + ((int64_t)page * a.cache.heads + head) * (int64_t)a.cache.block_bytes;
-      q.kword = q.vword = 0;
-      if (q.here) {
-        const uint4* kp = reinterpret_cast<const uint4*>(blk + (slot + ct) * (D / 2)) + c;
-#pragma unroll
-        for (int i = 0; i < SH::LOADS; ++i) {
-          load16(q.k[i], kp + i * (TPL * SH::CH));
-          load16(q.v[i], kp + i * (TPL * SH::CH) + P * SH::CH);
-        }
-        // what no row sees may be memory that was never written: its scales count as 0
-        const int t = t0 + (lane & (TPW - 1));
-        if (t < any_hi && (t >= any_lo || t < a.sinks)) {
-          const uint32_t* wp = reinterpret_cast<const uint32_t*>(blk + P * D) + (t & (P - 1));
-          q.kword = load4(wp);
-          q.vword = load4(wp + P);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < SH::LOADS; ++i) q.k[i] = q.v[i] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    // where word k of load i goes: (at ^ 16 k) + i (128 TPL), swizzled by the token
-    const uint32_t at = kq::smem_u32(kv_smem) + (c >> 1) * (BN * 128) + (TPW * w + ct) * 128 +
+    // where word k of load i of group 0 goes: (at ^ 16 k) + i (128 TPL), swizzled by the token
+    const uint32_t at = kq::smem_u32(kv_smem) + (c >> 1) * (BN * 128) + ct * 128 +
                         (((4 * (c & 1)) ^ (ct & 7)) << 4);
     static_assert(TPL % 8 == 0 || TPL == 4, "the swizzle of a load's tokens");
     auto put = [&](uint32_t base, int i, int k, uint4 v) {
@@ -399,90 +443,67 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                    : "memory");
     };
-    auto announce = [&](const Codes& q, int j) {            // this warp's largest value scale
-      // (scales are not negative: their bits are in the numbers' order; a NaN counts as 0)
-      const uint32_t bits = q.vword & ~15u;
-      const uint32_t big = __reduce_max_sync(0xffffffffu, bits > 0x7f800000u ? 0u : bits);
-      if (lane == 0) {
-        ctl.sv_warp[j & 1][w] = __uint_as_float(big);
-        ctl.here_warp[j & 1][w] = q.here;
-        kq::mbar_arrive(&ctl.scales);
+    struct Codes {
+      uint4 c[SH::LOADS];
+      uint32_t zeros[SH::LOADS];
+    };
+    // job n: step n / 8, keys (n & 4 == 0) or values, group n % 4
+    const int jobs = 8 * steps;
+    const int64_t vrel = (int64_t)a.cache.P * (D / 2);
+    auto ask = [&](Codes& q, int n) -> bool {
+      const int j = n >> 3, g = n & 3;
+      if (!wait(&ctl.num_full[j & 7], j >> 3)) return false;
+      const Numbers& num = ctl.num[j & 7];
+      const uint64_t p = num.codes[g];
+      const uint8_t* cp = reinterpret_cast<const uint8_t*>(p) + (n & 4 ? vrel : 0) + ct * (D / 2) + 16 * c;
+#pragma unroll
+      for (int i = 0; i < SH::LOADS; ++i) {
+        q.zeros[i] = num.zeros[GROUP * g + i * TPL + ct];
+        q.c[i] = make_uint4(0u, 0u, 0u, 0u);
       }
+      if (p) {
+#pragma unroll
+        for (int i = 0; i < SH::LOADS; ++i) load16(q.c[i], reinterpret_cast<const uint4*>(cp + i * (TPL * (D / 2))));
+      }
+      return true;
     };
     Codes cur, nxt;
-    int page = page_of_step(0);
-    if (steps > 0) {
-      load(nxt, 0, page);
-      announce(nxt, 0);
-    }
-    page = page_of_step(1);
-    float fv = 0.f;
-    bool ok = true;
-    for (int j = 0; j < steps; ++j) {
-      const int st = j & SM, ring = j & 7;
+    int n = warp - UNPACK_WARP0;
+    bool ok = n < jobs && ask(nxt, n);
+    for (; n < jobs && ok; n += UNPACKERS) {
+      const int j = n >> 3, g = n & 3, st = j & SM;
       cur = nxt;
-      if (j + 1 < steps) {
-        load(nxt, j + 1, page);
-        page = page_of_step(j + 2);
-      }
-      // ---- keys, and the numbers of this step
-      if (j >= STAGES) ok = wait(&ctl.k_empty[st], (j >> LG) + 1);
-      ok = ok && wait(&ctl.scales, j);
+      if (n + UNPACKERS < jobs) ok = ask(nxt, n + UNPACKERS);
+      const bool values = n & 4;
+      if (j >= STAGES) ok = ok && wait(values ? &ctl.v_empty[st] : &ctl.k_empty[st], (j >> LG) + 1);
       if (!ok) break;
-      // fv: a power of two that keeps value scales below 2^6 (see kv4_attend.cu)
-      const float big =
-          fmaxf(fmaxf(ctl.sv_warp[j & 1][0], ctl.sv_warp[j & 1][1]), fmaxf(ctl.sv_warp[j & 1][2], ctl.sv_warp[j & 1][3]));
-      float turn = 1.f;
-      if (big > 0.f && (fv == 0.f || big * fv > 64.f)) {
-        const int e = min(max(127 - (int)(__float_as_uint(big) >> 23), -100), 100);
-        const float nf = __uint_as_float((uint32_t)(127 + e) << 23);
-        if (fv != 0.f) turn = nf / fv;
-        fv = nf;
-      }
-      if (lane < TPW) {
-        ctl.fk[ring][TPW * w + lane] = word_scale(cur.kword) * a.scale_log2;
-        ctl.sv[ring][TPW * w + lane] = word_scale(cur.vword) * fv;
-      }
-      if (w == 0 && lane == 0) {
-        uint32_t gone = 0;
+      const uint32_t dst = at + g * (GROUP * 128) + st * SH::STAGE + (values ? SH::KV_BYTES : 0);
+      if (values || !BF) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) gone |= (ctl.here_warp[j & 1][i] ? 0u : 1u) << i;
-        ctl.absent[ring] = gone;
-        ctl.turn[ring] = turn;
-        ctl.fv[ring] = fv;
-      }
-      const uint32_t kd = at + st * SH::STAGE, vd = kd + SH::KV_BYTES;
-      uint32_t zeros[SH::LOADS];               // of the tokens this lane unpacks
+        for (int i = 0; i < SH::LOADS; ++i) {
+          const uint32_t z = values ? cur.zeros[i] >> 4 : cur.zeros[i] & 15u;
+          const uint32_t z1 = 0x64006400u + z * 0x00010001u, z2 = 0xd400d400u + z * 0x00100010u;
+          put(dst, i, 0, codes_f16(cur.c[i].x, z1, z2));
+          put(dst, i, 1, codes_f16(cur.c[i].y, z1, z2));
+          put(dst, i, 2, codes_f16(cur.c[i].z, z1, z2));
+          put(dst, i, 3, codes_f16(cur.c[i].w, z1, z2));
+        }
+      } else {
 #pragma unroll
-      for (int i = 0; i < SH::LOADS; ++i)
-        zeros[i] = __shfl_sync(0xffffffffu, (cur.kword & 15u) | ((cur.vword & 15u) << 4), i * TPL + ct);
-#pragma unroll
-      for (int i = 0; i < SH::LOADS; ++i) {
-        const uint32_t z = zeros[i] & 15u;
-        const uint32_t z1 = (BF ? 0x43004300u : 0x64006400u) + z * 0x00010001u;
-        const uint32_t z2 = 0xd400d400u + z * 0x00100010u;
-        const uint32_t kw[4] = {cur.k[i].x, cur.k[i].y, cur.k[i].z, cur.k[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) put(kd, i, k, BF ? codes_bf16(kw[k], z1) : codes_f16(kw[k], z1, z2));
+        for (int i = 0; i < SH::LOADS; ++i) {
+          const uint32_t z1 = 0x43004300u + (cur.zeros[i] & 15u) * 0x00010001u;
+          put(dst, i, 0, codes_bf16(cur.c[i].x, z1));
+          put(dst, i, 1, codes_bf16(cur.c[i].y, z1));
+          put(dst, i, 2, codes_bf16(cur.c[i].z, z1));
+          put(dst, i, 3, codes_bf16(cur.c[i].w, z1));
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) kq::mbar_arrive(&ctl.k_full[st]);
-      // ---- values
-      if (j >= STAGES) ok = wait(&ctl.v_empty[st], (j >> LG) + 1);
-      if (!ok) break;
-#pragma unroll
-      for (int i = 0; i < SH::LOADS; ++i) {
-        const uint32_t z = zeros[i] >> 4;
-        const uint32_t z1 = 0x64006400u + z * 0x00010001u, z2 = 0xd400d400u + z * 0x00100010u;
-        const uint32_t vw[4] = {cur.v[i].x, cur.v[i].y, cur.v[i].z, cur.v[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) put(vd, i, k, codes_f16(vw[k], z1, z2));
+      if (lane == 0) {
+        kq::mbar_arrive(values ? &ctl.v_full[st] : &ctl.k_full[st]);
+        if (values) kq::mbar_arrive(&ctl.num_free[j & 7]);
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) kq::mbar_arrive(&ctl.v_full[st]);
-      if (j + 1 < steps) announce(nxt, j + 1);
     }
   } else if (warp < 4 * tiles || (NT == 1 && warp < 4)) {
     // ---------------------------------------------------------- softmax
@@ -502,10 +523,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     bool ok = true;
     auto step = [&](auto is_masked, int j, int key0) {
       constexpr bool masked = decltype(is_masked)::value;
-      const int st = j & 7;
       const uint32_t s_at = tbase + (2 * tile + (j & 1)) * BN;
-      const float turn = ctl.turn[st];
-      const uint32_t gone = masked ? ctl.absent[st] : 0u;
+      const Numbers& num = ctl.num[j & 7];
+      const float turn = num.turn;
+      const uint32_t gone = masked ? num.absent : 0u;
       f32x2 t[BN / 2];             // scores relative to the running maximum
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       const f32x2 neg_m = pair(-m, -m);
@@ -514,7 +535,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         float x[32];
         kq::tmem_ld32(s_at + 32 * h, x);
         kq::tmem_wait_ld();
-        const ulonglong2* fk = reinterpret_cast<const ulonglong2*>(&ctl.fk[st][32 * h]);
+        const ulonglong2* fk = reinterpret_cast<const ulonglong2*>(&num.fk[32 * h]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const ulonglong2 f = fk[i];
@@ -563,7 +584,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
           }
         }
       }
-      const ulonglong2* sv = reinterpret_cast<const ulonglong2*>(ctl.sv[st]);
+      const ulonglong2* sv = reinterpret_cast<const ulonglong2*>(num.sv);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t pk[16];
@@ -591,21 +612,25 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       if (!ok) break;
       kq::tc_fence_after();
       const int key0 = key_of(i0 + j);
-      if (ctl.absent[j & 7] || !(key0 + BN <= all_hi && (key0 >= all_lo || key0 + BN <= a.sinks)))
+      if (ctl.num[j & 7].absent || !(key0 + BN <= all_hi && (key0 >= all_lo || key0 + BN <= a.sinks)))
         step(std::true_type{}, j, key0);
       else
         step(std::false_type{}, j, key0);
       kq::tmem_wait_st();
       kq::tc_fence_before();
       __syncwarp();
-      if (lane == 0) kq::mbar_arrive(&ctl.p_ready[tile][j & 1]);
+      if (lane == 0) {
+        kq::mbar_arrive(&ctl.p_ready[tile][j & 1]);
+        kq::mbar_arrive(&ctl.num_free[j & 7]);
+      }
     }
     // ---- output
     const float2 ls = halves(add2(l2[0], l2[1]));
     const float l = ls.x + ls.y;
     if (steps > 0) ok = ok && wait(&ctl.o_full, 0);
     kq::tc_fence_after();
-    const float rfv = steps > 0 && ctl.fv[(steps - 1) & 7] != 0.f ? 1.f / ctl.fv[(steps - 1) & 7] : 0.f;
+    const float fv = steps > 0 ? ctl.num[(steps - 1) & 7].fv : 0.f;
+    const float rfv = fv != 0.f ? 1.f / fv : 0.f;
     const int rr = 128 * tile + tr;
     const bool mine = r0 + rr < rows;
     const int64_t slot = ((int64_t)(u.slot0 + (int)blockIdx.x - u.base) * a.cache.heads + head) * R + rr;
