@@ -1,13 +1,20 @@
 // Attention of new queries over the paged 4-bit cache, many query rows per key
 // (prompts, chunks of prompts, long drafts): tcgen05 with the same arithmetic as
 // kv4_attend.cu.  Codes are unpacked once per block and tile of keys into shared
-// memory as the whole numbers c - z (exact in fp16 and bf16), so
-//   S = Q K^T      in the queries' type, fp32 accumulators in tensor memory
-//   x = S s_j scale log2(e),  p = 2^(x - m),  P = p s'_j (fp16)
-//   O += P V       with P as the tensor-memory operand, over S
-// and the only rounding besides fp32's is P's.  The running maximum m is a whole
-// number and moves only when a score passes it by 8; what was summed before is
-// then scaled by a power of two.
+// memory as fp16 numbers; S = Q K^T and O += P V have fp32 accumulators in tensor
+// memory, P is the tensor-memory operand, over S.  Two ways, by the queries' type:
+//   fp16  the unpacked numbers are c - z, exact; scores and probabilities take the
+//         scale of their key, x = S s_j scale log2(e), P = 2^(x - m) s'_j, and the only
+//         rounding besides fp32's is P's.
+//   bf16  the unpacked numbers are the keys and values themselves, s (c - z) rounded to
+//         fp16 (the scale in two terms, so rounded once; a value's scale in one), and
+//         queries are taken to fp16 by a power of two per row, exactly.  That is 2^-11
+//         relative per key and value where the output is rounded at 2^-8, and it spares
+//         every row reading two numbers per key: reads of the same 16 bytes by all lanes
+//         cost four passes through shared memory each, and those were 1000 of the 2400
+//         passes per step that bounded the kernel.
+// The running maximum m is a whole number and moves only when a score passes it by 8;
+// what was summed before is then scaled by a power of two.
 //
 // One block = up to 256 rows (two tiles of 128; one at head_dim 256) of one
 // sequence and key/value head, over its keys 64 at a time.  Warps:
@@ -36,7 +43,6 @@ namespace {
 constexpr int MMA_WARP = 8, NUM_WARP = 9, UNPACK_WARP0 = 10, UNPACKERS = 6, THREADS = 512;
 constexpr int BN = 64, GROUP = 16, GROUPS = BN / GROUP;    // keys per step, per unpacking job
 constexpr float NO_MAX = -0x1p127f;     // a split's maximum where it saw no key
-constexpr float LAG = 8.f;
 
 template <int D>
 struct Shape {
@@ -57,11 +63,14 @@ struct Shape {
 
 // What the other warps need to know of a step's keys.
 struct alignas(16) Numbers {
-  float fk[BN], sv[BN];      // score factor; value scale x fv
+  float fk[BN], sv[BN];      // fp16 queries: score factor; value scale x fv
+  uint32_t ks[BN];           // bf16: key scale x 2^f as two halves (high term, low term)
+  uint16_t vs[BN];           // bf16: value scale x fv
   uint8_t zeros[BN];         // key's zero point | value's << 4
   uint64_t codes[GROUPS];    // address of the group's first key's codes, 0: no page
   uint32_t absent;           // bit per group: no page
   float turn, fv;            // fv over fv of the step before; fv
+  float down;                // bf16: 2^-f
 };
 
 struct alignas(16) Ctl {
@@ -72,6 +81,7 @@ struct alignas(16) Ctl {
   uint64_t pv_done[2], o_full;
   uint32_t tmem;
   int abort;
+  float row[256];                        // bf16: score factor of each row
 };
 
 // One lane of a converged warp, the same one every time.  The operands of what it issues
@@ -181,23 +191,31 @@ KQ_DEV uint4 codes_f16(uint32_t w, uint32_t z1, uint32_t z2) {
   }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
-// The same in bf16; z1: 128 + z in both halves.
-KQ_DEV uint4 codes_bf16(uint32_t w, uint32_t z1) {
-  const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&z1);
-  uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 x = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), a);
-    r[i] = *reinterpret_cast<const uint32_t*>(&x);
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
+KQ_DEV uint32_t mul_half2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+KQ_DEV uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
+                            *reinterpret_cast<const __half2*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// v (hi + lo), rounded once (the product with lo is 2^-11 of it)
+KQ_DEV uint4 scaled(uint4 v, uint32_t hi, uint32_t lo) {
+  return make_uint4(fma_half2(v.x, hi, mul_half2(v.x, lo)), fma_half2(v.y, hi, mul_half2(v.y, lo)),
+                    fma_half2(v.z, hi, mul_half2(v.z, lo)), fma_half2(v.w, hi, mul_half2(v.w, lo)));
+}
+KQ_DEV uint4 scaled(uint4 v, uint32_t s) {
+  return make_uint4(mul_half2(v.x, s), mul_half2(v.y, s), mul_half2(v.z, s), mul_half2(v.w, s));
 }
 
 template <int D, bool BF>
 __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs a) {
   using SH = Shape<D>;
   constexpr int NT = SH::NT, R = SH::R, ATOMS = SH::ATOMS;
+  // how far scores may pass the running maximum, and where it is put below a new one: P is
+  // at most 2^14, times a value's scale below 2^6 on the fp16 way
+  constexpr float LAG = BF ? 14.f : 8.f, BASE = BF ? 6.f : 0.f;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl ctl;
   uint8_t* q_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -269,9 +287,26 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         for (int j = 0; j < 8; ++j) h[j] = __ldg(p + j);
         v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
       }
-      v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                     __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
     }
+    if (BF) {
+      // to fp16 by the power of two that takes the row's largest to about 2^10 (the
+      // D / 8 lanes of a row are neighbours)
+      float x[8];
+      unpack8(v, BF16, x);
+      float big = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(x[j]));
+#pragma unroll
+      for (int o = 1; o < D / 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      const int e = min(max(137 - (int)(__float_as_uint(big) >> 23), -126), 126);
+      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= up;
+      v = pack8(x, FP16);
+      if (c == 0) ctl.row[r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
+    }
+    v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                   __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
     uint8_t* dst = q_smem + ((r >> 7) * ATOMS + (c >> 3)) * 16384 + (r & 127) * 128 +
                    (((c & 7) ^ (r & 7)) << 4);
     *reinterpret_cast<uint4*>(dst) = v;
@@ -291,7 +326,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     // -------------------------------------------------------------- MMAs
     const uint32_t tm = uniform(tmem), qa = uniform(kq::smem_u32(q_smem)), kv = uniform(kq::smem_u32(kv_smem));
     auto issue_s = [&](int tile, int j) {
-      constexpr uint32_t idesc = kq::idesc_f16(128, BN, BF ? 1 : 0, 0, 0);
+      constexpr uint32_t idesc = kq::idesc_f16(128, BN, 0, 0, 0);
       const uint32_t d = tm + (2 * tile + (j & 1)) * BN;
       const uint64_t qd = kq::smem_desc(qa + tile * (ATOMS * 16384), 16, 1024, kq::kLayoutSwizzle128B);
       const uint64_t kd = kq::smem_desc(kv + (j & SM) * SH::STAGE, 16, 1024, kq::kLayoutSwizzle128B);
@@ -410,11 +445,36 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         fv = nf;
       }
       Numbers& n = ctl.num[j & 7];
+      // bf16: f takes the step's largest key scale to [1/2, 1) x 2
+      float kup = 1.f;
+      if (BF) {
+        const uint32_t k0 = cur.k[0] & ~15u, k1 = cur.k[1] & ~15u;
+        const uint32_t kb = __reduce_max_sync(0xffffffffu, max(k0 > 0x7f800000u ? 0u : k0, k1 > 0x7f800000u ? 0u : k1));
+        const int e = min(max(127 - (int)(kb >> 23), -126), 126);
+        kup = __uint_as_float((uint32_t)(127 + e) << 23);
+        if (lane == 0) n.down = __uint_as_float((uint32_t)(127 - e) << 23);
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        n.fk[lane + 32 * i] = word_scale(cur.k[i]) * a.scale_log2;
-        n.sv[lane + 32 * i] = word_scale(cur.v[i]) * fv;
-        n.zeros[lane + 32 * i] = (uint8_t)((cur.k[i] & 15u) | ((cur.v[i] & 15u) << 4));
+        const int t = lane + 32 * i;
+        float ks = word_scale(cur.k[i]), vs = word_scale(cur.v[i]) * fv;
+        if (BF) {
+          // a value that is not finite must not meet the zero probabilities of rows that do
+          // not see it: it counts as 0, and its key makes the score of those that do a NaN
+          if (!(vs < INFINITY)) {
+            vs = 0.f;
+            ks = NAN;
+          }
+          ks *= kup;
+          const __half hi = __float2half_rn(ks);
+          const __half2 k2 = __halves2half2(hi, __float2half_rn(ks - __half2float(hi)));
+          n.ks[t] = *reinterpret_cast<const uint32_t*>(&k2);
+          n.vs[t] = __half_as_ushort(__float2half_rn(vs));
+        } else {
+          n.fk[t] = ks * a.scale_log2;
+          n.sv[t] = vs;
+        }
+        n.zeros[t] = (uint8_t)((cur.k[i] & 15u) | ((cur.v[i] & 15u) << 4));
       }
       const uint32_t there = __ballot_sync(0xffffffffu, cur.codes != 0);
       if (lane < GROUPS) n.codes[lane] = cur.codes;
@@ -445,7 +505,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     };
     struct Codes {
       uint4 c[SH::LOADS];
-      uint32_t zeros[SH::LOADS];
+      uint32_t zeros[SH::LOADS], scale[SH::LOADS];
     };
     // job n: step n / 8, keys (n & 4 == 0) or values, group n % 4
     const int jobs = 8 * steps;
@@ -458,7 +518,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       const uint8_t* cp = reinterpret_cast<const uint8_t*>(p) + (n & 4 ? vrel : 0) + ct * (D / 2) + 16 * c;
 #pragma unroll
       for (int i = 0; i < SH::LOADS; ++i) {
-        q.zeros[i] = num.zeros[GROUP * g + i * TPL + ct];
+        const int t = GROUP * g + i * TPL + ct;
+        q.zeros[i] = num.zeros[t];
+        if (BF) q.scale[i] = n & 4 ? num.vs[t] : num.ks[t];
         q.c[i] = make_uint4(0u, 0u, 0u, 0u);
       }
       if (p) {
@@ -478,24 +540,21 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       if (j >= STAGES) ok = ok && wait(values ? &ctl.v_empty[st] : &ctl.k_empty[st], (j >> LG) + 1);
       if (!ok) break;
       const uint32_t dst = at + g * (GROUP * 128) + st * SH::STAGE + (values ? SH::KV_BYTES : 0);
-      if (values || !BF) {
 #pragma unroll
-        for (int i = 0; i < SH::LOADS; ++i) {
-          const uint32_t z = values ? cur.zeros[i] >> 4 : cur.zeros[i] & 15u;
-          const uint32_t z1 = 0x64006400u + z * 0x00010001u, z2 = 0xd400d400u + z * 0x00100010u;
-          put(dst, i, 0, codes_f16(cur.c[i].x, z1, z2));
-          put(dst, i, 1, codes_f16(cur.c[i].y, z1, z2));
-          put(dst, i, 2, codes_f16(cur.c[i].z, z1, z2));
-          put(dst, i, 3, codes_f16(cur.c[i].w, z1, z2));
-        }
-      } else {
+      for (int i = 0; i < SH::LOADS; ++i) {
+        const uint32_t z = values ? cur.zeros[i] >> 4 : cur.zeros[i] & 15u;
+        const uint32_t z1 = 0x64006400u + z * 0x00010001u, z2 = 0xd400d400u + z * 0x00100010u;
+        const uint32_t hi = __byte_perm(cur.scale[i], 0, 0x1010), lo = __byte_perm(cur.scale[i], 0, 0x3232);
+        const uint32_t w[4] = {cur.c[i].x, cur.c[i].y, cur.c[i].z, cur.c[i].w};
+        if (!BF) {
 #pragma unroll
-        for (int i = 0; i < SH::LOADS; ++i) {
-          const uint32_t z1 = 0x43004300u + (cur.zeros[i] & 15u) * 0x00010001u;
-          put(dst, i, 0, codes_bf16(cur.c[i].x, z1));
-          put(dst, i, 1, codes_bf16(cur.c[i].y, z1));
-          put(dst, i, 2, codes_bf16(cur.c[i].z, z1));
-          put(dst, i, 3, codes_bf16(cur.c[i].w, z1));
+          for (int k = 0; k < 4; ++k) put(dst, i, k, codes_f16(w[k], z1, z2));
+        } else if (values) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) put(dst, i, k, scaled(codes_f16(w[k], z1, z2), hi));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) put(dst, i, k, scaled(codes_f16(w[k], z1, z2), hi, lo));
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -511,6 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     const int tr = (warp & 3) * 32 + lane;              // row within the tile
     const uint32_t tbase = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t o_at = tbase + SH::O_COL + tile * D;
+    const float row = BF ? ctl.row[128 * tile + tr] : 0.f;
     const int r = min(last, r0 + 128 * tile + tr);
     const int qi = r / a.g;
     const int lo = lo_of(qi), hi = hi_of(qi);
@@ -529,7 +589,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       const uint32_t gone = masked ? num.absent : 0u;
       f32x2 t[BN / 2];             // scores relative to the running maximum
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      const f32x2 neg_m = pair(-m, -m);
+      const f32x2 neg_m = pair(-m, -m), row2 = BF ? pair(row * num.down, row * num.down) : 0ull;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float x[32];
@@ -538,7 +598,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         const ulonglong2* fk = reinterpret_cast<const ulonglong2*>(&num.fk[32 * h]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const ulonglong2 f = fk[i];
+          const ulonglong2 f = BF ? make_ulonglong2(row2, row2) : fk[i];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int e = 4 * i + 2 * k;
@@ -560,7 +620,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       if (__any_sync(0xffffffffu, high > lag || turn != 1.f)) {
         // the maximum moves by a whole number; what was summed before turns by a power of two
         const bool up = high > lag;
-        const float by = up ? (high < INFINITY ? ceilf(high) : high) : 0.f;
+        const float by = up ? (high < INFINITY ? ceilf(high) - BASE : high) : 0.f;
         const float al = up && lag == LAG ? exp2_approx(-by) : 1.f;
         if (up) lag = LAG;
         m += by;
@@ -590,14 +650,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const ulonglong2 f = sv[8 * h + i];
+          const ulonglong2 f = BF ? make_ulonglong2(0ull, 0ull) : sv[8 * h + i];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float2 v = halves(t[16 * h + 2 * i + k]);
             const f32x2 p = pair(exp2_approx(v.x), exp2_approx(v.y));
             l2[k] = add2(l2[k], p);
-            float2 w = halves(mul2(p, k ? f.y : f.x));
-            if constexpr (masked) {                     // (0 times a NaN scale)
+            float2 w = halves(BF ? p : mul2(p, k ? f.y : f.x));
+            if constexpr (masked && !BF) {                     // (0 times a NaN scale)
               if (v.x == -INFINITY) w.x = 0.f;
               if (v.y == -INFINITY) w.y = 0.f;
             }
