@@ -20,13 +20,14 @@
 // sequence and key/value head, over its keys 64 at a time.  Warps:
 //   0-3, 4-7  softmax of tile 0, of tile 1: a thread owns a row, reads its 64 scores and
 //             writes the probabilities over them, so no reduction crosses lanes
-//   8         issues the MMAs.  Every tile has two S buffers and S runs two steps ahead
+//   8, 9      issue the MMAs, of a tile each (one warp needs some 70 cycles per MMA, more
+//             than an MMA of 64 keys takes).  Every tile has two S buffers and S runs two steps ahead
 //             (S of step j + 2 goes over P of step j behind P V of step j), so the softmax
 //             never waits for a product: with 128 keys and one buffer (all of tensor
 //             memory) it did, and a step took twice as long.
-//   9         numbers: looks up the pages, turns the keys' words into factors, up to 8
+//   10        numbers: looks up the pages, turns the keys' words into factors, up to 8
 //             steps ahead
-//   10-15     unpacking: 16 tokens' keys or values at a time, in turn (eight such jobs to
+//   11-15     unpacking: 32 tokens' keys or values at a time, in turn (four such jobs to
 //             a step), the next one's codes on their way; rows of 128 bytes, 128-byte
 //             swizzled, for both operands (keys K-major, values MN-major)
 // Dims stay in the order unpacking yields within each 8 (0 4 1 5 2 6 3 7): queries
@@ -40,8 +41,9 @@
 namespace kv4 {
 namespace {
 
-constexpr int MMA_WARP = 8, NUM_WARP = 9, UNPACK_WARP0 = 10, UNPACKERS = 6, THREADS = 512;
-constexpr int BN = 64, GROUP = 16, GROUPS = BN / GROUP;    // keys per step, per unpacking job
+constexpr int MMA_WARP0 = 8, NUM_WARP = 10, UNPACK_WARP0 = 11, THREADS = 512;
+constexpr int BN = 64, GROUP = 16, GROUPS = BN / GROUP;    // keys per step; that surely share a page
+constexpr int JOB = 32, JOBS = BN / JOB;                   // keys per unpacking job; jobs for a step's keys
 constexpr float NO_MAX = -0x1p127f;     // a split's maximum where it saw no key
 
 template <int D>
@@ -54,10 +56,16 @@ struct Shape {
   static constexpr int STAGE = 2 * KV_BYTES;
   static constexpr int CH = D / 32;                  // 16-byte chunks of a token's codes
   static constexpr int TPL = 32 / CH;                // tokens per load of a warp
-  static constexpr int LOADS = GROUP / TPL;          // chunks per lane
+  static constexpr int LOADS = JOB / TPL;            // chunks per lane of a job
   static constexpr int O_COL = 256;                  // tensor memory: S buffers, 64 columns each, then O
   static constexpr int STAGES = D == 256 ? 2 : 4;    // of keys and values: what fits
   static constexpr int LG = D == 256 ? 1 : 2;
+  // Unpacking warps.  A job of step j waits for its stage's last user, step j - STAGES; a
+  // barrier tells two phases apart, so step j - 2 STAGES must be known to be done.  It is:
+  // with four stages the warp's job before was of step j - 2 at the least and waited for S
+  // or P V of step j - 6, both behind P V of step j - 8; with two, four warps have one kind
+  // of job each and wait for every step.
+  static constexpr int UNPACKERS = D == 256 ? 4 : 5;
   static constexpr int SMEM = Q_BYTES + STAGES * STAGE + 1024;
 };
 
@@ -247,13 +255,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
   auto key_of = [&](int i) { return (i < sp.sb ? i : sp.lb + i - sp.sb) * BN; };   // first key of block i
 
   volatile int* abort = &ctl.abort;
+  constexpr int UNPACKERS = SH::UNPACKERS;
   constexpr int STAGES = SH::STAGES, LG = SH::LG, SM = STAGES - 1;    // stage of step j: j & SM, its phase j >> LG
   if (threadIdx.x == 0) {
     for (int i = 0; i < SH::STAGES; ++i) {
-      kq::mbar_init(&ctl.k_full[i], 4);
-      kq::mbar_init(&ctl.k_empty[i], 1);
-      kq::mbar_init(&ctl.v_full[i], 4);
-      kq::mbar_init(&ctl.v_empty[i], 1);
+      kq::mbar_init(&ctl.k_full[i], JOBS);
+      kq::mbar_init(&ctl.k_empty[i], tiles);
+      kq::mbar_init(&ctl.v_full[i], JOBS);
+      kq::mbar_init(&ctl.v_empty[i], tiles);
     }
     for (int i = 0; i < 2; ++i) {
       for (int k = 0; k < 2; ++k) {
@@ -264,13 +273,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     }
     for (int i = 0; i < 8; ++i) {
       kq::mbar_init(&ctl.num_full[i], 1);
-      kq::mbar_init(&ctl.num_free[i], 4 * tiles + GROUPS);   // softmax warps, unpackers of the values
+      kq::mbar_init(&ctl.num_free[i], 4 * tiles + JOBS);   // softmax warps, unpackers of the values
     }
-    kq::mbar_init(&ctl.o_full, 1);
+    kq::mbar_init(&ctl.o_full, tiles);
     ctl.abort = 0;
     kq::fence_barrier_init();
   }
-  if (warp == MMA_WARP) kq::tmem_alloc(&ctl.tmem, 512);
+  if (warp == MMA_WARP0) kq::tmem_alloc(&ctl.tmem, 512);
   // queries: rows of 128-byte lines, dims of each 8 in the codes' order
   for (int e = threadIdx.x; e < R * (D / 8); e += THREADS) {
     const int r = e / (D / 8), c = e - r * (D / 8);
@@ -322,10 +331,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     return __all_sync(0xffffffffu, kq::mbar_wait(bar, (uint32_t)parity & 1u, abort, a.info));
   };
 
-  if (warp == MMA_WARP) {
+  if (warp >= MMA_WARP0 && warp < MMA_WARP0 + tiles) {
+    const int tile = warp - MMA_WARP0;
     // -------------------------------------------------------------- MMAs
     const uint32_t tm = uniform(tmem), qa = uniform(kq::smem_u32(q_smem)), kv = uniform(kq::smem_u32(kv_smem));
-    auto issue_s = [&](int tile, int j) {
+    auto issue_s = [&](int j) {
       constexpr uint32_t idesc = kq::idesc_f16(128, BN, 0, 0, 0);
       const uint32_t d = tm + (2 * tile + (j & 1)) * BN;
       const uint64_t qd = kq::smem_desc(qa + tile * (ATOMS * 16384), 16, 1024, kq::kLayoutSwizzle128B);
@@ -337,12 +347,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
           for (int kk = 0; kk < 4; ++kk)
             kq::mma_f16(d, qd + ((at * 16384 + kk * 32) >> 4), kd + ((at * (BN * 128) + kk * 32) >> 4), idesc,
                         at || kk);
-        if (tile == tiles - 1) kq::mma_commit(&ctl.k_empty[j & SM]);
+        kq::mma_commit(&ctl.k_empty[j & SM]);
         kq::mma_commit(&ctl.s_full[tile][j & 1]);
         kq::mbar_arrive(&ctl.s_full[tile][j & 1]);
       }
     };
-    auto issue_pv = [&](int tile, int j) {
+    auto issue_pv = [&](int j) {
       constexpr uint32_t idesc = kq::idesc_f16(128, D, 0, 0, 1);
       const uint32_t d = tm + SH::O_COL + tile * D, p = tm + (2 * tile + (j & 1)) * BN;
       const uint64_t vd =
@@ -350,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk) mma_f16_ts(d, p + kk * 8, vd + ((kk * 2048) >> 4), idesc, kk > 0 || j > 0);
-        if (tile == tiles - 1) kq::mma_commit(&ctl.v_empty[j & SM]);
+        kq::mma_commit(&ctl.v_empty[j & SM]);
         kq::mma_commit(&ctl.pv_done[tile]);
       }
     };
@@ -359,22 +369,19 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       ok = wait(&ctl.k_full[j], 0);
       if (!ok) break;
       kq::tc_fence_after();
-      for (int i = 0; i < tiles; ++i) issue_s(i, j);
+      issue_s(j);
     }
     for (int j = 0; j < steps && ok; ++j) {
-      ok = wait(&ctl.v_full[j & SM], j >> LG);
-      for (int i = 0; i < tiles && ok; ++i) {
-        ok = wait(&ctl.p_ready[i][j & 1], j >> 1);
-        if (!ok) break;
-        kq::tc_fence_after();
-        issue_pv(i, j);
-      }
-      if (ok && j + 2 < steps) {
+      ok = wait(&ctl.v_full[j & SM], j >> LG) && wait(&ctl.p_ready[tile][j & 1], j >> 1);
+      if (!ok) break;
+      kq::tc_fence_after();
+      issue_pv(j);
+      if (j + 2 < steps) {
         ok = wait(&ctl.k_full[(j + 2) & SM], (j + 2) >> LG);
         if (!ok) break;
         kq::tc_fence_after();
         // (over P, in issue order behind the MMAs that read it)
-        for (int i = 0; i < tiles; ++i) issue_s(i, j + 2);
+        issue_s(j + 2);
       }
     }
     // (also after a wait that gave up: nothing is in flight when the block ends)
@@ -383,9 +390,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     volatile int none = 0;
     kq::mbar_wait(&ctl.o_full, 0, &none, a.info);
     __syncwarp();
+  } else if (warp == MMA_WARP0 + 1) {
+    // (one tile: nothing to issue)
   } else if (warp == NUM_WARP) {
     // ----------------------------------------------------------- numbers
-    // Page numbers are asked for two steps ahead (lane g: group g), words one step ahead
+    // Page numbers are asked for three steps ahead (lane g: group g), words two steps ahead
     // (keys lane and lane + 32): their latencies pass while earlier steps are written.
     const int any_lo = lo_of(q_first), any_hi = hi_of(q_last);
     const int P = a.cache.P;
@@ -420,16 +429,19 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         }
       }
     };
-    Words cur, nxt;
+    Words cur, nxt, after;
     int page = ask_page(0);
     if (steps > 0) ask_words(nxt, 0, page);
     page = ask_page(1);
+    if (steps > 1) ask_words(after, 1, page);
+    page = ask_page(2);
     float fv = 0.f;
     for (int j = 0; j < steps; ++j) {
       cur = nxt;
-      if (j + 1 < steps) {
-        ask_words(nxt, j + 1, page);
-        page = ask_page(j + 2);
+      nxt = after;
+      if (j + 2 < steps) {
+        ask_words(after, j + 2, page);
+        page = ask_page(j + 3);
       }
       if (j >= 8 && !wait(&ctl.num_free[j & 7], (j >> 3) + 1)) break;
       // fv: a power of two that keeps value scales below 2^6 (see kv4_attend.cu).  Scales
@@ -507,39 +519,45 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       uint4 c[SH::LOADS];
       uint32_t zeros[SH::LOADS], scale[SH::LOADS];
     };
-    // job n: step n / 8, keys (n & 4 == 0) or values, group n % 4
-    const int jobs = 8 * steps;
+    // job n: step n / 4, keys (n & 2 == 0) or values, half n & 1 of the step
+    static_assert(JOBS == 2 && JOB == 2 * GROUP, "four jobs to a step, two pages to a job");
+    const int jobs = 2 * JOBS * steps;
     const int64_t vrel = (int64_t)a.cache.P * (D / 2);
     auto ask = [&](Codes& q, int n) -> bool {
-      const int j = n >> 3, g = n & 3;
+      const int j = n >> 2, g = n & 1;
       if (!wait(&ctl.num_full[j & 7], j >> 3)) return false;
       const Numbers& num = ctl.num[j & 7];
-      const uint64_t p = num.codes[g];
-      const uint8_t* cp = reinterpret_cast<const uint8_t*>(p) + (n & 4 ? vrel : 0) + ct * (D / 2) + 16 * c;
+      const int64_t rel = (n & 2 ? vrel : 0) + ct * (D / 2) + 16 * c;
 #pragma unroll
       for (int i = 0; i < SH::LOADS; ++i) {
-        const int t = GROUP * g + i * TPL + ct;
+        const int t = JOB * g + i * TPL + ct;
         q.zeros[i] = num.zeros[t];
-        if (BF) q.scale[i] = n & 4 ? num.vs[t] : num.ks[t];
-        q.c[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (BF) q.scale[i] = n & 2 ? num.vs[t] : num.ks[t];
       }
-      if (p) {
 #pragma unroll
-        for (int i = 0; i < SH::LOADS; ++i) load16(q.c[i], reinterpret_cast<const uint4*>(cp + i * (TPL * (D / 2))));
+      for (int h = 0; h < 2; ++h) {
+        const uint64_t p = num.codes[2 * g + h];
+#pragma unroll
+        for (int i = h * (SH::LOADS / 2); i < (h + 1) * (SH::LOADS / 2); ++i) {
+          q.c[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (p)
+            load16(q.c[i], reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(p) + rel +
+                                                          (i - h * (SH::LOADS / 2)) * (TPL * (D / 2))));
+        }
       }
       return true;
     };
     Codes cur, nxt;
     int n = warp - UNPACK_WARP0;
-    bool ok = n < jobs && ask(nxt, n);
+    bool ok = n < jobs && warp < UNPACK_WARP0 + UNPACKERS && ask(nxt, n);
     for (; n < jobs && ok; n += UNPACKERS) {
-      const int j = n >> 3, g = n & 3, st = j & SM;
+      const int j = n >> 2, g = n & 1, st = j & SM;
       cur = nxt;
       if (n + UNPACKERS < jobs) ok = ask(nxt, n + UNPACKERS);
-      const bool values = n & 4;
+      const bool values = n & 2;
       if (j >= STAGES) ok = ok && wait(values ? &ctl.v_empty[st] : &ctl.k_empty[st], (j >> LG) + 1);
       if (!ok) break;
-      const uint32_t dst = at + g * (GROUP * 128) + st * SH::STAGE + (values ? SH::KV_BYTES : 0);
+      const uint32_t dst = at + g * (JOB * 128) + st * SH::STAGE + (values ? SH::KV_BYTES : 0);
 #pragma unroll
       for (int i = 0; i < SH::LOADS; ++i) {
         const uint32_t z = values ? cur.zeros[i] >> 4 : cur.zeros[i] & 15u;
@@ -726,7 +744,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
   }
   kq::tc_fence_before();
   __syncthreads();
-  if (warp == MMA_WARP) {
+  if (warp == MMA_WARP0) {
     kq::tc_fence_after();
     kq::tmem_dealloc(tmem, 512);
   }
