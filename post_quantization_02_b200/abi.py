@@ -73,9 +73,9 @@ def lib() -> ctypes.CDLL:
         "kronq_kv4_append": ([P, I64, I64, P, I64, I64, P, I64, I64, I32, I64, I32, P, P, I64, I32, I32, P, P,
                               P, I64, I32, I32, I32, P, I64, I64, P, P, I64, P, P], I32),
         "kronq_kv4_gather": ([P, P, I32, I64, P, I64, I32, I32, I32, P, I64, I64, P, P, I64, P, P], I32),
-        "kronq_kv4_attention_workspace_size": ([I64, I32, I32, I32, I64], SZ),
         "kronq_kv4_attention": ([P, I64, I64, I32, I64, I32, P, I64, I32, I32, I32, P, I64, I64, P, P, I64,
                                  F32, I32, I32, I32, P, I64, I64, P, P, P, SZ, P], I32),
+        "kronq_kv4_attention_workspace_size": ([I64, I32, I32, I32, I64], SZ),
         "kronq_timing_enable": ([I32], I32),
         "kronq_timing_read": ([I32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_uint64)], I32),
     }
@@ -493,133 +493,45 @@ def kronq_quantize_layer_gptaq(W, U, P, bits: int, group: int, block: int, codes
 
 
 # ------------------------------------------------ 4-bit key/value cache
-KV_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_KV_ROWS = (torch.bfloat16, torch.float16)
-
-
 def kronq_kv4_block_bytes(page_size: int, head_dim: int) -> int:
     return int(lib().kronq_kv4_block_bytes(page_size, head_dim))
 
 
-# These run once per layer and token, so the checks below go straight to the
-# tensors' fields: a decode step's kernels take a few microseconds themselves.
-def _kv_rows(t, name, dtype, T, D):
-    """Address and strides of a T x heads x D tensor with a contiguous last dimension."""
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 3 or shape[0] != T or shape[2] != D:
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected ({T}, heads, {D})")
-    st, sh, sd = t.stride()
-    if sd != 1:
-        raise ValueError(f"{name} needs unit stride along its last dimension")
-    return t.data_ptr(), st, sh
+_kv4 = None
 
 
-def _kv_vector(t, name, dtype, count, dev):
-    """Address of a contiguous vector (None: none)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.numel() != count or not t.is_contiguous():
-        raise ValueError(f"{name} must hold {count} {dtype} elements in order, got {t.dtype} {tuple(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-    return t.data_ptr()
+def _kv4_calls():
+    """The torch binding of the cache's per-token calls (csrc/kv4_torch.cpp):
+    checks, device and stream are handled there."""
+    global _kv4
+    if _kv4 is None:
+        lib()                # _kv4.so links libkronq.so
+        try:
+            from . import _kv4 as module
+        except ImportError as e:
+            raise RuntimeError(f"{HERE / '_kv4.so'} is not built; run "
+                               "`python -m post_quantization_02_b200.build`") from e
+        module.set_error(KronqError)
+        _kv4 = module
+    return _kv4
 
 
-def _kv_device(*tensors):
-    """The current CUDA device, on which all of them have to be."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != dev or dev < 0:
-            raise ValueError(f"tensors on {[str(x.device) for x in tensors]}: one CUDA device is wanted")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
-    return dev
-
-
-def _kv_args(fn, cache, block_table, q_start, kv_len, D):
-    """The (cache, batch) part of a kronq_kv4 call after its checks."""
-    if cache.dtype is not torch.uint8 or cache.dim() != 3 or not cache.is_contiguous():
-        raise ValueError(f"{fn}: cache must be a contiguous uint8 tensor of 3 dims (pages, heads, bytes)")
-    if block_table.dtype is not torch.int32 or q_start.dtype is not torch.int32 or kv_len.dtype is not torch.int32:
-        raise ValueError(f"{fn}: block_table, q_start and kv_len must be int32")
-    if block_table.dim() != 2 or q_start.dim() != 1 or kv_len.dim() != 1:
-        raise ValueError(f"{fn}: block_table has 2 dims, q_start and kv_len have 1")
-    B, max_pages = block_table.shape
-    if q_start.shape[0] != B + 1 or kv_len.shape[0] != B:
-        raise ValueError(f"{fn}: block_table has {B} rows, q_start {q_start.numel()} entries "
-                         f"({B + 1} expected), kv_len {kv_len.numel()} ({B} expected)")
-    ld, last = block_table.stride()
-    if B == 1:
-        ld = max_pages
-    if (max_pages > 1 and last != 1) or not q_start.is_contiguous() or not kv_len.is_contiguous():
-        raise ValueError(f"{fn}: block_table, q_start and kv_len need unit stride along their last dimension")
-    if ld < max_pages:
-        raise ValueError(f"{fn}: block_table's rows overlap")
-    pages, heads, nbytes = cache.shape
-    page = nbytes // (D + 8)
-    if page * (D + 8) != nbytes:
-        raise ValueError(f"{fn}: a cache block of {nbytes} bytes does not hold whole tokens of head_dim {D}")
-    return (cache.data_ptr(), pages, page, heads, D, block_table.data_ptr(), ld, max_pages,
-            q_start.data_ptr(), kv_len.data_ptr(), B)
-
-
-def _kv_stream(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+def _raw(stream) -> int:
+    return 0 if stream is None else stream.cuda_stream
 
 
 def kronq_kv4_append(q, k, v, cache, block_table, q_start, kv_len, q_out=None, table=None,
                      interleaved: bool = False, positions=None, signs=None, info=None, stream=None):
-    """New keys and values (T x heads x D, bf16 or fp16) into the 4-bit cache,
-    keys and queries rotated on the way (see kronq.h).  q and q_out may be None."""
-    dt = k.dtype
-    if dt not in _KV_ROWS or k.dim() != 3:
-        raise ValueError(f"k must be bf16 or fp16 with 3 dims, got {dt} {tuple(k.shape)}")
-    T, heads, D = k.shape
-    kr = _kv_rows(k, "k", dt, T, D)
-    vr = _kv_rows(v, "v", dt, T, D)
-    args = _kv_args("kronq_kv4_append", cache, block_table, q_start, kv_len, D)
-    if v.shape[1] != heads or args[3] != heads:
-        raise ValueError("kronq_kv4_append: k, v and the cache differ in their heads")
-    if (q is None) != (q_out is None):
-        raise ValueError("kronq_kv4_append: q and q_out go together")
-    if q is None:
-        dev = _kv_device(k, v, cache, block_table, q_start, kv_len)
-        qr, q_heads, qo = (None, 0, 0), 0, None
-    else:
-        qr = _kv_rows(q, "q", dt, T, D)
-        if q_out.dtype is not dt or q_out.shape != q.shape or not q_out.is_contiguous():
-            raise ValueError("q_out must be contiguous with q's type and shape")
-        dev = _kv_device(k, v, cache, block_table, q_start, kv_len, q, q_out)
-        q_heads, qo = q.shape[1], q_out.data_ptr()
-    rows = rot = 0
-    if table is not None:
-        if table.dim() != 2:
-            raise ValueError("table must have 2 dims (positions, rot)")
-        rows, rot = table.shape
-    _check("kronq_kv4_append", lib().kronq_kv4_append(
-        *qr, *kr, *vr, KV_DTYPES[dt], T, q_heads, qo, _kv_vector(table, "table", torch.float32, rows * rot, dev),
-        rows, rot, 1 if interleaved else 0, _kv_vector(positions, "positions", torch.int32, T, dev),
-        _kv_vector(signs, "signs", torch.int8, D, dev), *args, _kv_vector(info, "info", torch.int32, 1, dev),
-        _kv_stream(stream, dev)))
+    """New keys and values (T x heads x D, bf16 or fp16) into the 4-bit cache, keys and
+    queries rotated on the way (see kronq.h).  q may be None; returns q_out, which is
+    allocated when it is not given."""
+    return _kv4_calls().append(q, k, v, cache, block_table, q_start, kv_len, q_out, table, interleaved, positions,
+                               signs, info, _raw(stream))
 
 
 def kronq_kv4_gather(cache, block_table, q_start, kv_len, k_out, v_out, info=None, stream=None):
     """The values the cache holds for the batch's new tokens (see kronq.h)."""
-    dt = k_out.dtype
-    if dt not in KV_DTYPES or k_out.dim() != 3 or not k_out.is_contiguous():
-        raise ValueError(f"k_out must be contiguous bf16, fp16 or fp32 with 3 dims, got {dt} {tuple(k_out.shape)}")
-    if v_out.dtype is not dt or v_out.shape != k_out.shape or not v_out.is_contiguous():
-        raise ValueError("v_out must be contiguous with k_out's type and shape")
-    T, heads, D = k_out.shape
-    args = _kv_args("kronq_kv4_gather", cache, block_table, q_start, kv_len, D)
-    if args[3] != heads:
-        raise ValueError("kronq_kv4_gather: k_out and the cache differ in their heads")
-    dev = _kv_device(k_out, v_out, cache, block_table, q_start, kv_len)
-    _check("kronq_kv4_gather", lib().kronq_kv4_gather(
-        k_out.data_ptr(), v_out.data_ptr(), KV_DTYPES[dt], T, *args, _kv_vector(info, "info", torch.int32, 1, dev),
-        _kv_stream(stream, dev)))
+    _kv4_calls().gather(cache, block_table, q_start, kv_len, k_out, v_out, info, _raw(stream))
 
 
 def kronq_kv4_attention_workspace_size(T: int, q_heads: int, heads: int, head_dim: int, batch: int) -> int:
@@ -632,27 +544,12 @@ def kv4_workspace(T: int, q_heads: int, heads: int, head_dim: int, batch: int, d
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device or "cuda")
 
 
-def kronq_kv4_attention(q, cache, block_table, q_start, kv_len, out, ws, scale: float, causal: bool = True,
-                        window: int = 0, sinks: int = 0, lse=None, info=None, stream=None):
-    """out = attention of q (T x q_heads x D) over the 4-bit cache (see kronq.h)."""
-    dt = q.dtype
-    if dt not in _KV_ROWS or q.dim() != 3:
-        raise ValueError(f"q must be bf16 or fp16 with 3 dims, got {dt} {tuple(q.shape)}")
-    T, q_heads, D = q.shape
-    qr = _kv_rows(q, "q", dt, T, D)
-    orow = _kv_rows(out, "out", dt, T, D)
-    if out.shape[1] != q_heads:
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
-    if lse is not None and tuple(lse.shape) != (T, q_heads):
-        raise ValueError(f"lse has shape {tuple(lse.shape)}, expected {(T, q_heads)}")
-    args = _kv_args("kronq_kv4_attention", cache, block_table, q_start, kv_len, D)
-    if ws is None or not ws.is_contiguous():
-        raise ValueError("ws must be a contiguous tensor")
-    dev = _kv_device(q, out, cache, block_table, q_start, kv_len, ws)
-    _check("kronq_kv4_attention", lib().kronq_kv4_attention(
-        *qr, KV_DTYPES[dt], T, q_heads, *args, scale, 1 if causal else 0, window, sinks, *orow,
-        _kv_vector(lse, "lse", torch.float32, T * q_heads, dev), _kv_vector(info, "info", torch.int32, 1, dev),
-        ws.data_ptr(), ws.numel() * ws.element_size(), _kv_stream(stream, dev)))
+def kronq_kv4_attention(q, cache, block_table, q_start, kv_len, out=None, ws=None, scale: float | None = None,
+                        causal: bool = True, window: int = 0, sinks: int = 0, lse=None, info=None, stream=None):
+    """Attention of q (T x q_heads x D) over the 4-bit cache (see kronq.h); returns out.
+    out and ws are allocated when they are not given, scale is D^-1/2."""
+    return _kv4_calls().attention(q, cache, block_table, q_start, kv_len, out, ws, scale, causal, window, sinks,
+                                  lse, info, _raw(stream))
 
 
 TIMERS = {"lazy_update": 0, "chol_update": 1, "chol_panel": 2, "obs_block": 3}

@@ -1,4 +1,5 @@
-"""Build libkronq.so in-tree with nvcc for sm_100a (B200).
+"""Build libkronq.so in-tree with nvcc for sm_100a (B200), and _kv4.so, the torch
+binding of its 4-bit cache calls, with the host compiler.
 
 Usage: python -m post_quantization_02_b200.build [--force]
 """
@@ -17,6 +18,8 @@ SRC = HERE / "csrc"
 INCLUDE = HERE.parent / "include"
 OBJ = HERE / "_build"
 LIB = HERE / "libkronq.so"
+BINDING = HERE / "_kv4.so"
+BINDING_SRC = SRC / "kv4_torch.cpp"
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17",
@@ -49,7 +52,36 @@ def up_to_date() -> bool:
     return all(p.stat().st_mtime <= t for p in _deps())
 
 
+def _build_binding(force: bool = False) -> None:
+    """_kv4.so beside libkronq.so, which it finds by its own place."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    if not force and BINDING.exists() and BINDING.stat().st_mtime >= max(
+            p.stat().st_mtime for p in (BINDING_SRC, *INCLUDE.glob("*.h"))):
+        return
+    lib = pathlib.Path(torch.__file__).resolve().parent / "lib"
+    cuda = pathlib.Path(nvcc()).resolve().parents[1]
+    inc = [f"-I{p}" for p in (*cpp_extension.include_paths(), sysconfig.get_path("include"), cuda / "include")]
+    tmp = BINDING.with_suffix(".so.tmp")
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *inc, str(BINDING_SRC), "-o", str(tmp), f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           f"-L{HERE}", "-l:libkronq.so", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building the torch binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> pathlib.Path:
+    lib = _build_lib(force, verbose)
+    _build_binding(force)
+    return lib
+
+
+def _build_lib(force: bool, verbose: bool) -> pathlib.Path:
     if not force and up_to_date():
         return LIB
     OBJ.mkdir(exist_ok=True)

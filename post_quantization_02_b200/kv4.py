@@ -19,8 +19,6 @@ given are allocated on the current stream.
 
 from __future__ import annotations
 
-import functools
-
 import torch
 
 from . import abi
@@ -50,11 +48,8 @@ def append(q, k, v, cache, block_table, q_start, kv_len, rope=None, interleaved:
         with torch.cuda.stream(stream):
             return append(q, k, v, cache, block_table, q_start, kv_len, rope, interleaved, positions, signs,
                           q_out, info)
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    abi.kronq_kv4_append(q, k, v, cache, block_table, q_start, kv_len, q_out, rope, interleaved, positions,
-                         signs, info)
-    return q_out
+    return abi.kronq_kv4_append(q, k, v, cache, block_table, q_start, kv_len, q_out, rope, interleaved, positions,
+                                signs, info)
 
 
 def gather(cache, block_table, q_start, kv_len, tokens: int, head_dim: int, dtype=torch.bfloat16,
@@ -64,12 +59,7 @@ def gather(cache, block_table, q_start, kv_len, tokens: int, head_dim: int, dtyp
     if stream is not None:
         with torch.cuda.stream(stream):
             return gather(cache, block_table, q_start, kv_len, tokens, head_dim, dtype, info)
-    k, v = torch.empty((2, tokens, cache.shape[1], head_dim), dtype=dtype, device=cache.device)
-    abi.kronq_kv4_gather(cache, block_table, q_start, kv_len, k, v, info)
-    return k, v
-
-
-_workspace_size = functools.lru_cache(maxsize=1024)(abi.kronq_kv4_attention_workspace_size)
+    return abi._kv4_calls().gather_new(cache, block_table, q_start, kv_len, tokens, head_dim, dtype, info)
 
 
 def attend(q, cache, block_table, q_start, kv_len, scale: float | None = None, causal: bool = True,
@@ -80,12 +70,5 @@ def attend(q, cache, block_table, q_start, kv_len, scale: float | None = None, c
     if stream is not None:
         with torch.cuda.stream(stream):
             return attend(q, cache, block_table, q_start, kv_len, scale, causal, window, sinks, out, lse, ws, info)
-    T, Hq, D = q.shape
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if ws is None:
-        nbytes = _workspace_size(T, Hq, cache.shape[1], D, kv_len.shape[0])
-        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
-    abi.kronq_kv4_attention(q, cache, block_table, q_start, kv_len, out, ws, D ** -0.5 if scale is None else scale,
-                            causal, window, sinks, lse, info)
-    return out
+    return abi.kronq_kv4_attention(q, cache, block_table, q_start, kv_len, out, ws, scale, causal, window, sinks,
+                                   lse, info)
