@@ -432,8 +432,8 @@ size_t kronq_kv4_block_bytes(int page_size, int head_dim);
  * on the pairs (i, i + rot/2) or, interleaved, (2i, 2i + 1), i < rot/2; row p
  * of `table` (table_rows x rot fp32, 16-byte aligned) holds the rot/2 cosines
  * and then the sines of position p; p is positions[row] or, when that is NULL,
- * the token's index.  Then, when `signs` (head_dim int8, +-1) is given, the
- * signed Hadamard transform x -> head_dim^-1/2 H (signs x) of every head, as
+ * the token's index.  Then, when `signs` (head_dim int8, +-1, 8-byte aligned) is
+ * given, the signed Hadamard transform x -> head_dim^-1/2 H (signs x) of every head, as
  * kronq_biip_rotate applies it: it spreads outlier channels over the head,
  * and scores of equally transformed queries and keys do not change.
  * Keys (after that) and values: the 4-bit grid of each vector,

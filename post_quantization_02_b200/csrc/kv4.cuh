@@ -59,6 +59,41 @@ KQ_DEV float max_nan(float a, float b) {
   return r;
 }
 
+// Two fp32 in one 64-bit register: one instruction for both.
+using f32x2 = unsigned long long;
+KQ_DEV f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+KQ_DEV float2 unpack2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+KQ_DEV f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+KQ_DEV f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+KQ_DEV f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+KQ_DEV f32x2 neg2(f32x2 a) { return a ^ 0x8000000080000000ull; }
+// (a, b) -> (a + b, a - b)
+KQ_DEV void butterfly(f32x2& a, f32x2& b) {
+  const f32x2 s = add2(a, b);
+  b = add2(a, neg2(b));
+  a = s;
+}
+
 KQ_DEV float to_f32(uint16_t h, int dt) {
   return dt == BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
 }

@@ -15,11 +15,14 @@
 // whole rest).  A vector with a NaN or an infinity, or wider than fp32, gets a
 // NaN scale: it reads back as NaN instead of as some other value.
 //
-// Split: 8 lanes per vector (a query, key or value head of one token), four
-// vectors of the same token per warp; lane l holds dims 8 l + 64 r .. + 8, so
-// loads are 16 bytes per lane and 128 bytes per vector and r, the first three
-// butterflies and the last (D/64) are inside the lane, three go by shuffle, and
-// a run of 8 dims is one word of codes.
+// Split: 8 lanes per vector (a query, key or value head of one token), four vectors
+// of the same token per warp; lane l holds dims 8 l + 64 r .. + 8, so loads are 16
+// bytes per lane and 128 bytes per vector and r, the first three butterflies and the
+// last (D/64) are inside the lane, three go by shuffle, and a run of 8 dims is one
+// word of codes.  (64 dims per lane, with fewer shuffles, needs 160 registers: a fifth
+// slower.)  What bounds it is instructions, so fp32 operations go in packed pairs, a
+// block looks its token's place up once for all its vectors, and the first vector is
+// asked for before that.
 #include "kv4.cuh"
 
 namespace {
@@ -44,7 +47,7 @@ struct AppendArgs {
   const int32_t* positions;
   const int8_t* signs;
   int64_t table_rows;
-  int T, Hq, dt, rot, interleaved, blocks_per_token;
+  int T, Hq, dt, rot, interleaved;
   int32_t* info;
 };
 
@@ -57,190 +60,266 @@ KQ_DEV int64_t page_of(const Batch& b, const Cache& c, int s, int at) {
   return id >= 0 && id < c.pages ? id : -1;
 }
 
-template <int D>
+// Products that are rounded by themselves: packed ones (and fused ones with a zero) are
+// contracted with the packed sum behind them.
+KQ_DEV f32x2 mul2_rn(f32x2 a, f32x2 b) {
+  const float2 x = unpack2(a), y = unpack2(b);
+  return pack2(__fmul_rn(x.x, y.x), __fmul_rn(x.y, y.y));
+}
+
+// x: dims 8 l + 64 r + 2 i and the next, in the order written above, packed in pairs.
+template <int D, int DT>
 __global__ void __launch_bounds__(TPB) kv4_append_kernel(const AppendArgs a) {
   constexpr int R = D / 64;
-  const int i = blockIdx.x / a.blocks_per_token;
-  const int item = (blockIdx.x - i * a.blocks_per_token) * ITEMS + (threadIdx.x >> 3);
-  const int l = threadIdx.x & 7;
-  const int s = find_sequence(a.b.q_start, a.b.B, i);
-  if (s < 0 || s >= a.b.B) return;                       // a row of no sequence (whole warp)
-  const int at = a.b.kv_len[s] - (a.b.q_start[s + 1] - i);
-  const int Hkv = a.cache.heads;
-  const bool act = item < a.Hq + 2 * Hkv;
-  const int kind = item < a.Hq ? 0 : item < a.Hq + Hkv ? 1 : 2;   // query, key, value
-  const int head = kind == 0 ? item : kind == 1 ? item - a.Hq : item - a.Hq - Hkv;
-  const Rows& src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-
-  int64_t pos = a.positions ? a.positions[i] : at;
-  bool ok = act && at >= 0;
-  if (a.rot && (pos < 0 || pos >= a.table_rows)) ok = false;
-  int64_t page = -1;
-  if (ok && kind) {
-    page = page_of(a.b, a.cache, s, at);
-    if (page < 0) ok = false;
-  }
-  if (act && !ok) {
-    if (l == 0) kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
-  }
-
-  float x[R][8];
-  if (ok) {
-    const uint16_t* p = src.p + (int64_t)i * src.st + (int64_t)head * src.sh;
+  const int i = blockIdx.x, l = threadIdx.x & 7;
+  const int Hkv = a.cache.heads, items = a.Hq + 2 * Hkv;
+  int item = blockIdx.y * ITEMS + (threadIdx.x >> 3);
+  const int stride = gridDim.y * ITEMS;
+  // the first vector is asked for before its place is looked up (every row may be read)
+  uint4 in[R];
+  auto source = [&](int it, const Rows** src) -> const uint16_t* {
+    const int kind = it < a.Hq ? 0 : it < a.Hq + Hkv ? 1 : 2;
+    const int head = kind == 0 ? it : kind == 1 ? it - a.Hq : it - a.Hq - Hkv;
+    *src = kind == 0 ? &a.q : kind == 1 ? &a.k : &a.v;
+    return (*src)->p + (int64_t)i * (*src)->st + (int64_t)head * (*src)->sh;
+  };
+  auto ask = [&](int it) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) load8(p + 8 * l + 64 * r, src.vec, a.dt, x[r]);
-    if (kind < 2 && a.rot) {
-      const int half = a.rot >> 1;
-      const float* row = a.table + pos * a.rot;
+    for (int r = 0; r < R; ++r) in[r] = make_uint4(0u, 0u, 0u, 0u);
+    if (it < items) {
+      const Rows* src;
+      const uint16_t* p = source(it, &src) + 8 * l;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int d = 8 * l + 64 * r;
-        if (d >= a.rot) continue;
-        if (a.interleaved) {
+        if (src->vec) {
+          in[r] = __ldg(reinterpret_cast<const uint4*>(p + 64 * r));
+        } else {
+          uint32_t w[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[j] = __ldg(p + 64 * r + j);
+          in[r] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+        }
+      }
+    }
+  };
+  ask(item);
+  const int s = find_sequence(a.b.q_start, a.b.B, i);
+  if (s < 0 || s >= a.b.B) return;                       // a row of no sequence
+  const int at = a.b.kv_len[s] - (a.b.q_start[s + 1] - i);
+  const int64_t pos = a.positions ? a.positions[i] : at;
+  const bool placed = at >= 0 && (!a.rot || (pos >= 0 && pos < a.table_rows));
+  const int64_t page = placed ? page_of(a.b, a.cache, s, at) : -1;
+  if (page < 0 && threadIdx.x == 0) kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
+  const float* row = a.table + (placed && a.rot ? pos * a.rot : 0);
+  const int half = a.rot >> 1;
+  // +-1 for each dim of this lane
+  f32x2 sg[R][4];
+  if (a.signs) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(a.signs + 8 * l + 64 * r));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t u = k < 2 ? w.x : w.y;
+        sg[r][k] = pack2(__uint_as_float(0x3f800000u | ((u << (24 - 16 * (k & 1))) & 0x80000000u)),
+                         __uint_as_float(0x3f800000u | ((u << (16 - 16 * (k & 1))) & 0x80000000u)));
+      }
+    }
+  }
+
+  for (; item - (int)(threadIdx.x >> 3) < items; item += stride) {      // (the same in all threads)
+    const int kind = item < a.Hq ? 0 : item < a.Hq + Hkv ? 1 : 2;
+    const int head = kind == 0 ? item : kind == 1 ? item - a.Hq : item - a.Hq - Hkv;
+    const bool ok = item < items && placed && (kind == 0 || page >= 0);
+    f32x2 x[R][4];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float v[8];
+      unpack8(in[r], DT, v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[r][k] = pack2(v[2 * k], v[2 * k + 1]);
+    }
+    if (ok && kind < 2 && a.rot) {
+      if (!a.interleaved && a.rot == D && R > 1) {
+        // the two halves of a pair are runs r and r + R / 2 of this lane
+#pragma unroll
+        for (int r = 0; r < R / 2; ++r) {
+          const ulonglong2* co = reinterpret_cast<const ulonglong2*>(row + 8 * l + 64 * r);
+          const ulonglong2* si = reinterpret_cast<const ulonglong2*>(row + half + 8 * l + 64 * r);
+#pragma unroll
+          for (int k2 = 0; k2 < 2; ++k2) {
+            const ulonglong2 c2 = __ldg(co + k2), s2 = __ldg(si + k2);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const f32x2 c = k ? c2.y : c2.x, sn = k ? s2.y : s2.x;
+              f32x2 &u = x[r][2 * k2 + k], &w = x[r + R / 2][2 * k2 + k];
+              const f32x2 y = add2(mul2_rn(u, c), mul2_rn(w, neg2(sn)));
+              w = add2(mul2_rn(w, c), mul2_rn(u, sn));
+              u = y;
+            }
+          }
+        }
+      } else if (a.interleaved) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int d = 8 * l + 64 * r;
+          if (d >= a.rot) continue;
           const float4 co = __ldg(reinterpret_cast<const float4*>(row + d / 2));
           const float4 si = __ldg(reinterpret_cast<const float4*>(row + half + d / 2));
           const float c4[4] = {co.x, co.y, co.z, co.w}, s4[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float u = x[r][2 * j], w = x[r][2 * j + 1];
-            x[r][2 * j] = __fsub_rn(__fmul_rn(u, c4[j]), __fmul_rn(w, s4[j]));
-            x[r][2 * j + 1] = __fadd_rn(__fmul_rn(w, c4[j]), __fmul_rn(u, s4[j]));
+          for (int k = 0; k < 4; ++k) {
+            const float2 v = unpack2(x[r][k]);
+            x[r][k] = add2(mul2_rn(x[r][k], pack2(c4[k], c4[k])), mul2_rn(pack2(v.y, v.x), pack2(-s4[k], s4[k])));
           }
-        } else {
-          // the other half of each pair is a run of another lane (or of this
-          // one): read again, from L1
+        }
+      } else {
+        // the other half of each pair is a run of another lane (or of this one): read
+        // again, from L1
+        const Rows* src;
+        const uint16_t* p = source(item, &src);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int d = 8 * l + 64 * r;
+          if (d >= a.rot) continue;
           const bool up = d >= half;
           const int e = up ? d - half : d;
+          const float g = up ? 1.f : -1.f;
           float o[8];
-          load8(p + (up ? e : e + half), src.vec, a.dt, o);
+          load8(p + (up ? e : e + half), src->vec, DT, o);
 #pragma unroll
-          for (int j4 = 0; j4 < 2; ++j4) {
-            const float4 co = __ldg(reinterpret_cast<const float4*>(row + e + 4 * j4));
-            const float4 si = __ldg(reinterpret_cast<const float4*>(row + half + e + 4 * j4));
-            const float c4[4] = {co.x, co.y, co.z, co.w}, s4[4] = {si.x, si.y, si.z, si.w};
+          for (int k2 = 0; k2 < 2; ++k2) {
+            const float4 co = __ldg(reinterpret_cast<const float4*>(row + e + 4 * k2));
+            const float4 si = __ldg(reinterpret_cast<const float4*>(row + half + e + 4 * k2));
+            const f32x2 c[2] = {pack2(co.x, co.y), pack2(co.z, co.w)};
+            const f32x2 sn[2] = {pack2(g * si.x, g * si.y), pack2(g * si.z, g * si.w)};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float u = __fmul_rn(x[r][4 * j4 + j], c4[j]), w = __fmul_rn(o[4 * j4 + j], s4[j]);
-              x[r][4 * j4 + j] = up ? __fadd_rn(u, w) : __fsub_rn(u, w);
-            }
+            for (int k = 0; k < 2; ++k)
+              x[r][2 * k2 + k] = add2(mul2_rn(x[r][2 * k2 + k], c[k]),
+                                      mul2_rn(pack2(o[4 * k2 + 2 * k], o[4 * k2 + 2 * k + 1]), sn[k]));
           }
         }
       }
     }
-  } else {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[r][j] = 0.f;
-  }
+    // (the next vector comes while this one is transformed)
+    ask(item + stride);
 
-  if (a.signs) {                                          // (all lanes: shuffles)
-    if (kind < 2) {
+    if (a.signs && __any_sync(0xffffffffu, kind < 2)) {
+      f32x2 y[R][4];
+      const f32x2 minus = pack2(-1.f, -1.f);
+      auto butterfly = [&](f32x2& u, f32x2& w) {
+        const f32x2 t = add2(u, w);
+        w = fma2(w, minus, u);
+        u = t;
+      };
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int r = 0; r < R; ++r) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[r][j] = a.signs[8 * l + 64 * r + j] < 0 ? -x[r][j] : x[r][j];
-    }
-    float y[R][8];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[r][j] = x[r][j];
-#pragma unroll
-    for (int h = 1; h < 8; h *= 2)
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (!(j & h)) {
-            const float u = y[r][j], w = y[r][j + h];
-            y[r][j] = __fadd_rn(u, w);
-            y[r][j + h] = __fsub_rn(u, w);
-          }
-#pragma unroll
-    for (int h = 1; h < 8; h *= 2)
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float w = __shfl_xor_sync(0xffffffffu, y[r][j], h);
-          y[r][j] = (l & h) ? __fsub_rn(w, y[r][j]) : __fadd_rn(y[r][j], w);
+        for (int k = 0; k < 4; ++k) {                       // distance 1
+          const float2 v = unpack2(mul2(x[r][k], sg[r][k]));     // (exact)
+          y[r][k] = pack2(__fadd_rn(v.x, v.y), __fsub_rn(v.x, v.y));
         }
+        butterfly(y[r][0], y[r][1]);                        // 2
+        butterfly(y[r][2], y[r][3]);
+        butterfly(y[r][0], y[r][2]);                        // 4
+        butterfly(y[r][1], y[r][3]);
+      }
 #pragma unroll
-    for (int h = 1; h < R; h *= 2)
+      for (int h = 1; h < 8; h *= 2) {                      // 8, 16, 32: other lanes
+        const float g = (l & h) ? -1.f : 1.f;
+        const f32x2 g2 = pack2(g, g);
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (!(r & h))
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float u = y[r][j], w = y[r + h][j];
-            y[r][j] = __fadd_rn(u, w);
-            y[r + h][j] = __fsub_rn(u, w);
-          }
-    constexpr float norm = D == 64 ? 0.125f : D == 128 ? 0.08838834764831845f : 0.0625f;
-    if (kind < 2) {
+          for (int k = 0; k < 4; ++k) y[r][k] = fma2(y[r][k], g2, __shfl_xor_sync(0xffffffffu, y[r][k], h));
+      }
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int h = 1; h < R; h *= 2)                        // 64, 128
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[r][j] = __fmul_rn(y[r][j], norm);
-    }
-  }
-
-  if (kind == 0) {
-    if (ok) {
-      uint16_t* o = a.q_out + ((int64_t)i * a.Hq + head) * D;
+        for (int r = 0; r < R; ++r)
+          if (!(r & h))
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-        *reinterpret_cast<uint4*>(o + 8 * l + 64 * r) = pack8(x[r], a.dt);
-    }
-  }
-  // a warp that holds only queries is done; in a mixed warp all lanes go on
-  if (__all_sync(0xffffffffu, kind == 0)) return;
-
-  float lo = 0.f, hi = 0.f;
+            for (int k = 0; k < 4; ++k) butterfly(y[r][k], y[r + h][k]);
+      constexpr float norm = D == 64 ? 0.125f : D == 128 ? 0.08838834764831845f : 0.0625f;
+      const f32x2 n2 = pack2(norm, norm);
+      if (kind < 2) {
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      lo = min_nan(lo, x[r][j]);
-      hi = max_nan(hi, x[r][j]);
-    }
-#pragma unroll
-  for (int h = 1; h < 8; h *= 2) {
-    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, h));
-    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, h));
-  }
-  if (!ok || kind == 0) return;
-  float sc = fmaxf(__fmul_rn(__fsub_rn(hi, lo), 1.f / 15.f), 0x1p-100f);
-  if (!(__fsub_rn(hi, lo) < INFINITY)) sc = INFINITY;     // NaN, infinite or too wide
-  sc = __uint_as_float((__float_as_uint(sc) + 8u) & ~15u);
-  uint32_t word, code[R];
-  if (sc < INFINITY) {
-    const float rs = __fdiv_rn(1.f, sc);
-    const float z = fminf(fmaxf(rintf(__fmul_rn(-lo, rs)), 0.f), 15.f);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      code[r] = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float c = fminf(fmaxf(__fadd_rn(rintf(__fmul_rn(x[r][j], rs)), z), 0.f), 15.f);
-        // c is a whole number: adding 2^23 leaves it in the low mantissa bits
-        code[r] |= (__float_as_uint(__fadd_rn(c, 8388608.f)) & 15u) << (4 * j);
+          for (int k = 0; k < 4; ++k) x[r][k] = mul2(y[r][k], n2);
       }
     }
-    word = __float_as_uint(sc) | (uint32_t)z;
-  } else {
-    word = 0x7FC00000u;
+
+    if (kind == 0 && ok) {
+      uint16_t* o = a.q_out + ((int64_t)i * a.Hq + head) * D + 8 * l;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 w = unpack2(x[r][k]);
+          v[2 * k] = w.x;
+          v[2 * k + 1] = w.y;
+        }
+        *reinterpret_cast<uint4*>(o + 64 * r) = pack8(v, DT);
+      }
+    }
+    // a warp that holds only queries is done with them; in a mixed warp all lanes go on
+    if (__all_sync(0xffffffffu, kind == 0 || !ok)) continue;
+
+    float lo = 0.f, hi = 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 v = unpack2(x[r][k]);
+        lo = min_nan(lo, min_nan(v.x, v.y));
+        hi = max_nan(hi, max_nan(v.x, v.y));
+      }
+#pragma unroll
+    for (int h = 1; h < 8; h *= 2) {
+      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, h));
+      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, h));
+    }
+    if (!ok || kind == 0) continue;
+    float sc = fmaxf(__fmul_rn(__fsub_rn(hi, lo), 1.f / 15.f), 0x1p-100f);
+    if (!(__fsub_rn(hi, lo) < INFINITY)) sc = INFINITY;     // NaN, infinite or too wide
+    sc = __uint_as_float((__float_as_uint(sc) + 8u) & ~15u);
+    uint32_t word = 0x7FC00000u, code[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) code[r] = 0;
-  }
-  const int P = a.cache.P, slot = at & (P - 1);
-  uint8_t* blk = a.cache.base + (page * Hkv + head) * (int64_t)a.cache.block_bytes;
-  uint32_t* codes = reinterpret_cast<uint32_t*>(blk + (kind == 2 ? P * (D / 2) : 0)) + slot * (D / 8);
-  uint32_t* words = reinterpret_cast<uint32_t*>(blk + P * D) + (kind == 2 ? P : 0);
+    if (sc < INFINITY) {
+      // 1.5 2^23 + y is rounded to a whole number as rint rounds y (|y| <= 16); the code
+      // is clamped there and taken from the low bits
+      constexpr float M = 12582912.f;
+      const float rs = __fdiv_rn(1.f, sc);
+      const float z = fminf(fmaxf(rintf(__fmul_rn(-lo, rs)), 0.f), 15.f);
+      const f32x2 rs2 = pack2(rs, rs), m2 = pack2(M, M), z2 = pack2(z, z);
 #pragma unroll
-  for (int r = 0; r < R; ++r) codes[l + 8 * r] = code[r];
-  if (l == 0) words[slot] = word;
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 y = unpack2(add2(add2(mul2_rn(x[r][k], rs2), m2), z2));
+          code[r] |= (__float_as_uint(fminf(fmaxf(y.x, M), M + 15.f)) & 15u) << (8 * k) |
+                     (__float_as_uint(fminf(fmaxf(y.y, M), M + 15.f)) & 15u) << (8 * k + 4);
+        }
+      word = __float_as_uint(sc) | (uint32_t)z;
+    }
+    const int P = a.cache.P, slot = at & (P - 1);
+    uint8_t* blk = a.cache.base + (page * Hkv + head) * (int64_t)a.cache.block_bytes;
+    uint32_t* codes = reinterpret_cast<uint32_t*>(blk + (kind == 2 ? P * (D / 2) : 0)) + slot * (D / 8);
+#pragma unroll
+    for (int r = 0; r < R; ++r) codes[l + 8 * r] = code[r];
+    if (l == 0) (reinterpret_cast<uint32_t*>(blk + P * D) + (kind == 2 ? P : 0))[slot] = word;
+  }
+}
+
+template <int D>
+void launch_append(const AppendArgs& a, dim3 grid, cudaStream_t st) {
+  if (a.dt == BF16)
+    kv4_append_kernel<D, BF16><<<grid, TPB, 0, st>>>(a);
+  else
+    kv4_append_kernel<D, FP16><<<grid, TPB, 0, st>>>(a);
 }
 
 struct GatherArgs {
@@ -348,7 +427,7 @@ int kq_kv4_append(const void* q, int64_t q_st, int64_t q_sh, const void* k, int6
   if (dtype != BF16 && dtype != FP16) return KRONQ_ERR_UNSUPPORTED;
   if (T < 0 || Hq < 0 || Hq > 65535 || rot < 0 || rot > D || rot % 16) return KRONQ_ERR_INVALID_ARG;
   if (rot && (!table || table_rows <= 0 || !kqh::aligned(table, 16))) return KRONQ_ERR_INVALID_ARG;
-  if (!kqh::aligned(positions, 4)) return KRONQ_ERR_INVALID_ARG;
+  if (!kqh::aligned(positions, 4) || !kqh::aligned(signs, 8)) return KRONQ_ERR_INVALID_ARG;
   if (T == 0) return KRONQ_OK;
   AppendArgs a = {};
   if (!rows_ok(k, k_st, k_sh, &a.k) || !rows_ok(v, v_st, v_sh, &a.v)) return KRONQ_ERR_INVALID_ARG;
@@ -366,17 +445,18 @@ int kq_kv4_append(const void* q, int64_t q_st, int64_t q_sh, const void* k, int6
   a.dt = dtype;
   a.rot = rot;
   a.interleaved = interleaved;
-  a.blocks_per_token = (Hq + 2 * c.heads + ITEMS - 1) / ITEMS;
   a.info = info;
-  if (T > INT32_MAX / a.blocks_per_token) return KRONQ_ERR_UNSUPPORTED;
+  if (T > INT32_MAX) return KRONQ_ERR_UNSUPPORTED;
   a.T = (int)T;
-  const unsigned grid = (unsigned)(T * a.blocks_per_token);
+  // a block per token; with few tokens their vectors are spread over more blocks
+  const int passes = (Hq + 2 * c.heads + ITEMS - 1) / ITEMS;
+  const dim3 grid((unsigned)T, T < 8 * kqh::num_sms() ? (unsigned)passes : 1u);
   if (D == 64)
-    kv4_append_kernel<64><<<grid, TPB, 0, st>>>(a);
+    launch_append<64>(a, grid, st);
   else if (D == 128)
-    kv4_append_kernel<128><<<grid, TPB, 0, st>>>(a);
+    launch_append<128>(a, grid, st);
   else
-    kv4_append_kernel<256><<<grid, TPB, 0, st>>>(a);
+    launch_append<256>(a, grid, st);
   KQ_CHECK_LAUNCH();
   return KRONQ_OK;
 }

@@ -149,33 +149,6 @@ KQ_DEV uint32_t load4(const uint32_t* p) {
   return v;
 }
 
-// Two fp32 in one 64-bit register: one instruction for both.
-using f32x2 = unsigned long long;
-KQ_DEV f32x2 pair(float lo, float hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-KQ_DEV float2 halves(f32x2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-KQ_DEV f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-KQ_DEV f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-KQ_DEV f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 KQ_DEV float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -597,7 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     // the running maximum, a whole number, and how far scores may pass it; 0 and -infinity's
     // neighbour until the row has seen a key
     float m = 0.f, lag = -0x1.fffffep127f;
-    f32x2 l2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+    f32x2 l2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
     bool ok = true;
     auto step = [&](auto is_masked, int j, int key0) {
       constexpr bool masked = decltype(is_masked)::value;
@@ -607,7 +580,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       const uint32_t gone = masked ? num.absent : 0u;
       f32x2 t[BN / 2];             // scores relative to the running maximum
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      const f32x2 neg_m = pair(-m, -m), row2 = BF ? pair(row * num.down, row * num.down) : 0ull;
+      const f32x2 neg_m = pack2(-m, -m), row2 = BF ? pack2(row * num.down, row * num.down) : 0ull;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float x[32];
@@ -621,14 +594,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
           for (int k = 0; k < 2; ++k) {
             const int e = 4 * i + 2 * k;
             f32x2& tc = t[16 * h + 2 * i + k];
-            tc = fma2(pair(x[e], x[e + 1]), k ? f.y : f.x, neg_m);
-            float2 v = halves(tc);
+            tc = fma2(pack2(x[e], x[e + 1]), k ? f.y : f.x, neg_m);
+            float2 v = unpack2(tc);
             if constexpr (masked) {
               const int key = key0 + 32 * h + e;
               const bool page = !((gone >> (2 * h + (e >> 4))) & 1u);
               if (!(page && key < hi && (key >= lo || key < a.sinks))) v.x = -INFINITY;
               if (!(page && key + 1 < hi && (key + 1 >= lo || key + 1 < a.sinks))) v.y = -INFINITY;
-              tc = pair(v.x, v.y);
+              tc = pack2(v.x, v.y);
             }
             top[i & 3] = max3(top[i & 3], v.x, v.y);
           }
@@ -642,7 +615,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         const float al = up && lag == LAG ? exp2_approx(-by) : 1.f;
         if (up) lag = LAG;
         m += by;
-        const f32x2 down = pair(-by, -by), al2 = pair(al, al);
+        const f32x2 down = pack2(-by, -by), al2 = pack2(al, al);
         l2[0] = mul2(l2[0], al2);
         l2[1] = mul2(l2[1], al2);
 #pragma unroll
@@ -671,10 +644,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
           const ulonglong2 f = BF ? make_ulonglong2(0ull, 0ull) : sv[8 * h + i];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float2 v = halves(t[16 * h + 2 * i + k]);
-            const f32x2 p = pair(exp2_approx(v.x), exp2_approx(v.y));
+            const float2 v = unpack2(t[16 * h + 2 * i + k]);
+            const f32x2 p = pack2(exp2_approx(v.x), exp2_approx(v.y));
             l2[k] = add2(l2[k], p);
-            float2 w = halves(BF ? p : mul2(p, k ? f.y : f.x));
+            float2 w = unpack2(BF ? p : mul2(p, k ? f.y : f.x));
             if constexpr (masked && !BF) {                     // (0 times a NaN scale)
               if (v.x == -INFINITY) w.x = 0.f;
               if (v.y == -INFINITY) w.y = 0.f;
@@ -703,7 +676,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       }
     }
     // ---- output
-    const float2 ls = halves(add2(l2[0], l2[1]));
+    const float2 ls = unpack2(add2(l2[0], l2[1]));
     const float l = ls.x + ls.y;
     if (steps > 0) ok = ok && wait(&ctl.o_full, 0);
     kq::tc_fence_after();
