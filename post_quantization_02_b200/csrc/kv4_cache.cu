@@ -69,7 +69,7 @@ KQ_DEV f32x2 mul2_rn(f32x2 a, f32x2 b) {
 
 // x: dims 8 l + 64 r + 2 i and the next, in the order written above, packed in pairs.
 template <int D, int DT>
-__global__ void __launch_bounds__(TPB) kv4_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(TPB, D == 64 ? 6 : D == 128 ? 5 : 4) kv4_append_kernel(const AppendArgs a) {
   constexpr int R = D / 64;
   const int i = blockIdx.x, l = threadIdx.x & 7;
   const int Hkv = a.cache.heads, items = a.Hq + 2 * Hkv;
