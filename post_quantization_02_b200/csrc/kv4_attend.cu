@@ -172,16 +172,16 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
   __shared__ __align__(16) Plan plans[WARPS];
 
   Unit u;
-  if (!find_unit<R, BLK, THREADS>(a, blockIdx.x, &u)) return;
-  const int head = blockIdx.y;
+  if (!find_unit<R, BLK, THREADS>(a, &u)) return;
+  const int head = u.head;
   // (only a batch whose rows overlap can ask for more slots than there are)
-  if (u.nsplit > 1 && (u.slot0 < 0 || u.slot0 + (int)blockIdx.x - u.base >= a.slots)) {
+  if (u.nsplit > 1 && (u.slot < 0 || u.slot >= a.slots)) {
     kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
     return;
   }
   const Seq s = seq_of(a, u.b, nullptr);
   if (threadIdx.x == 0 && head == 0 && u.tile == 0 && u.split == 0)
-    a.meta[u.b] = make_int2(u.slot0, u.nsplit);
+    a.meta[u.b] = make_int2(u.slot, u.nsplit);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gr = lane >> 2, t = lane & 3;
   const int rows = s.n * a.g, r0 = u.tile * R;
@@ -544,6 +544,7 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
     }
   }
   copy_wait<0>();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge kernel, which waits
   flush();
   __syncthreads();                       // the rings become the joining buffer
 
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
       }
     }
   __syncthreads();
-  const int64_t slot = ((int64_t)(u.slot0 + (int)blockIdx.x - u.base) * a.cache.heads + head) * R;
+  const int64_t slot = ((int64_t)u.slot * a.cache.heads + head) * R;
   for (int e = threadIdx.x; e < R * (D / 4); e += THREADS) {
     const int r = e / (D / 4), d4 = e - r * (D / 4);
     if (r0 + r >= rows) break;
@@ -617,12 +618,14 @@ __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, 
   constexpr int E = D / 32;
   __shared__ __align__(16) float sum_o[WARPS][D];
   __shared__ float sum_l[WARPS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = blockIdx.x;
   const int b = find_sequence(a.b.q_start, a.b.B, i);
+  const Seq s = seq_of(a, min(max(b, 0), a.b.B - 1), nullptr);
+  // the attention kernel's results from here on (every thread waits: this kernel's
+  // end stands for that one's too)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (b < 0 || b >= a.b.B) return;
-  const Seq s = seq_of(a, b, nullptr);
   if (i < s.row0 || i >= s.row0 + s.n) return;
   const int2 mt = a.meta[b];
   const int ns = mt.y;
@@ -690,10 +693,10 @@ __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, 
 
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
-constexpr unsigned long long TARGET = 148ull * 12;   // units over all heads
+constexpr int SMS = 148;
 constexpr int MIN_CHUNK = 2;                         // 256 keys
+constexpr float UNIT_COST = 1.5f, PROMPT_UNIT_COST = 5.f;
 constexpr int64_t PROMPT_ROWS = 16;
-constexpr unsigned long long PROMPT_TARGET = 148ull * 4;
 constexpr int PROMPT_MIN_KEYS = 512;
 
 // How a call is run.  Rows per sequence and key/value head decide (on average:
@@ -701,14 +704,15 @@ constexpr int PROMPT_MIN_KEYS = 512;
 // there are.
 struct Way {
   bool prompt;
-  int R, BLK, min_chunk;
-  unsigned long long target;
+  int R, BLK, min_chunk, resident;
+  float unit_cost;
 };
 
 Way way_of(int64_t T, int g, int D, int64_t B) {
   if (T * g > PROMPT_ROWS * B)
-    return {true, prompt_rows(D), prompt_block(D), PROMPT_MIN_KEYS / prompt_block(D), PROMPT_TARGET};
-  return {false, D == 256 || T * g <= 8 * B ? 8 : 16, BLK, MIN_CHUNK, TARGET};
+    return {true, prompt_rows(D), prompt_block(D), PROMPT_MIN_KEYS / prompt_block(D), SMS, PROMPT_UNIT_COST};
+  const int R = D == 256 || T * g <= 8 * B ? 8 : 16;
+  return {false, R, BLK, MIN_CHUNK, SMS * (D == 256 || R == 16 ? 2 : 4), UNIT_COST};
 }
 
 struct Layout {
@@ -716,7 +720,7 @@ struct Layout {
 };
 
 Layout layout_of(const Way& w, int D, int heads, int64_t B) {
-  const size_t rows = (size_t)max_slots(heads, w.target) * heads * w.R;
+  const size_t rows = (size_t)max_slots(heads, w.resident) * heads * w.R;
   Layout l;
   l.meta = 0;
   l.ml = up256((size_t)B * sizeof(int2));
@@ -728,14 +732,13 @@ Layout layout_of(const Way& w, int D, int heads, int64_t B) {
 template <int D, int NT>
 int launch(AttendArgs& a, cudaStream_t st) {
   constexpr int R = 8 * NT;
-  const long long ux = max_units(a.T, a.g, a.b.B, R, a.cache.heads, a.target);
-  if (ux > INT32_MAX) return KRONQ_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)ux, (unsigned)a.cache.heads);
-  constexpr int rings = WARPS * RING * Step<D>::BYTES, join = WARPS * R * D * (int)sizeof(float);
+  const long long grid = max_units(a, R, BLK);
+  if (grid > INT32_MAX) return KRONQ_ERR_UNSUPPORTED;
+    constexpr int rings = WARPS * RING * Step<D>::BYTES, join = WARPS * R * D * (int)sizeof(float);
   constexpr int smem = rings > join ? rings : join;
   static kqh::PerDevice attr;
   if (kqh::smem_attr_once(attr, kv4_attend_kernel<D, NT>, smem) <= 0) return KRONQ_ERR_CUDA;
-  kv4_attend_kernel<D, NT><<<grid, THREADS, smem, st>>>(a);
+  kv4_attend_kernel<D, NT><<<(unsigned)grid, THREADS, smem, st>>>(a);
   KQ_CHECK_LAUNCH();
   return KRONQ_OK;
 }
@@ -818,8 +821,9 @@ int kq_kv4_attention(const void* q, int64_t q_st, int64_t q_sh, int dtype, int64
   a.scale_log2 = scale * 1.4426950408889634f;
   const Way way = way_of(T, g, D, b.B);
   a.min_chunk = way.min_chunk;
-  a.target = way.target;
-  a.slots = (int)max_slots(c.heads, way.target);
+  a.resident = way.resident;
+  a.unit_cost = way.unit_cost;
+  a.slots = (int)max_slots(c.heads, way.resident);
   a.info = info;
   const Layout w = layout_of(way, D, c.heads, b.B);
   uint8_t* base = static_cast<uint8_t*>(ws);

@@ -8,11 +8,15 @@
 //
 // Lengths are on the device (a captured graph serves any), so the division is
 // made there: every block adds up the work of the batch, sets the chunk of key
-// blocks that gives about `target` units, and finds its own (sequence, tile,
-// split) in the running sum of units.  A sequence with one split is written
+// blocks of one unit, and finds its own (sequence, tile, split) in the running
+// sum of units.  The chunk is chosen for whole waves: of eight that give between
+// one and two units for each of the `resident` blocks the device holds at a time, the
+// one with the least waves x (mean unit + a unit's fixed cost).  A sequence with one split is written
 // straight to the output; the units of the others leave partial results, in
 // slots counted over those sequences alone, that kv4_merge_kernel joins.
 #pragma once
+
+#include <algorithm>
 
 #include "kv4.cuh"
 
@@ -35,7 +39,8 @@ struct AttendArgs {
   int causal, window, sinks;
   float scale_log2;      // softmax scale x log2 e
   int min_chunk;         // key blocks
-  unsigned long long target;
+  int resident;          // blocks on the device at a time
+  float unit_cost;       // what a unit costs beside its key blocks, in key blocks
   float* part_o;         // slots x heads x R x D
   Part* part_ml;         // slots x heads x R
   int2* meta;            // per sequence: first slot, splits
@@ -49,7 +54,7 @@ struct Seq {
 
 struct Unit {
   int b, tile, split, nsplit;
-  int base, slot0;       // the sequence's first unit and first slot
+  int head, slot;        // its key/value head; its slot, if it is one of several splits
 };
 
 struct Span {
@@ -97,32 +102,85 @@ KQ_DEV Span span_of(const AttendArgs& a, const Seq& s, int q0, int q1) {
   return r;
 }
 
-// Finds unit u (all threads of the block call it; false: there is none).
+// Units aimed at, in eighths of `resident`.
+constexpr int CHOICES = 8;
+KQ_DEV int eighths(int k) { return k < 7 ? 8 + k : 16; }
+
+// Finds the block's unit (all threads call it; false: there is none); heads change
+// fastest, so blocks without one come last.  Of up to 32
+// sequences every warp finds it by itself, one sequence a lane, without a barrier.
+// Work and costs are fp32 sums in one order, so all blocks agree; the chunk is
+// rounded up by more than their error, which keeps max_units a bound.
 template <int R, int BLK, int THREADS>
-KQ_DEV bool find_unit(const AttendArgs& a, int u, Unit* out) {
-  __shared__ unsigned long long sums[THREADS / 32];
-  __shared__ unsigned long long wsum[THREADS / 32];
+KQ_DEV bool find_unit(const AttendArgs& a, Unit* out) {
+  constexpr int WARPS = THREADS / 32;
+  __shared__ float sums[WARPS];
+  __shared__ uint32_t counts[WARPS][CHOICES];
+  __shared__ unsigned long long wsum[WARPS];
   __shared__ Unit found;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int u = blockIdx.x / a.cache.heads;
+  out->head = blockIdx.x - u * a.cache.heads;
+  const bool wide = a.b.B > 32;
   const int per = ceil_div(a.b.B, THREADS);
-  const int b0 = min(a.b.B, tid * per), b1 = min(a.b.B, b0 + per);
+  const int b0 = min(a.b.B, wide ? tid * per : lane), b1 = min(a.b.B, b0 + per);
   int tiles1 = 0, blocks1 = 0;                 // kept when a thread has one sequence
-  unsigned long long mine = 0;
+  float work = 0.f;
   for (int b = b0; b < b1; ++b) {
     bool bad;
     seq_work<R, BLK>(a, seq_of(a, b, &bad), &tiles1, &blocks1);
-    if (bad && (blockIdx.x | blockIdx.y) == 0) kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
-    mine += (unsigned long long)tiles1 * blocks1;
+    if (bad && blockIdx.x == 0) kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
+    work += (float)tiles1 * (float)blocks1;
   }
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sums[warp] = mine;
-  if (tid == 0) found.b = -1;
-  __syncthreads();
-  unsigned long long total = 0;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) total += sums[w];
-  const unsigned long long c = (total * a.cache.heads + a.target - 1) / a.target;
-  const int chunk = (int)max((unsigned long long)a.min_chunk, c);
+  for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+  if (wide) {
+    if (lane == 0) sums[warp] = work;
+    if (tid == 0) found.b = -1;
+    __syncthreads();
+    work = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) work += sums[w];
+  }
+  work *= a.cache.heads;
+  // lane k: the chunk of choice k % CHOICES
+  const float aim = 0.125f * (float)(eighths(lane % CHOICES) * a.resident);
+  const int mine_c = (int)fmaxf((float)a.min_chunk, ceilf(fminf(__fdividef(work, aim) * (1.00001f + per * 0x1p-23f), 0x1p30f)));
+  int chunk = __shfl_sync(0xffffffffu, mine_c, 0);
+  if (chunk > a.min_chunk) {                   // (the same in all threads)
+    const float mine_r = __frcp_rn((float)mine_c);
+    float n[CHOICES], r[CHOICES];
+#pragma unroll
+    for (int k = 0; k < CHOICES; ++k) {
+      n[k] = 0.f;
+      r[k] = __shfl_sync(0xffffffffu, mine_r, k);
+    }
+    for (int b = b0; b < b1; ++b) {
+      if (per > 1) seq_work<R, BLK>(a, seq_of(a, b, nullptr), &tiles1, &blocks1);
+#pragma unroll
+      for (int k = 0; k < CHOICES; ++k)
+        n[k] += (float)tiles1 * fmaxf(1.f, ceilf((float)blocks1 * r[k]));
+    }
+    uint32_t units = 0;                        // lane k: of choice k % CHOICES
+#pragma unroll
+    for (int k = 0; k < CHOICES; ++k) {
+      const uint32_t x = __reduce_add_sync(0xffffffffu, (uint32_t)n[k]);
+      if (lane % CHOICES == k) units = x;
+    }
+    if (wide) {
+      if (lane < CHOICES) counts[warp][lane] = units;
+      __syncthreads();
+      units = 0;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) units += counts[w][lane % CHOICES];
+    }
+    const float all = (float)units * a.cache.heads;
+    const float waves = __fdividef(all, (float)a.resident);
+    const float cost = ceilf(waves) * __fdividef(work, all) + waves * a.unit_cost;
+    const uint32_t best =
+        __reduce_min_sync(0xffffffffu, (__float_as_uint(cost) & ~7u) | (lane % CHOICES));
+    chunk = __shfl_sync(0xffffffffu, mine_c, best & 7);
+  }
   // low half: units; high half: those that need a slot
   unsigned long long units = 0;
   for (int b = b0; b < b1; ++b) {
@@ -132,37 +190,52 @@ KQ_DEV bool find_unit(const AttendArgs& a, int u, Unit* out) {
     units += k + (ns > 1 ? k << 32 : 0);
   }
   unsigned long long incl = units;
+#pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const unsigned long long x = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += x;
   }
-  if (lane == 31) wsum[warp] = incl;
-  __syncthreads();
   unsigned long long before = incl - units;
+  if (wide) {
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w)
-    if (w < warp) before += wsum[w];
+    for (int w = 0; w < WARPS; ++w)
+      if (w < warp) before += wsum[w];
+  }
   int base = (int)(uint32_t)before, slot0 = (int)(before >> 32);
+  Unit x = {-1, 0, 0, 1, out->head, 0};
   if (u >= base && u < base + (int)(uint32_t)units) {
     for (int b = b0; b < b1; ++b) {
       if (per > 1) seq_work<R, BLK>(a, seq_of(a, b, nullptr), &tiles1, &blocks1);
       const int ns = max(1, ceil_div(blocks1, chunk)), k = tiles1 * ns;
       if (u < base + k) {
-        found.tile = (u - base) / ns;
-        found.split = u - base - found.tile * ns;
-        found.nsplit = ns;
-        found.base = base;
-        found.slot0 = slot0;
-        found.b = b;
+        x.tile = (u - base) / ns;
+        x.split = u - base - x.tile * ns;
+        x.nsplit = ns;
+        x.slot = slot0 + u - base;
+        x.b = b;
         break;
       }
       base += k;
       if (ns > 1) slot0 += k;
     }
+    if (wide) found = x;
   }
-  __syncthreads();
-  *out = found;
-  return found.b >= 0;
+  if (wide) {
+    __syncthreads();
+    *out = found;
+    return found.b >= 0;
+  }
+  const uint32_t has = __ballot_sync(0xffffffffu, x.b >= 0);
+  if (!has) return false;
+  const int src = __ffs(has) - 1;
+  out->b = src;
+  out->tile = __shfl_sync(0xffffffffu, x.tile, src);
+  out->split = __shfl_sync(0xffffffffu, x.split, src);
+  out->nsplit = __shfl_sync(0xffffffffu, x.nsplit, src);
+  out->slot = __shfl_sync(0xffffffffu, x.slot, src);
+  return true;
 }
 
 // Four dims from d on of one output row from its sum relative to 2^m; a row
@@ -194,12 +267,16 @@ int launch_prompt(const AttendArgs& a, int D, cudaStream_t st);
 
 // Bounds of what find_unit hands out: a sequence with t tiles and w key blocks
 // has t ceil(w / chunk) <= t + t w / chunk units, and at most twice t w / chunk
-// when it is split.
-inline long long max_units(long long T, int g, int B, int R, int heads, unsigned long long target) {
-  return (T * g) / R + B + (long long)(target / heads) + 1;
+// when it is split; the sum of t w / chunk is at most 2 resident / heads.  Blocks
+// without a unit still look for one, so the grid is also kept to what the table's
+// width can give.
+inline long long max_units(const AttendArgs& a, int R, int BLK) {    // of all heads
+  const long long tiles = (long long)a.T * a.g / R + a.b.B;
+  const long long blocks = (((long long)a.b.max_pages << a.cache.lgP) + BLK - 1) / BLK;
+  const long long each = (blocks + a.min_chunk - 1) / a.min_chunk;
+  return a.cache.heads *
+         std::min(tiles + 2 * a.resident / a.cache.heads + 1, tiles * std::max(1ll, each));
 }
-inline long long max_slots(int heads, unsigned long long target) {
-  return 2 * (long long)(target / heads) + 2;
-}
+inline long long max_slots(int heads, int resident) { return 4 * resident / heads + 2; }
 
 }  // namespace kv4

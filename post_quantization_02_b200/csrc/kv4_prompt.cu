@@ -204,16 +204,16 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
   uint8_t* kv_smem = q_smem + SH::Q_BYTES;
 
   Unit u;
-  if (!find_unit<R, BN, THREADS>(a, blockIdx.x, &u)) return;
-  const int head = blockIdx.y;
+  if (!find_unit<R, BN, THREADS>(a, &u)) return;
+  const int head = u.head;
   // (only a batch whose rows overlap can ask for more slots than there are)
-  if (u.nsplit > 1 && (u.slot0 < 0 || u.slot0 + (int)blockIdx.x - u.base >= a.slots)) {
+  if (u.nsplit > 1 && (u.slot < 0 || u.slot >= a.slots)) {
     kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
     return;
   }
   const Seq s = seq_of(a, u.b, nullptr);
   if (threadIdx.x == 0 && head == 0 && u.tile == 0 && u.split == 0)
-    a.meta[u.b] = make_int2(u.slot0, u.nsplit);
+    a.meta[u.b] = make_int2(u.slot, u.nsplit);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = s.n * a.g, r0 = u.tile * R;
   const int last = min(rows, r0 + R) - 1;
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     const float rfv = fv != 0.f ? 1.f / fv : 0.f;
     const int rr = 128 * tile + tr;
     const bool mine = r0 + rr < rows;
-    const int64_t slot = ((int64_t)(u.slot0 + (int)blockIdx.x - u.base) * a.cache.heads + head) * R + rr;
+    const int64_t slot = ((int64_t)u.slot * a.cache.heads + head) * R + rr;
     const int hq = head * a.g + r - qi * a.g;
     if (ok) {
 #pragma unroll 1
@@ -726,12 +726,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
 template <int D, bool BF>
 int launch(const AttendArgs& a, cudaStream_t st) {
   using SH = Shape<D>;
-  const long long ux = max_units(a.T, a.g, a.b.B, SH::R, a.cache.heads, a.target);
-  if (ux > INT32_MAX) return KRONQ_ERR_UNSUPPORTED;
+  const long long grid = max_units(a, SH::R, prompt_block(D));
+  if (grid > INT32_MAX) return KRONQ_ERR_UNSUPPORTED;
   static kqh::PerDevice attr;
   if (kqh::smem_attr_once(attr, kv4_prompt_kernel<D, BF>, SH::SMEM) <= 0) return KRONQ_ERR_CUDA;
-  const dim3 grid((unsigned)ux, (unsigned)a.cache.heads);
-  kv4_prompt_kernel<D, BF><<<grid, THREADS, SH::SMEM, st>>>(a);
+    kv4_prompt_kernel<D, BF><<<(unsigned)grid, THREADS, SH::SMEM, st>>>(a);
   KQ_CHECK_LAUNCH();
   return KRONQ_OK;
 }
