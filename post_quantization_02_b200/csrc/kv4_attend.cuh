@@ -238,6 +238,15 @@ KQ_DEV bool find_unit(const AttendArgs& a, Unit* out) {
   return true;
 }
 
+KQ_DEV uint2 pack4(float4 o, int dt) {
+  if (dt == BF16) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x, o.y), y = __floats2bfloat162_rn(o.z, o.w);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  }
+  const __half2 x = __floats2half2_rn(o.x, o.y), y = __floats2half2_rn(o.z, o.w);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+}
+
 // Four dims from d on of one output row from its sum relative to 2^m; a row
 // that saw no key is 0 with a log-sum-exp of -inf.
 KQ_DEV void store_row(const AttendArgs& a, int row, int hq, int d, float4 o, float m, float l) {
@@ -247,15 +256,7 @@ KQ_DEV void store_row(const AttendArgs& a, int row, int hq, int d, float4 o, flo
   o.z *= r;
   o.w *= r;
   uint16_t* p = static_cast<uint16_t*>(a.out) + (int64_t)row * a.o_st + (int64_t)hq * a.o_sh + d;
-  uint2 w;
-  if (a.dt == BF16) {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x, o.y), y = __floats2bfloat162_rn(o.z, o.w);
-    w = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-  } else {
-    const __half2 x = __floats2half2_rn(o.x, o.y), y = __floats2half2_rn(o.z, o.w);
-    w = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-  }
-  *reinterpret_cast<uint2*>(p) = w;
+  *reinterpret_cast<uint2*>(p) = pack4(o, a.dt);
   if (a.lse && d == 0)
     a.lse[(int64_t)row * a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }

@@ -41,7 +41,7 @@
 namespace kv4 {
 namespace {
 
-constexpr int MMA_WARP0 = 8, NUM_WARP = 10, UNPACK_WARP0 = 11, THREADS = 512;
+constexpr int NUM_QUERY_WARPS = 8, MMA_WARP0 = 8, NUM_WARP = 10, UNPACK_WARP0 = 11, THREADS = 512;
 constexpr int BN = 64, GROUP = 16, GROUPS = BN / GROUP;    // keys per step; that surely share a page
 constexpr int JOB = 32, JOBS = BN / JOB;                   // keys per unpacking job; jobs for a step's keys
 constexpr float NO_MAX = -0x1p127f;     // a split's maximum where it saw no key
@@ -86,7 +86,7 @@ struct alignas(16) Ctl {
   uint64_t num_full[8], num_free[8];
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2][2], p_ready[2][2];  // per tile and buffer
-  uint64_t pv_done[2], o_full;
+  uint64_t pv_done[2], o_full, q_full;
   uint32_t tmem;
   int abort;
   float row[256];                        // bf16: score factor of each row
@@ -249,51 +249,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       kq::mbar_init(&ctl.num_free[i], 4 * tiles + JOBS);   // softmax warps, unpackers of the values
     }
     kq::mbar_init(&ctl.o_full, tiles);
+    kq::mbar_init(&ctl.q_full, NUM_QUERY_WARPS);
     ctl.abort = 0;
     kq::fence_barrier_init();
   }
   if (warp == MMA_WARP0) kq::tmem_alloc(&ctl.tmem, 512);
-  // queries: rows of 128-byte lines, dims of each 8 in the codes' order
-  for (int e = threadIdx.x; e < R * (D / 8); e += THREADS) {
-    const int r = e / (D / 8), c = e - r * (D / 8);
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (r0 + r < rows) {
-      const int qi = (r0 + r) / a.g;
-      const uint16_t* p = a.q + (int64_t)(s.row0 + qi) * a.q_st +
-                          (int64_t)(head * a.g + r0 + r - qi * a.g) * a.q_sh + 8 * c;
-      if (a.q_vec) {
-        v = __ldg(reinterpret_cast<const uint4*>(p));
-      } else {
-        uint32_t h[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = __ldg(p + j);
-        v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-      }
-    }
-    if (BF) {
-      // to fp16 by the power of two that takes the row's largest to about 2^10 (the
-      // D / 8 lanes of a row are neighbours)
-      float x[8];
-      unpack8(v, BF16, x);
-      float big = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(x[j]));
-#pragma unroll
-      for (int o = 1; o < D / 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-      const int e = min(max(137 - (int)(__float_as_uint(big) >> 23), -126), 126);
-      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] *= up;
-      v = pack8(x, FP16);
-      if (c == 0) ctl.row[r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
-    }
-    v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                   __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-    uint8_t* dst = q_smem + ((r >> 7) * ATOMS + (c >> 3)) * 16384 + (r & 127) * 128 +
-                   (((c & 7) ^ (r & 7)) << 4);
-    *reinterpret_cast<uint4*>(dst) = v;
-  }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   kq::tc_fence_before();
   __syncthreads();
   kq::tc_fence_after();
@@ -303,6 +263,66 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
   auto wait = [&](uint64_t* bar, int parity) -> bool {
     return __all_sync(0xffffffffu, kq::mbar_wait(bar, (uint32_t)parity & 1u, abort, a.info));
   };
+
+  if (warp < NUM_QUERY_WARPS) {
+    // Queries: rows of 128-byte lines, dims of each 8 in the codes' order.  The softmax
+    // warps load them while the first keys are unpacked.
+    constexpr int ALL = R * (D / 8) / (32 * NUM_QUERY_WARPS), PART = ALL < 8 ? ALL : 8;
+#pragma unroll 1
+    for (int i = 0; i < ALL; i += PART) {
+      uint4 v[PART];
+#pragma unroll
+      for (int k = 0; k < PART; ++k) {
+        const int e = threadIdx.x + (i + k) * (32 * NUM_QUERY_WARPS);
+        const int r = e / (D / 8), c = e - r * (D / 8);
+        v[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (r0 + r < rows) {
+          const int qi = (r0 + r) / a.g;
+          const uint16_t* p = a.q + (int64_t)(s.row0 + qi) * a.q_st +
+                              (int64_t)(head * a.g + r0 + r - qi * a.g) * a.q_sh + 8 * c;
+          if (a.q_vec) {
+            load16(v[k], reinterpret_cast<const uint4*>(p));
+          } else {
+            uint32_t h[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[j] = __ldg(p + j);
+            v[k] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < PART; ++k) {
+        const int e = threadIdx.x + (i + k) * (32 * NUM_QUERY_WARPS);
+        const int r = e / (D / 8), c = e - r * (D / 8);
+        uint4 w = v[k];
+        if (BF) {
+          // to fp16 by the power of two that takes the row's largest to about 2^10 (the
+          // D / 8 lanes of a row are neighbours)
+          float x[8];
+          unpack8(w, BF16, x);
+          float big = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(x[j]));
+#pragma unroll
+          for (int o = 1; o < D / 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+          const int ex = min(max(137 - (int)(__float_as_uint(big) >> 23), -126), 126);
+          const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] *= up;
+          w = pack8(x, FP16);
+          if (c == 0) ctl.row[r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
+        }
+        w = make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632),
+                       __byte_perm(w.y, w.w, 0x5410), __byte_perm(w.y, w.w, 0x7632));
+        uint8_t* dst = q_smem + ((r >> 7) * ATOMS + (c >> 3)) * 16384 + (r & 127) * 128 +
+                       (((c & 7) ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(dst) = w;
+      }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) kq::mbar_arrive(&ctl.q_full);
+  }
 
   if (warp >= MMA_WARP0 && warp < MMA_WARP0 + tiles) {
     const int tile = warp - MMA_WARP0;
@@ -337,7 +357,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         kq::mma_commit(&ctl.pv_done[tile]);
       }
     };
-    bool ok = true;
+    bool ok = wait(&ctl.q_full, 0);
     for (int j = 0; j < min(steps, 2) && ok; ++j) {
       ok = wait(&ctl.k_full[j], 0);
       if (!ok) break;
@@ -561,6 +581,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     const int tr = (warp & 3) * 32 + lane;              // row within the tile
     const uint32_t tbase = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t o_at = tbase + SH::O_COL + tile * D;
+    bool ok = wait(&ctl.q_full, 0);
     const float row = BF ? ctl.row[128 * tile + tr] : 0.f;
     const int r = min(last, r0 + 128 * tile + tr);
     const int qi = r / a.g;
@@ -571,7 +592,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     // neighbour until the row has seen a key
     float m = 0.f, lag = -0x1.fffffep127f;
     f32x2 l2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
-    bool ok = true;
     auto step = [&](auto is_masked, int j, int key0) {
       constexpr bool masked = decltype(is_masked)::value;
       const uint32_t s_at = tbase + (2 * tile + (j & 1)) * BN;
@@ -682,36 +702,55 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     kq::tc_fence_after();
     const float fv = steps > 0 ? ctl.num[(steps - 1) & 7].fv : 0.f;
     const float rfv = fv != 0.f ? 1.f / fv : 0.f;
-    const int rr = 128 * tile + tr;
-    const bool mine = r0 + rr < rows;
-    const int64_t slot = ((int64_t)u.slot * a.cache.heads + head) * R + rr;
-    const int hq = head * a.g + r - qi * a.g;
+    const bool mine = r0 + 128 * tile + tr < rows;
+    const int64_t slot = ((int64_t)u.slot * a.cache.heads + head) * R + 128 * tile + tr;
+    const int hq = head * a.g + r - qi * a.g, out_row = s.row0 + qi;
+    const bool split = u.nsplit > 1;
     if (ok) {
+      // Through shared memory (the queries and what lies behind them are not needed any more),
+      // so that a warp stores whole rows: a thread has a row, and rows are far apart.  Each
+      // warp has its own 32 rows of D floats; chunk c of 4 of row t lies at c ^ (t & 7).
+      static_assert(SH::Q_BYTES + SH::STAGES * SH::STAGE >= R * D * 4, "room for the output");
+      float* buf = reinterpret_cast<float*>(q_smem) + (128 * tile + (warp & 3) * 32) * D;
+      const float f = split ? rfv : l == 0.f ? 0.f : rfv / l;
 #pragma unroll 1
-      for (int d = 0; d < D; d += 16) {
-        uint32_t o[16];
+      for (int d = 0; d < D; d += 32) {
+        uint32_t o[32];
         if (steps > 0) {
-          tmem_ld16(o_at + d, o);
+          tmem_ld16(o_at + d, reinterpret_cast<uint32_t(&)[16]>(o[0]));
+          tmem_ld16(o_at + d + 16, reinterpret_cast<uint32_t(&)[16]>(o[16]));
           kq::tmem_wait_ld();
         } else {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = 0u;
+          for (int k = 0; k < 32; ++k) o[k] = 0u;
         }
 #pragma unroll
-        for (int k = 0; k < 16; k += 4) {
-          if (!mine) break;
+        for (int k = 0; k < 32; k += 4) {
           // dims 8 (k / 8) + 0..3 are columns 0 2 4 6 of the 8, dims 4..7 columns 1 3 5 7
-          const int b = (k & 8) + ((k >> 2) & 1);
-          const float4 v = make_float4(__uint_as_float(o[b]) * rfv, __uint_as_float(o[b + 2]) * rfv,
-                                       __uint_as_float(o[b + 4]) * rfv, __uint_as_float(o[b + 6]) * rfv);
-          if (u.nsplit > 1) {
-            *reinterpret_cast<float4*>(a.part_o + slot * D + d + k) = v;
-            if (d + k == 0) a.part_ml[slot] = {lag == LAG ? m : NO_MAX, l};
-          } else {
-            store_row(a, s.row0 + qi, hq, d + k, v, m, l);
-          }
+          const int b = (k & 24) + ((k >> 2) & 1);
+          *reinterpret_cast<float4*>(buf + lane * D + 4 * (((d + k) >> 2) ^ (lane & 7))) =
+              make_float4(__uint_as_float(o[b]) * f, __uint_as_float(o[b + 2]) * f,
+                          __uint_as_float(o[b + 4]) * f, __uint_as_float(o[b + 6]) * f);
         }
-        __syncwarp();
+      }
+      // where the lane's row goes
+      uint64_t to = 0;
+      if (mine && split) to = reinterpret_cast<uint64_t>(a.part_o + slot * D);
+      if (mine && !split)
+        to = reinterpret_cast<uint64_t>(static_cast<uint16_t*>(a.out) + (int64_t)out_row * a.o_st +
+                                        (int64_t)hq * a.o_sh);
+      if (mine && split) a.part_ml[slot] = {lag == LAG ? m : NO_MAX, l};
+      if (mine && !split && a.lse)
+        a.lse[(int64_t)out_row * a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      __syncwarp();
+#pragma unroll 8
+      for (int i = 0; i < D / 4; ++i) {
+        constexpr int CHUNKS = D / 4;
+        const int t = (i * 32 + lane) / CHUNKS, c = (i * 32 + lane) % CHUNKS;
+        const uint64_t p = __shfl_sync(0xffffffffu, (unsigned long long)to, t);
+        const float4 x = *reinterpret_cast<const float4*>(buf + t * D + 4 * (c ^ (t & 7)));
+        if (p && split) reinterpret_cast<float4*>(p)[c] = x;
+        if (p && !split) reinterpret_cast<uint2*>(p)[c] = pack4(x, a.dt);
       }
     }
   }
