@@ -255,9 +255,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
   }
   if (warp == MMA_WARP0) kq::tmem_alloc(&ctl.tmem, 512);
   kq::tc_fence_before();
-  __syncthreads();
-  kq::tc_fence_after();
-  const uint32_t tmem = ctl.tmem;
+  // The barriers are set up and tensor memory is there: every warp comes by here once, those
+  // that have something to ask of global memory after asking it.
+  auto set_up = [&]() {
+    asm volatile("bar.sync 0;" ::: "memory");
+    kq::tc_fence_after();
+  };
 
   // a wait of the whole warp: all lanes agree on its outcome
   auto wait = [&](uint64_t* bar, int parity) -> bool {
@@ -267,6 +270,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
   if (warp < NUM_QUERY_WARPS) {
     // Queries: rows of 128-byte lines, dims of each 8 in the codes' order.  The softmax
     // warps load them while the first keys are unpacked.
+    const float rg = 1.f / (float)a.g;
     constexpr int ALL = R * (D / 8) / (32 * NUM_QUERY_WARPS), PART = ALL < 8 ? ALL : 8;
 #pragma unroll 1
     for (int i = 0; i < ALL; i += PART) {
@@ -277,7 +281,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         const int r = e / (D / 8), c = e - r * (D / 8);
         v[k] = make_uint4(0u, 0u, 0u, 0u);
         if (r0 + r < rows) {
-          const int qi = (r0 + r) / a.g;
+          // (the quotient is below 2^9 + 1: half a row off an integer, fp32 does not miss it)
+          const int qi = q_first + (int)(((float)(r0 + r - q_first * a.g) + 0.5f) * rg);
           const uint16_t* p = a.q + (int64_t)(s.row0 + qi) * a.q_st +
                               (int64_t)(head * a.g + r0 + r - qi * a.g) * a.q_sh + 8 * c;
           if (a.q_vec) {
@@ -290,6 +295,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
           }
         }
       }
+      if (i == 0) set_up();
 #pragma unroll
       for (int k = 0; k < PART; ++k) {
         const int e = threadIdx.x + (i + k) * (32 * NUM_QUERY_WARPS);
@@ -322,12 +328,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) kq::mbar_arrive(&ctl.q_full);
+  } else if (warp != NUM_WARP) {
+    set_up();
   }
 
   if (warp >= MMA_WARP0 && warp < MMA_WARP0 + tiles) {
     const int tile = warp - MMA_WARP0;
     // -------------------------------------------------------------- MMAs
-    const uint32_t tm = uniform(tmem), qa = uniform(kq::smem_u32(q_smem)), kv = uniform(kq::smem_u32(kv_smem));
+    const uint32_t tm = uniform(ctl.tmem), qa = uniform(kq::smem_u32(q_smem)), kv = uniform(kq::smem_u32(kv_smem));
     auto issue_s = [&](int j) {
       constexpr uint32_t idesc = kq::idesc_f16(128, BN, 0, 0, 0);
       const uint32_t d = tm + (2 * tile + (j & 1)) * BN;
@@ -423,11 +431,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       }
     };
     Words cur, nxt, after;
-    int page = ask_page(0);
-    if (steps > 0) ask_words(nxt, 0, page);
-    page = ask_page(1);
-    if (steps > 1) ask_words(after, 1, page);
-    page = ask_page(2);
+    const int page0 = ask_page(0), page1 = ask_page(1);
+    int page = ask_page(2);
+    set_up();
+    if (steps > 0) ask_words(nxt, 0, page0);
+    if (steps > 1) ask_words(after, 1, page1);
     float fv = 0.f;
     for (int j = 0; j < steps; ++j) {
       cur = nxt;
@@ -579,7 +587,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     // ---------------------------------------------------------- softmax
     const int tile = NT == 2 ? warp >> 2 : 0;
     const int tr = (warp & 3) * 32 + lane;              // row within the tile
-    const uint32_t tbase = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tbase = ctl.tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t o_at = tbase + SH::O_COL + tile * D;
     bool ok = wait(&ctl.q_full, 0);
     const float row = BF ? ctl.row[128 * tile + tr] : 0.f;
@@ -743,22 +751,39 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       if (mine && !split && a.lse)
         a.lse[(int64_t)out_row * a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       __syncwarp();
-#pragma unroll 8
-      for (int i = 0; i < D / 4; ++i) {
-        constexpr int CHUNKS = D / 4;
-        const int t = (i * 32 + lane) / CHUNKS, c = (i * 32 + lane) % CHUNKS;
-        const uint64_t p = __shfl_sync(0xffffffffu, (unsigned long long)to, t);
-        const float4 x = *reinterpret_cast<const float4*>(buf + t * D + 4 * (c ^ (t & 7)));
-        if (p && split) reinterpret_cast<float4*>(p)[c] = x;
-        if (p && !split) reinterpret_cast<uint2*>(p)[c] = pack4(x, a.dt);
-      }
+      constexpr int CHUNKS = D / 4;
+      auto store = [&](auto is_split) {
+#pragma unroll 1
+        for (int i = 0; i < D / 4; i += 8) {
+          float4 x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int t = ((i + k) * 32 + lane) / CHUNKS, c = ((i + k) * 32 + lane) % CHUNKS;
+            x[k] = *reinterpret_cast<const float4*>(buf + t * D + 4 * (c ^ (t & 7)));
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int t = ((i + k) * 32 + lane) / CHUNKS, c = ((i + k) * 32 + lane) % CHUNKS;
+            const uint64_t p = __shfl_sync(0xffffffffu, (unsigned long long)to, t);
+            if (!p) continue;
+            if constexpr (decltype(is_split)::value)
+              reinterpret_cast<float4*>(p)[c] = x[k];
+            else
+              reinterpret_cast<uint2*>(p)[c] = pack4(x[k], BF ? BF16 : FP16);
+          }
+        }
+      };
+      if (split)
+        store(std::true_type{});
+      else
+        store(std::false_type{});
     }
   }
   kq::tc_fence_before();
   __syncthreads();
   if (warp == MMA_WARP0) {
     kq::tc_fence_after();
-    kq::tmem_dealloc(tmem, 512);
+    kq::tmem_dealloc(ctl.tmem, 512);
   }
 }
 
