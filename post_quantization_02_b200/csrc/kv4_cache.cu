@@ -327,52 +327,95 @@ struct GatherArgs {
   void* v_out;
   Cache cache;
   Batch b;
-  int T, dt, blocks_per_token;
+  int T, dt;
   int32_t* info;
 };
 
-// Reads tokens back as the values they stand for; 8 lanes per vector as above.
-template <int D>
+// Reads tokens back as the values they stand for, the last new tokens of each sequence:
+// bound by the stores (2 bytes or 4 for half a byte read).  A block takes N tokens; their
+// places are looked up once, a warp per token, and 8 lanes read a vector as above.  N = 8
+// keeps four independent loads of a thread in flight; few tokens are spread instead (N = 1).
+template <int D, int N>
 __global__ void __launch_bounds__(TPB) kv4_gather_kernel(const GatherArgs a) {
   constexpr int R = D / 64;
-  const int i = blockIdx.x / a.blocks_per_token;
-  const int item = (blockIdx.x - i * a.blocks_per_token) * ITEMS + (threadIdx.x >> 3);
-  const int l = threadIdx.x & 7;
-  const int s = find_sequence(a.b.q_start, a.b.B, i);
-  if (s < 0 || s >= a.b.B) return;
-  const int Hkv = a.cache.heads;
-  if (item >= 2 * Hkv) return;
-  const int isv = item >= Hkv, head = isv ? item - Hkv : item;
-  const int at = a.b.kv_len[s] - (a.b.q_start[s + 1] - i);
-  const int64_t page = page_of(a.b, a.cache, s, at);
-  if (page < 0) {
-    if (l == 0) kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
-    return;
-  }
-  const int P = a.cache.P, slot = at & (P - 1);
-  const uint8_t* blk = a.cache.base + (page * Hkv + head) * (int64_t)a.cache.block_bytes;
-  const uint32_t* codes =
-      reinterpret_cast<const uint32_t*>(blk + (isv ? P * (D / 2) : 0)) + slot * (D / 8);
-  const uint32_t word = reinterpret_cast<const uint32_t*>(blk + P * D)[(isv ? P : 0) + slot];
-  const float sc = word_scale(word), z = word_zero(word);
-  const int64_t row = ((int64_t)i * Hkv + head) * D;
-  void* out = isv ? a.v_out : a.k_out;
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const uint32_t c = codes[l + 8 * r];
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      x[j] = __fmul_rn(sc, __fsub_rn(__uint_as_float(0x4B000000u | ((c >> (4 * j)) & 15u)), 8388608.f + z));
-    const int64_t o = row + 8 * l + 64 * r;
-    if (a.dt == FP32) {
-      float4* f = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
-      f[0] = make_float4(x[0], x[1], x[2], x[3]);
-      f[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o) = pack8(x, a.dt);
+  __shared__ const uint8_t* place[N];      // the page's block of head 0, or null
+  __shared__ int slots[N];
+  const int Hkv = a.cache.heads, P = a.cache.P, lane = threadIdx.x & 31;
+  for (int n = threadIdx.x >> 5; n < N; n += TPB / 32) {
+    const int i = blockIdx.x * N + n;
+    const uint8_t* p = nullptr;
+    int slot = 0;
+    if (i < a.T) {                         // (the same in the whole warp)
+      const int s = find_sequence(a.b.q_start, a.b.B, i);
+      if (s >= 0 && s < a.b.B) {
+        const int at = a.b.kv_len[s] - (a.b.q_start[s + 1] - i);
+        const int64_t page = page_of(a.b, a.cache, s, at);
+        if (page >= 0) {
+          p = a.cache.base + page * Hkv * (int64_t)a.cache.block_bytes;
+          slot = at & (P - 1);
+        } else if (lane == 0) {
+          kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
+        }
+      }
+    }
+    if (lane == 0) {
+      place[n] = p;
+      slots[n] = slot;
     }
   }
+  __syncthreads();
+  const int l = threadIdx.x & 7;
+  constexpr int U = N == 1 ? 1 : 4;        // vectors in flight
+  for (int e0 = threadIdx.x >> 3; e0 < N * 2 * Hkv; e0 += U * ITEMS) {
+    uint32_t word[U], c[U][R];
+    int64_t row[U];                        // of the output, + 2^62: values; negative: none
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int e = min(e0 + u * ITEMS, N * 2 * Hkv - 1);
+      const int n = N == 1 ? 0 : e / (2 * Hkv), item = e - n * (2 * Hkv);
+      const int isv = item >= Hkv, head = isv ? item - Hkv : item, slot = slots[n];
+      const bool here = place[n] && e == e0 + u * ITEMS;
+      // (without a page the pool's first bytes are read, and nothing is stored)
+      const uint8_t* blk = (place[n] ? place[n] : a.cache.base) + head * (int64_t)a.cache.block_bytes;
+      const uint32_t* codes =
+          reinterpret_cast<const uint32_t*>(blk + (isv ? P * (D / 2) : 0)) + slot * (D / 8);
+      word[u] = __ldg(reinterpret_cast<const uint32_t*>(blk + P * D) + (isv ? P : 0) + slot);
+#pragma unroll
+      for (int r = 0; r < R; ++r) c[u][r] = __ldg(codes + l + 8 * r);
+      row[u] = here ? ((((int64_t)(blockIdx.x * N + n) * Hkv + head) * D) | ((int64_t)isv << 62)) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (row[u] < 0) continue;
+      const float sc = word_scale(word[u]), z = word_zero(word[u]);
+      void* out = row[u] >> 62 ? a.v_out : a.k_out;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          x[j] = __fmul_rn(sc, __fsub_rn(__uint_as_float(0x4B000000u | ((c[u][r] >> (4 * j)) & 15u)),
+                                         8388608.f + z));
+        const int64_t o = (row[u] & ((1ll << 62) - 1)) + 8 * l + 64 * r;
+        if (a.dt == FP32) {
+          float4* f = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
+          f[0] = make_float4(x[0], x[1], x[2], x[3]);
+          f[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o) = pack8(x, a.dt);
+        }
+      }
+    }
+  }
+}
+
+template <int D>
+void launch_gather(const GatherArgs& a, cudaStream_t st) {
+  constexpr int N = 8;
+  if (a.T < 8 * kqh::num_sms())
+    kv4_gather_kernel<D, 1><<<(unsigned)a.T, TPB, 0, st>>>(a);
+  else
+    kv4_gather_kernel<D, N><<<(unsigned)((a.T + N - 1) / N), TPB, 0, st>>>(a);
 }
 
 }  // namespace
@@ -473,17 +516,15 @@ int kq_kv4_gather(void* k_out, void* v_out, int dtype, int64_t T, int D, const C
   a.cache = c;
   a.b = b;
   a.dt = dtype;
-  a.blocks_per_token = (2 * c.heads + ITEMS - 1) / ITEMS;
   a.info = info;
-  if (T > INT32_MAX / a.blocks_per_token) return KRONQ_ERR_UNSUPPORTED;
+  if (T > INT32_MAX - 8) return KRONQ_ERR_UNSUPPORTED;
   a.T = (int)T;
-  const unsigned grid = (unsigned)(T * a.blocks_per_token);
   if (D == 64)
-    kv4_gather_kernel<64><<<grid, TPB, 0, st>>>(a);
+    launch_gather<64>(a, st);
   else if (D == 128)
-    kv4_gather_kernel<128><<<grid, TPB, 0, st>>>(a);
+    launch_gather<128>(a, st);
   else
-    kv4_gather_kernel<256><<<grid, TPB, 0, st>>>(a);
+    launch_gather<256>(a, st);
   KQ_CHECK_LAUNCH();
   return KRONQ_OK;
 }
