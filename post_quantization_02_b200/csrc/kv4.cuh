@@ -87,12 +87,6 @@ KQ_DEV f32x2 add2(f32x2 a, f32x2 b) {
   return r;
 }
 KQ_DEV f32x2 neg2(f32x2 a) { return a ^ 0x8000000080000000ull; }
-// (a, b) -> (a + b, a - b)
-KQ_DEV void butterfly(f32x2& a, f32x2& b) {
-  const f32x2 s = add2(a, b);
-  b = add2(a, neg2(b));
-  a = s;
-}
 
 KQ_DEV float to_f32(uint16_t h, int dt) {
   return dt == BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));

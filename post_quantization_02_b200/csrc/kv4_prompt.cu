@@ -33,6 +33,12 @@
 // Dims stay in the order unpacking yields within each 8 (0 4 1 5 2 6 3 7): queries
 // are stored that way and the output is put right when it leaves.
 //
+// Measured: two chunks of 2048 tokens over 16k, 32 query heads of 128, bf16: 1.31 ms,
+// 785 TFLOP/s of the two products; bound by the softmax warps (one exponential and some
+// five more instructions per score and row, 256 rows a step), which the MMAs wait for.
+// A unit costs some 12 us beside its steps (division of the work, first loads, output):
+// 1777 tokens under a window of 1024, heads of 256: 204 us, 380 TFLOP/s.
+//
 // All waits are bounded; one that gives up records KRONQ_ERR_TIMEOUT in `info`.
 #include <type_traits>
 
@@ -206,14 +212,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
   Unit u;
   if (!find_unit<R, BN, THREADS>(a, &u)) return;
   const int head = u.head;
+  if (threadIdx.x == 0 && head == 0 && u.tile == 0 && u.split == 0)
+    a.meta[u.b] = make_int2(u.slot, u.nsplit);
   // (only a batch whose rows overlap can ask for more slots than there are)
   if (u.nsplit > 1 && (u.slot < 0 || u.slot >= a.slots)) {
     kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
     return;
   }
   const Seq s = seq_of(a, u.b, nullptr);
-  if (threadIdx.x == 0 && head == 0 && u.tile == 0 && u.split == 0)
-    a.meta[u.b] = make_int2(u.slot, u.nsplit);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = s.n * a.g, r0 = u.tile * R;
   const int last = min(rows, r0 + R) - 1;

@@ -12,6 +12,11 @@ exact probabilities, V the cached values and o the exact output,
 Ex: scores are sums of head_dim fp16 x 4-bit products in fp32: head_dim roundings
 (counted at 2^-23, a truncating sum) of at most scale sum_d |q_d| s_j 15, twice
 (codes, zero point).  Ea: one rounding of 2^-23 per 16 keys and 64 for joins.
+
+Many rows per key and bf16 queries: keys and values themselves are rounded to fp16.
+A key's dim is off by 2^-11 |k_jd|, and by 2^-25 of a step's largest scale where it
+is a subnormal: Ex gets scale sum_d |q_d| (2^-11 |k_jd| + 2^-24 15 max s).  A value is
+the rounded product of its codes and its rounded scale: two more 2^-11 sum_j p_j |V_j|.
 """
 
 import numpy as np
@@ -98,6 +103,7 @@ def check_attention(st, q, out, scale, causal=True, window=0, sinks=0, lse=None,
     eps = torch.finfo(dt).eps
     qh, oh = f64(q), f64(out)
     g = q.shape[1] // st.heads
+    rounded = dt == torch.bfloat16 and st.start[-1] * g > 16 * len(st.kv)
     for b in range(len(st.kv)) if seqs is None else seqs:
         if st.new[b] == 0:
             continue
@@ -118,8 +124,12 @@ def check_attention(st, q, out, scale, causal=True, window=0, sinks=0, lse=None,
                     continue
                 pr, vh = pr[mask], v[kh][mask]
                 ex = 2 * st.D * 2.0 ** -23 * scale * np.abs(qh[row, h]).sum() * 15 * ks[kh][mask].max()
+                if rounded:
+                    qa = np.abs(qh[row, h])
+                    ex += scale * (2.0 ** -11 * (np.abs(k[kh][mask]) @ qa).max()
+                                   + 2.0 ** -24 * 15 * qa.sum() * ks[kh][mask].max())
                 ea = 2.0 ** -23 * (mask.sum() / 16 + 64)
-                tol = (eps / 2 * np.abs(o) + (2.0 ** -11 + 2 * ex) * (pr @ np.abs(vh))
+                tol = (eps / 2 * np.abs(o) + ((3 if rounded else 1) * 2.0 ** -11 + 2 * ex) * (pr @ np.abs(vh))
                        + ea * 30 * (pr @ vs[kh][mask]) + torch.finfo(dt).tiny)
                 bad = np.abs(got - o) > tol
                 assert not bad.any(), (b, i, h, np.abs(got - o)[bad][:4], tol[bad][:4])
@@ -297,6 +307,9 @@ def test_attention_empty_rows(cuda):
     (128, 64, 1, 4, "fp16", 300, 1, 150, 0, 0),
     (64, 64, 1, 2, "fp16", 3000, 1, 7, 0, 0),
     (128, 64, 1, 4, "bf16", 2, 5, 12345, 0, 0),
+    (128, 64, 2, 4, "fp16", 40, 1, 9000, 0, 0),
+    (64, 32, 2, 2, "bf16", 33, 2, 6000, 1500, 4),
+    (256, 64, 2, 2, "fp16", 50, 1, 3000, 0, 0),
 ])
 def test_attention_long_and_many(cuda, D, P, heads, g, dtype, B, n, L, window, sinks):
     """Split sequences, and more sequences than a block has threads."""
@@ -321,6 +334,14 @@ def test_attention_long_and_many(cuda, D, P, heads, g, dtype, B, n, L, window, s
     (64, 64, 2, 1, "fp16", [400], [1300], True, 64, 0),
     (128, 64, 1, 2, "fp16", [200, 33], [500, 40], False, 0, 0),
     (128, 256, 1, 1, "bf16", [300, 0, 200], [300, 50, 100], True, 0, 0),
+    # wide heads, a few steps and many; one row behind a tile
+    (256, 64, 2, 4, "bf16", [33, 64, 65], [33, 64, 129], True, 0, 0),
+    (256, 16, 1, 4, "fp16", [300, 200], [2000, 2100], True, 64, 0),
+    (256, 64, 1, 8, "bf16", [129], [3000], True, 1024, 16),
+    (64, 128, 1, 16, "bf16", [17, 33], [64, 2049], True, 0, 0),
+    # new tokens of decoding sequences beside a prompt's, some without any key
+    (128, 64, 2, 4, "bf16", [1, 300, 1, 2, 4], [700, 900, 33, 2000, 2], True, 0, 0),
+    (128, 32, 2, 4, "fp16", [1, 300, 1, 2, 4], [700, 900, 33, 2000, 0], True, 50, 3),
 ])
 def test_attention_prompts(cuda, D, P, heads, g, dtype, new, kv, causal, window, sinks):
     """Many query rows per key."""
@@ -521,6 +542,57 @@ def test_decode_loop_in_a_graph(cuda):
         if i in (1, 2, 11, 12, steps - 1):
             for (q, o), window in zip(outs, (0, 9)):
                 check_attention(st, q, o, D ** -0.5, True, window, 2 if window else 0)
+
+
+@pytest.mark.parametrize("new", [3, 70])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_attention_unaligned(cuda, new, dtype):
+    """Queries that no 16-byte load fits, outputs on 8-byte boundaries, rows apart."""
+    r = np.random.default_rng(20 + new)
+    st = Setup(cuda, r, [new, 2], [400, 130], 2, 128, 64)
+    st.fill(r)
+    T, H, D = st.T, 6, 128
+    q = torch.randn(1 + T * H * (D + 1), device=cuda).to(dtype)[1:].view(T, H, D + 1)[..., :D]
+    buf = torch.full((4 + T * (H * (D + 4) + 8),), 3.0, dtype=dtype, device=cuda)
+    out = buf.as_strided((T, H, D), (H * (D + 4) + 8, D + 4, 1), 4)
+    kv4.attend(q, st.cache, *st.args, out=out)
+    check_attention(st, q, out, D ** -0.5)
+    out.fill_(3.0)
+    assert (buf == 3).all()                        # nothing between the rows was written
+
+
+@pytest.mark.parametrize("new", [1, 100])
+def test_shared_pages(cuda, new):
+    """Two sequences over the same pages (a shared prompt), each with its own length."""
+    r = np.random.default_rng(21)
+    st = Setup(cuda, r, [new, new], [3000, 2500], 2, 128, 64)
+    st.bt[1, :40] = st.bt[0, :40]
+    st.args = (t(st.bt, cuda),) + st.args[1:]
+    st.fill_fast(torch.Generator(cuda).manual_seed(2))
+    q = torch.randn(st.T, 8, 128, device=cuda).half()
+    check_attention(st, q, kv4.attend(q, st.cache, *st.args), 128 ** -0.5, rows=[0, 50, 99])
+
+
+@pytest.mark.parametrize("new,n", [(2, 150), (64, 150), (200, 10)])
+def test_overlapping_rows(cuda, new, n):
+    """Many sequences that claim the same rows ask for more blocks than the grid has: noticed, and
+    nothing outside the output is touched (a workspace full of large numbers leads nowhere)."""
+    r = np.random.default_rng(22)
+    L = 4000
+    st = Setup(cuda, r, [new], [L], 1, 128, 64)
+    st.fill_fast(torch.Generator(cuda).manual_seed(3))
+    q = torch.randn(new, 4, 128, device=cuda).bfloat16()
+    start = np.zeros(2 * n, dtype=np.int32)
+    start[1::2] = new                              # every second sequence has the rows, the others fewer than none
+    bt = np.repeat(st.bt, 2 * n - 1, 0)
+    info = torch.zeros(1, dtype=torch.int32, device=cuda)
+    need = abi.kronq_kv4_attention_workspace_size(new, 4, 1, 128, 2 * n - 1)
+    ws = torch.full((need + 4096,), 127, dtype=torch.uint8, device=cuda)
+    out = torch.full((new + 2, 4, 128), 5.0, dtype=torch.bfloat16, device=cuda)
+    kv4.attend(q, st.cache, t(bt, cuda), t(start, cuda), i32([L] * (2 * n - 1), cuda), out=out[:new],
+               ws=ws[:-4096], info=info)
+    torch.cuda.synchronize()
+    assert info.item() == -1 and (ws[-4096:] == 127).all() and (out[new:] == 5).all()
 
 
 def test_merging_by_log_sum_exp(cuda):
