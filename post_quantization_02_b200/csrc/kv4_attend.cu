@@ -179,14 +179,14 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
   Unit u;
   if (!find_unit<R, BLK, THREADS>(a, &u)) return;
   const int head = u.head;
-  if (threadIdx.x == 0 && head == 0 && u.tile == 0 && u.split == 0)
-    a.meta[u.b] = make_int2(u.slot, u.nsplit);
   // (only a batch whose rows overlap can ask for more slots than there are)
   if (u.nsplit > 1 && (u.slot < 0 || u.slot >= a.slots)) {
     kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
     return;
   }
   const Seq s = seq_of(a, u.b, nullptr);
+  if (threadIdx.x == 0 && head == 0 && u.tile == 0 && u.split == 0)
+    a.meta[u.b] = make_int2(u.slot, u.nsplit);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gr = lane >> 2, t = lane & 3;
   const int rows = s.n * a.g, r0 = u.tile * R;
@@ -702,12 +702,21 @@ size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 constexpr int SMS = 148;
 constexpr int MIN_CHUNK = 2;                         // 256 keys
 constexpr float UNIT_COST = 1.5f, PROMPT_UNIT_COST = 5.f;
-constexpr int64_t PROMPT_ROWS = 16;
 constexpr int PROMPT_MIN_KEYS = 512;
 
-// How a call is run.  Rows per sequence and key/value head decide (on average:
-// lengths are on the device): the tensor-memory kernel fills 128 rows whatever
-// there are.
+// How a call is run.  Rows per sequence and key/value head decide (on average: lengths
+// are on the device).  The tensor-memory kernel's time is that of 128 rows (256: the
+// second tile rides along) whatever there are; the other's grows with every 16 (head_dim
+// 256: 8), and per row it is the slower one:
+//   rows            16    24    32    48    64    80    96
+//   head_dim 128    39    60    61    77   103   135   151     8 sequences of 8k, 8 heads
+//                   95    97    98   100   102   104   106     (us; this kernel, kv4_prompt.cu)
+//   head_dim 256    65    82   110   160   192
+//                  129   131   132   135   138
+//   head_dim 64     30    46    47    59    79   113   116
+//                   73    75    75    77    79    82    84
+// Tiles of 8 rows (twice the blocks per SM) where 8 are enough: 16 rows take 42 us with
+// them, 39 with tiles of 16.
 struct Way {
   bool prompt;
   int R, BLK, min_chunk, resident;
@@ -715,7 +724,7 @@ struct Way {
 };
 
 Way way_of(int64_t T, int g, int D, int64_t B) {
-  if (T * g > PROMPT_ROWS * B)
+  if (T * g > (D == 256 ? 40 : 64) * B)
     return {true, prompt_rows(D), prompt_block(D), PROMPT_MIN_KEYS / prompt_block(D), SMS, PROMPT_UNIT_COST};
   const int R = D == 256 || T * g <= 8 * B ? 8 : 16;
   return {false, R, BLK, MIN_CHUNK, SMS * (D == 256 || R == 16 ? 2 : 4), UNIT_COST};

@@ -103,7 +103,7 @@ def check_attention(st, q, out, scale, causal=True, window=0, sinks=0, lse=None,
     eps = torch.finfo(dt).eps
     qh, oh = f64(q), f64(out)
     g = q.shape[1] // st.heads
-    rounded = dt == torch.bfloat16 and st.start[-1] * g > 16 * len(st.kv)
+    rounded = dt == torch.bfloat16 and st.start[-1] * g > (40 if st.D == 256 else 64) * len(st.kv)
     for b in range(len(st.kv)) if seqs is None else seqs:
         if st.new[b] == 0:
             continue
