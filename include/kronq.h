@@ -483,7 +483,7 @@ int kronq_kv4_gather(void* k_out, void* v_out, int dtype, int64_t T,
  * maximum and times the value's scale, are rounded to fp16 for the product.
  * bf16 queries with more than 64 rows (new tokens x query heads of a group; 40 at
  * head_dim 256) per sequence on average: keys and values are rounded to fp16 too, once or twice
- * 2^-11 relative to each, where the output is rounded at 2^-9.
+ * 2^-11 relative to each, where the output is rounded at 2^-8.
  *
  * q (T x q_heads x head_dim), out (same): KRONQ_BF16 or KRONQ_FP16, strides in
  * elements as above; out 8-byte aligned with strides that are multiples of 4.

@@ -3,10 +3,11 @@
 The compute lives in libkronq.so (C ABI: include/kronq.h), built in-tree by
 ``post_quantization_02_b200.build``.  ``abi`` binds each entry point under its
 C name; ``pipeline`` chains them for one sublayer; ``alloc`` is the host-side
-mixed-precision bit allocation.
+mixed-precision bit allocation; ``kv4`` is the 4-bit key/value cache of a served
+model.
 """
 
-from . import abi  # noqa: F401
+from . import abi, kv4  # noqa: F401
 from .abi import (  # noqa: F401
     KronqError,
     kronq_abi_version,
