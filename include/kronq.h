@@ -408,7 +408,7 @@ int kronq_unpack(const uint32_t* packed, int64_t m, int64_t n, int bits,
  * ones included, so new token i has index kv_len[b] - (q_start[b+1] -
  * q_start[b]) + i; tokens page_size t .. lie in page block_table[b table_ld + t],
  * t < max_pages.  Rows in front of q_start[0] and from q_start[batch] up to T
- * are padding: never read, never written.  Pages may be shared between
+ * are padding: what they hold does not matter, and they are never written.  Pages may be shared between
  * sequences for reading; two new tokens must not have the same place.
  *
  * A batch that contradicts itself or the cache (a length beyond the table or
