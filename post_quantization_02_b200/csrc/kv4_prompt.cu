@@ -19,7 +19,8 @@
 // One block = up to 256 rows (two tiles of 128; one at head_dim 256) of one
 // sequence and key/value head, over its keys 64 at a time.  Warps:
 //   0-3, 4-7  softmax of tile 0, of tile 1: a thread owns a row, reads its 64 scores and
-//             writes the probabilities over them, so no reduction crosses lanes
+//             writes the probabilities over them, so no reduction crosses lanes.  With one
+//             tile both take half of its columns: what the step waits for is their latency
 //   8, 9      issue the MMAs, of a tile each (one warp needs some 70 cycles per MMA, more
 //             than an MMA of 64 keys takes).  Every tile has two S buffers and S runs two steps ahead
 //             (S of step j + 2 goes over P of step j behind P V of step j), so the softmax
@@ -56,6 +57,7 @@ template <int D>
 struct Shape {
   static constexpr int NT = D == 256 ? 1 : 2;        // tiles of 128 rows
   static constexpr int R = 128 * NT;
+  static constexpr int HALVES = 2 / NT;              // softmax warps that share a row
   static constexpr int ATOMS = D / 64;               // 128-byte columns of an operand row
   static constexpr int Q_BYTES = R * D * 2;
   static constexpr int KV_BYTES = BN * D * 2;        // keys or values of a stage
@@ -96,7 +98,24 @@ struct alignas(16) Ctl {
   uint32_t tmem;
   int abort;
   float row[256];                        // bf16: score factor of each row
+  float2 pair[2][128];                   // what the two threads of a row tell each other
 };
+
+// Or of a predicate over the two warps of a barrier.
+KQ_DEV bool pair_or(int bar, bool x) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %2, 0;\n bar.red.or.pred p, %1, 64, q;\n"
+               " selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(r)
+               : "r"(bar), "r"((uint32_t)x)
+               : "memory");
+  return r != 0;
+}
+KQ_DEV void pair_sync(int bar) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
+}
 
 // One lane of a converged warp, the same one every time.  The operands of what it issues
 // are computed by the whole warp, so that they live in uniform registers; from one lane's
@@ -246,13 +265,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     for (int i = 0; i < 2; ++i) {
       for (int k = 0; k < 2; ++k) {
         kq::mbar_init(&ctl.s_full[i][k], 2);   // S itself, and that its keys' numbers are there
-        kq::mbar_init(&ctl.p_ready[i][k], 4);
+        kq::mbar_init(&ctl.p_ready[i][k], 4 * SH::HALVES);
       }
       kq::mbar_init(&ctl.pv_done[i], 1);
     }
     for (int i = 0; i < 8; ++i) {
       kq::mbar_init(&ctl.num_full[i], 1);
-      kq::mbar_init(&ctl.num_free[i], 4 * tiles + JOBS);   // softmax warps, unpackers of the values
+      kq::mbar_init(&ctl.num_free[i], 4 * SH::HALVES * tiles + JOBS);   // softmax warps, unpackers of the values
     }
     kq::mbar_init(&ctl.o_full, tiles);
     kq::mbar_init(&ctl.q_full, NUM_QUERY_WARPS);
@@ -589,9 +608,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         if (values) kq::mbar_arrive(&ctl.num_free[j & 7]);
       }
     }
-  } else if (warp < 4 * tiles || (NT == 1 && warp < 4)) {
+  } else if (warp < 4 * tiles * SH::HALVES) {
     // ---------------------------------------------------------- softmax
-    const int tile = NT == 2 ? warp >> 2 : 0;
+    // (one tile: two warps share their rows, a half of each step's keys to either, and agree
+    // by a barrier of their own on the maximum and on giving up)
+    constexpr int HALVES = SH::HALVES, COLS = BN / HALVES;
+    const int tile = NT == 2 ? warp >> 2 : 0, part = NT == 2 ? 0 : warp >> 2, bar = 1 + (warp & 3);
     const int tr = (warp & 3) * 32 + lane;              // row within the tile
     const uint32_t tbase = ctl.tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t o_at = tbase + SH::O_COL + tile * D;
@@ -606,21 +628,23 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     // neighbour until the row has seen a key
     float m = 0.f, lag = -0x1.fffffep127f;
     f32x2 l2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+    bool stop = false;
     auto step = [&](auto is_masked, int j, int key0) {
       constexpr bool masked = decltype(is_masked)::value;
       const uint32_t s_at = tbase + (2 * tile + (j & 1)) * BN;
       const Numbers& num = ctl.num[j & 7];
       const float turn = num.turn;
       const uint32_t gone = masked ? num.absent : 0u;
-      f32x2 t[BN / 2];             // scores relative to the running maximum
+      f32x2 t[COLS / 2];           // scores relative to the running maximum
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       const f32x2 neg_m = pack2(-m, -m), row2 = BF ? pack2(row * num.down, row * num.down) : 0ull;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < COLS / 32; ++h) {
+        const int hp = h + part;   // the half of the step's keys
         float x[32];
-        kq::tmem_ld32(s_at + 32 * h, x);
+        kq::tmem_ld32(s_at + 32 * hp, x);
         kq::tmem_wait_ld();
-        const ulonglong2* fk = reinterpret_cast<const ulonglong2*>(&num.fk[32 * h]);
+        const ulonglong2* fk = reinterpret_cast<const ulonglong2*>(&num.fk[32 * hp]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const ulonglong2 f = BF ? make_ulonglong2(row2, row2) : fk[i];
@@ -631,8 +655,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
             tc = fma2(pack2(x[e], x[e + 1]), k ? f.y : f.x, neg_m);
             float2 v = unpack2(tc);
             if constexpr (masked) {
-              const int key = key0 + 32 * h + e;
-              const bool page = !((gone >> (2 * h + (e >> 4))) & 1u);
+              const int key = key0 + 32 * hp + e;
+              const bool page = !((gone >> (2 * hp + (e >> 4))) & 1u);
               if (!(page && key < hi && (key >= lo || key < a.sinks))) v.x = -INFINITY;
               if (!(page && key + 1 < hi && (key + 1 >= lo || key + 1 < a.sinks))) v.y = -INFINITY;
               tc = pack2(v.x, v.y);
@@ -641,8 +665,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
           }
         }
       }
-      const float high = max3(max3(top[0], top[1], top[2]), top[3], top[3]);
-      if (__any_sync(0xffffffffu, high > lag || turn != 1.f)) {
+      float high = max3(max3(top[0], top[1], top[2]), top[3], top[3]);
+      const bool moves = high > lag || turn != 1.f;
+      // (two warps to a row: also before either writes P over scores of the other)
+      if (HALVES == 2 ? pair_or(bar, moves || !ok) : __any_sync(0xffffffffu, moves)) {
+        if constexpr (HALVES == 2) {
+          ctl.pair[part][tr] = make_float2(high, ok ? 1.f : 0.f);
+          pair_sync(bar);
+          const float2 other = ctl.pair[part ^ 1][tr];
+          high = max3(high, other.x, other.x);
+          // (this is the only way out of the steps, for both at once: neither waits in vain)
+          stop = !__all_sync(0xffffffffu, ok && other.y != 0.f);
+          ok = ok && !stop;
+          if (stop) return;
+        }
         // the maximum moves by a whole number; what was summed before turns by a power of two
         const bool up = high > lag;
         const float by = up ? (high < INFINITY ? ceilf(high) - BASE : high) : 0.f;
@@ -653,13 +689,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         l2[0] = mul2(l2[0], al2);
         l2[1] = mul2(l2[1], al2);
 #pragma unroll
-        for (int k = 0; k < BN / 2; ++k) t[k] = add2(t[k], down);
+        for (int k = 0; k < COLS / 2; ++k) t[k] = add2(t[k], down);
         if (j > 0) {
           ok = wait(&ctl.pv_done[tile], j - 1) && ok;
           kq::tc_fence_after();
           const float f = al * turn;
 #pragma unroll 1
-          for (int d = 0; d < D; d += 16) {
+          for (int d = part * (D / HALVES); d < (part + 1) * (D / HALVES); d += 16) {
             uint32_t o[16];
             tmem_ld16(o_at + d, o);
             kq::tmem_wait_ld();
@@ -671,11 +707,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       }
       const ulonglong2* sv = reinterpret_cast<const ulonglong2*>(num.sv);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < COLS / 32; ++h) {
         uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const ulonglong2 f = BF ? make_ulonglong2(0ull, 0ull) : sv[8 * h + i];
+          const ulonglong2 f = BF ? make_ulonglong2(0ull, 0ull) : sv[8 * (h + part) + i];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float2 v = unpack2(t[16 * h + 2 * i + k]);
@@ -689,18 +725,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
             pk[2 * i + k] = pack_half2(w.x, w.y);
           }
         }
-        tmem_st16(s_at + 16 * h, pk);
+        tmem_st16(s_at + 16 * (h + part), pk);
       }
     };
     for (int j = 0; j < steps; ++j) {
       ok = ok && wait(&ctl.s_full[tile][j & 1], j >> 1);
-      if (!ok) break;
+      // (of two warps to a row, one that gives up tells the other in step)
+      if (HALVES == 1 && !ok) break;
       kq::tc_fence_after();
       const int key0 = key_of(i0 + j);
       if (ctl.num[j & 7].absent || !(key0 + BN <= all_hi && (key0 >= all_lo || key0 + BN <= a.sinks)))
         step(std::true_type{}, j, key0);
       else
         step(std::false_type{}, j, key0);
+      if (HALVES == 2 && stop) break;
       kq::tmem_wait_st();
       kq::tc_fence_before();
       __syncwarp();
@@ -711,7 +749,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     }
     // ---- output
     const float2 ls = unpack2(add2(l2[0], l2[1]));
-    const float l = ls.x + ls.y;
+    float l = ls.x + ls.y;
+    if constexpr (HALVES == 2) {
+      pair_sync(bar);
+      ctl.pair[part][tr].x = l;
+      pair_sync(bar);
+      const float other = ctl.pair[part ^ 1][tr].x;
+      l = part ? other + l : l + other;
+    }
     if (steps > 0) ok = ok && wait(&ctl.o_full, 0);
     kq::tc_fence_after();
     const float fv = steps > 0 ? ctl.num[(steps - 1) & 7].fv : 0.f;
@@ -723,16 +768,17 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     if (ok) {
       // Through shared memory (the queries and what lies behind them are not needed any more),
       // so that a warp stores whole rows: a thread has a row, and rows are far apart.  Each
-      // warp has its own 32 rows of D floats; chunk c of 4 of row t lies at c ^ (t & 7).
+      // warp has its own 32 rows of DP floats; chunk c of 4 of row t lies at c ^ (t & 7).
       static_assert(SH::Q_BYTES + SH::STAGES * SH::STAGE >= R * D * 4, "room for the output");
-      float* buf = reinterpret_cast<float*>(q_smem) + (128 * tile + (warp & 3) * 32) * D;
+      constexpr int DP = D / HALVES;                   // dims of this warp's
+      float* buf = reinterpret_cast<float*>(q_smem) + warp * 32 * DP;
       const float f = split ? rfv : l == 0.f ? 0.f : rfv / l;
 #pragma unroll 1
-      for (int d = 0; d < D; d += 32) {
+      for (int d = 0; d < DP; d += 32) {
         uint32_t o[32];
         if (steps > 0) {
-          tmem_ld16(o_at + d, reinterpret_cast<uint32_t(&)[16]>(o[0]));
-          tmem_ld16(o_at + d + 16, reinterpret_cast<uint32_t(&)[16]>(o[16]));
+          tmem_ld16(o_at + part * DP + d, reinterpret_cast<uint32_t(&)[16]>(o[0]));
+          tmem_ld16(o_at + part * DP + d + 16, reinterpret_cast<uint32_t(&)[16]>(o[16]));
           kq::tmem_wait_ld();
         } else {
 #pragma unroll
@@ -742,30 +788,30 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         for (int k = 0; k < 32; k += 4) {
           // dims 8 (k / 8) + 0..3 are columns 0 2 4 6 of the 8, dims 4..7 columns 1 3 5 7
           const int b = (k & 24) + ((k >> 2) & 1);
-          *reinterpret_cast<float4*>(buf + lane * D + 4 * (((d + k) >> 2) ^ (lane & 7))) =
+          *reinterpret_cast<float4*>(buf + lane * DP + 4 * (((d + k) >> 2) ^ (lane & 7))) =
               make_float4(__uint_as_float(o[b]) * f, __uint_as_float(o[b + 2]) * f,
                           __uint_as_float(o[b + 4]) * f, __uint_as_float(o[b + 6]) * f);
         }
       }
       // where the lane's row goes
       uint64_t to = 0;
-      if (mine && split) to = reinterpret_cast<uint64_t>(a.part_o + slot * D);
+      if (mine && split) to = reinterpret_cast<uint64_t>(a.part_o + slot * D + part * DP);
       if (mine && !split)
         to = reinterpret_cast<uint64_t>(static_cast<uint16_t*>(a.out) + (int64_t)out_row * a.o_st +
-                                        (int64_t)hq * a.o_sh);
-      if (mine && split) a.part_ml[slot] = {lag == LAG ? m : NO_MAX, l};
-      if (mine && !split && a.lse)
+                                        (int64_t)hq * a.o_sh + part * DP);
+      if (mine && split && part == 0) a.part_ml[slot] = {lag == LAG ? m : NO_MAX, l};
+      if (mine && !split && part == 0 && a.lse)
         a.lse[(int64_t)out_row * a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       __syncwarp();
-      constexpr int CHUNKS = D / 4;
+      constexpr int CHUNKS = DP / 4;
       auto store = [&](auto is_split) {
 #pragma unroll 1
-        for (int i = 0; i < D / 4; i += 8) {
+        for (int i = 0; i < DP / 4; i += 8) {
           float4 x[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int t = ((i + k) * 32 + lane) / CHUNKS, c = ((i + k) * 32 + lane) % CHUNKS;
-            x[k] = *reinterpret_cast<const float4*>(buf + t * D + 4 * (c ^ (t & 7)));
+            x[k] = *reinterpret_cast<const float4*>(buf + t * DP + 4 * (c ^ (t & 7)));
           }
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
