@@ -34,11 +34,13 @@
 // Dims stay in the order unpacking yields within each 8 (0 4 1 5 2 6 3 7): queries
 // are stored that way and the output is put right when it leaves.
 //
-// Measured: two chunks of 2048 tokens over 16k, 32 query heads of 128, bf16: 1.31 ms,
-// 785 TFLOP/s of the two products; bound by the softmax warps (one exponential and some
-// five more instructions per score and row, 256 rows a step), which the MMAs wait for.
-// A unit costs some 12 us beside its steps (division of the work, first loads, output):
-// 1777 tokens under a window of 1024, heads of 256: 204 us, 380 TFLOP/s.
+// Measured: two chunks of 2048 tokens over 16k, 32 query heads of 128, bf16: 1.32 ms,
+// 778 TFLOP/s of the two products.  A step of 64 keys takes 2200 to 2800 cycles: the
+// softmax of a row some 1900 (500 for scores and maximum, 1200 for exponentials and P),
+// the MMAs 1280 of tensor pipe (S reads 48 KB of shared memory per tile, 384 cycles where
+// the products would take 256), issued one behind the other.  A unit costs some 12 us
+// beside its steps (division of the work, first loads, output): 1777 tokens under a window
+// of 1024, heads of 256: 172 us, 449 TFLOP/s (204 with one warp to a row).
 //
 // All waits are bounded; one that gives up records KRONQ_ERR_TIMEOUT in `info`.
 #include <type_traits>
@@ -98,6 +100,8 @@ struct alignas(16) Ctl {
   uint32_t tmem;
   int abort;
   float row[256];                        // bf16: score factor of each row
+  Unit unit;                             // for the output: nothing of it stays in registers
+  Seq seq;
   float2 pair[2][128];                   // what the two threads of a row tell each other
 };
 
@@ -273,6 +277,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       kq::mbar_init(&ctl.num_full[i], 1);
       kq::mbar_init(&ctl.num_free[i], 4 * SH::HALVES * tiles + JOBS);   // softmax warps, unpackers of the values
     }
+    ctl.unit = u;
+    ctl.seq = s;
     kq::mbar_init(&ctl.o_full, tiles);
     kq::mbar_init(&ctl.q_full, NUM_QUERY_WARPS);
     ctl.abort = 0;
@@ -638,12 +644,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       f32x2 t[COLS / 2];           // scores relative to the running maximum
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       const f32x2 neg_m = pack2(-m, -m), row2 = BF ? pack2(row * num.down, row * num.down) : 0ull;
+      float xs[COLS / 32][32];
+#pragma unroll
+      for (int h = 0; h < COLS / 32; ++h) kq::tmem_ld32(s_at + 32 * (h + part), xs[h]);
+      kq::tmem_wait_ld();
 #pragma unroll
       for (int h = 0; h < COLS / 32; ++h) {
         const int hp = h + part;   // the half of the step's keys
-        float x[32];
-        kq::tmem_ld32(s_at + 32 * hp, x);
-        kq::tmem_wait_ld();
+        const float(&x)[32] = xs[h];
         const ulonglong2* fk = reinterpret_cast<const ulonglong2*>(&num.fk[32 * hp]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -761,10 +769,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     kq::tc_fence_after();
     const float fv = steps > 0 ? ctl.num[(steps - 1) & 7].fv : 0.f;
     const float rfv = fv != 0.f ? 1.f / fv : 0.f;
-    const bool mine = r0 + 128 * tile + tr < rows;
-    const int64_t slot = ((int64_t)u.slot * a.cache.heads + head) * R + 128 * tile + tr;
-    const int hq = head * a.g + r - qi * a.g, out_row = s.row0 + qi;
-    const bool split = u.nsplit > 1;
+    const int row_in = ctl.unit.tile * R + 128 * tile + tr, to_head = ctl.unit.head;
+    const bool mine = row_in < ctl.seq.n * a.g;
+    const int64_t slot = ((int64_t)ctl.unit.slot * a.cache.heads + to_head) * R + 128 * tile + tr;
+    const int to_q = row_in / a.g, hq = to_head * a.g + row_in - to_q * a.g, out_row = ctl.seq.row0 + to_q;
+    const bool split = ctl.unit.nsplit > 1;
     if (ok) {
       // Through shared memory (the queries and what lies behind them are not needed any more),
       // so that a warp stores whole rows: a thread has a row, and rows are far apart.  Each
