@@ -616,8 +616,8 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
   }
 }
 
-// Joins the splits of the rows that have some: a block per token and `hpb` query
-// heads, one row at a time; warp w takes the splits w, w + 4, ..
+// Joins the splits of the rows that have some: a block per token and `hpb` query heads.
+// Few splits: a warp per row; many: one row at a time, warp w takes the splits w, w + 4, ..
 template <int D>
 __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, int R, int hpb) {
   constexpr int E = D / 32;
@@ -635,6 +635,63 @@ __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, 
   const int2 mt = a.meta[b];
   const int ns = mt.y;
   if (ns <= 1) return;
+  if (ns <= 8 && hpb > 1) {
+    // lane: chunk of 4 dims (head_dim 256: and the one 32 on; 64: of every other split)
+    constexpr int CPL = D == 256 ? 2 : 1, KP = D == 64 ? 2 : 1;
+    const int c = lane % (D == 64 ? 16 : 32), k0 = KP == 2 ? lane >> 4 : 0;
+    for (int h = warp; h < hpb; h += WARPS) {
+      const int hq = blockIdx.y * hpb + h;
+      if (hq >= a.Hq) return;
+      const int head = hq / a.g, r = (i - s.row0) * a.g + hq - head * a.g;
+      const int tile = r / R;
+      if (mt.x < 0 || mt.x + (tile + 1ll) * ns > a.slots) return;
+      const int64_t stride = (int64_t)a.cache.heads * R;
+      const int64_t s0 = ((int64_t)(mt.x + tile * ns) * a.cache.heads + head) * R + (r - tile * R);
+      const Part q = lane < ns ? a.part_ml[s0 + lane * stride] : Part{-INFINITY, 0.f};
+      float4 v[8 / KP][CPL];
+#pragma unroll
+      for (int k = 0; k < 8; k += KP)
+#pragma unroll
+        for (int j = 0; j < CPL; ++j)
+          v[k / KP][j] = k + k0 < ns ? *reinterpret_cast<const float4*>(a.part_o + (s0 + (k + k0) * stride) * D +
+                                                                        4 * (c + 32 * j))
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+      float m = q.m;
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      m = __shfl_sync(0xffffffffu, m, 0);              // (of the splits, lanes 0 .. 7)
+      const float w = exp2_approx(q.m - m);
+      float l = q.l * w;
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      l = __shfl_sync(0xffffffffu, l, 0);
+      float4 o[CPL];
+#pragma unroll
+      for (int j = 0; j < CPL; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 8; k += KP) {
+        const float wk = __shfl_sync(0xffffffffu, w, k + k0);
+        if (k + k0 >= ns) continue;
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+          o[j].x = fmaf(wk, v[k / KP][j].x, o[j].x);
+          o[j].y = fmaf(wk, v[k / KP][j].y, o[j].y);
+          o[j].z = fmaf(wk, v[k / KP][j].z, o[j].z);
+          o[j].w = fmaf(wk, v[k / KP][j].w, o[j].w);
+        }
+      }
+      if constexpr (KP == 2) {
+        o[0].x += __shfl_xor_sync(0xffffffffu, o[0].x, 16);
+        o[0].y += __shfl_xor_sync(0xffffffffu, o[0].y, 16);
+        o[0].z += __shfl_xor_sync(0xffffffffu, o[0].z, 16);
+        o[0].w += __shfl_xor_sync(0xffffffffu, o[0].w, 16);
+      }
+      if (KP == 1 || lane < 16)
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) store_row(a, i, hq, 4 * (c + 32 * j), o[j], m, l);
+    }
+    return;
+  }
   for (int h = 0; h < hpb; ++h) {
     const int hq = blockIdx.y * hpb + h;
     if (hq >= a.Hq) return;
@@ -760,7 +817,9 @@ int launch(AttendArgs& a, cudaStream_t st) {
 
 template <int D>
 int launch_merge(const AttendArgs& a, int R, cudaStream_t st) {
-  const int hpb = (long long)a.T * a.Hq <= 16384 ? 1 : a.Hq;
+  // (rows by themselves while the device holds a block for each; then four to a block)
+  const long long rows = (long long)a.T * a.Hq;
+  const int hpb = rows <= 4 * SMS ? 1 : rows <= 65536 ? 4 : a.Hq;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.T, (unsigned)((a.Hq + hpb - 1) / hpb));
   cfg.blockDim = dim3(THREADS);
