@@ -817,9 +817,13 @@ int launch(AttendArgs& a, cudaStream_t st) {
 
 template <int D>
 int launch_merge(const AttendArgs& a, int R, cudaStream_t st) {
-  // (rows by themselves while the device holds a block for each; then four to a block)
+  // Rows by themselves where the device holds a block for each or a sequence may have more
+  // splits than a warp takes (on average at most 2 resident / (heads B)); else four to a
+  // block.  512 rows of 12 splits: 23 us with a block each, 28 with four to a block; 4096 of
+  // two: 104 and 99.
   const long long rows = (long long)a.T * a.Hq;
-  const int hpb = rows <= 4 * SMS ? 1 : rows <= 65536 ? 4 : a.Hq;
+  const bool few = 2ll * a.resident <= 8ll * a.cache.heads * a.b.B;
+  const int hpb = rows <= 4 * SMS || (!few && rows <= 16384) ? 1 : rows <= 65536 ? 4 : a.Hq;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.T, (unsigned)((a.Hq + hpb - 1) / hpb));
   cfg.blockDim = dim3(THREADS);
