@@ -37,9 +37,9 @@
 // vote), so most steps have no cross-lane reduction.
 //
 // Measured (heads of 128, cold cache): 64 sequences of 4k to 8k tokens, 8 query heads
-// a key/value head, bf16: 104 us, 4.1 TB/s of codes and words; 4 sequences of 105k to
-// 131k tokens, 4 query heads, fp16: 102 us, 5.2 TB/s (of 6.55 that a copy moves).  One
-// sequence of 8k is latency: 11.7 us for the two launches.
+// a key/value head, bf16: 99 us, 4.4 TB/s of codes and words; 4 sequences of 105k to
+// 131k tokens, 4 query heads, fp16: 102 us, 5.3 TB/s (of 6.55 that a copy moves).  One
+// sequence of 8k is latency: 11.6 us for the two launches.
 #include <type_traits>
 
 #include "kv4_attend.cuh"
@@ -818,11 +818,11 @@ int launch(AttendArgs& a, cudaStream_t st) {
 template <int D>
 int launch_merge(const AttendArgs& a, int R, cudaStream_t st) {
   // Rows by themselves where the device holds a block for each or a sequence may have more
-  // splits than a warp takes (on average at most 2 resident / (heads B)); else four to a
+  // splits than a warp takes (on average less than 2 resident / (heads B)); else four to a
   // block.  512 rows of 12 splits: 23 us with a block each, 28 with four to a block; 4096 of
   // two: 104 and 99.
   const long long rows = (long long)a.T * a.Hq;
-  const bool few = 2ll * a.resident <= 8ll * a.cache.heads * a.b.B;
+  const bool few = 2ll * a.resident <= 12ll * a.cache.heads * a.b.B;
   const int hpb = rows <= 4 * SMS || (!few && rows <= 16384) ? 1 : rows <= 65536 ? 4 : a.Hq;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.T, (unsigned)((a.Hq + hpb - 1) / hpb));
