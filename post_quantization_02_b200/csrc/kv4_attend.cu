@@ -166,7 +166,10 @@ constexpr float NO_MAX = -0x1p127f;
 constexpr int RING = 3;
 constexpr int FLUSH = 4;      // steps between subtractions of the zero points' part
 
-template <int D, int NT>
+// FINE (fp16 outputs): probabilities in two fp16 terms.  One is off by 2^-11, as much as
+// the output's own rounding, and the two add up to 1.4 times its error; for bf16 outputs
+// it is an eighth of theirs.
+template <int D, int NT, bool FINE>
 __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_attend_kernel(const AttendArgs a) {
   constexpr int R = 8 * NT;
   using SP = Step<D>;
@@ -490,7 +493,7 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t zw[4], pf[NT][2];
+      uint32_t zw[4], pf[NT][2], pl[NT][2];
       lds_words<4>(zw, zp + 64 * h);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -505,13 +508,21 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
             if (x[nt][h][2 * k] == -INFINITY) w0 = 0.f;
             if (x[nt][h][2 * k + 1] == -INFINITY) w1 = 0.f;
           }
-          pf[nt][k] = turn8x8(pack_half2(w0, w1));
+          const uint32_t hi = pack_half2(w0, w1);
+          pf[nt][k] = turn8x8(hi);
+          if constexpr (FINE) {
+            const float2 up = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+            pl[nt][k] = turn8x8(pack_half2(w0 - up.x, w1 - up.y));
+          }
         }
       {
         const uint32_t z01 = __byte_perm(zw[0], zw[1], 0x5410) & 0x000f000fu;
         const uint32_t z23 = __byte_perm(zw[2], zw[3], 0x5410) & 0x000f000fu;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816(z[nt], z01, z01, z23, z23, pf[nt][0], pf[nt][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          mma16816(z[nt], z01, z01, z23, z23, pf[nt][0], pf[nt][1]);
+          if constexpr (FINE) mma16816(z[nt], z01, z01, z23, z23, pl[nt][0], pl[nt][1]);
+        }
       }
 #pragma unroll
       for (int c = 0; c < SP::VC; c += 2) {
@@ -522,8 +533,10 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
           const uint32_t b01 = __byte_perm(v[i], 0, 0x4140), b23 = __byte_perm(v[i], 0, 0x4342);
           const uint32_t c01 = b01 & 0x000f000fu, c23 = b23 & 0x000f000fu;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt) {
             mma16816(o[nt][2 * c + i], c01, b01, c23, b23, pf[nt][0], pf[nt][1]);
+            if constexpr (FINE) mma16816(o[nt][2 * c + i], c01, b01, c23, b23, pl[nt][0], pl[nt][1]);
+          }
         }
       }
     }
@@ -801,7 +814,7 @@ Layout layout_of(const Way& w, int D, int heads, int64_t B) {
   return l;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool FINE>
 int launch(AttendArgs& a, cudaStream_t st) {
   constexpr int R = 8 * NT;
   const long long grid = max_units(a, R, BLK);
@@ -809,8 +822,8 @@ int launch(AttendArgs& a, cudaStream_t st) {
     constexpr int rings = WARPS * RING * Step<D>::BYTES, join = WARPS * R * D * (int)sizeof(float);
   constexpr int smem = rings > join ? rings : join;
   static kqh::PerDevice attr;
-  if (kqh::smem_attr_once(attr, kv4_attend_kernel<D, NT>, smem) <= 0) return KRONQ_ERR_CUDA;
-  kv4_attend_kernel<D, NT><<<(unsigned)grid, THREADS, smem, st>>>(a);
+  if (kqh::smem_attr_once(attr, kv4_attend_kernel<D, NT, FINE>, smem) <= 0) return KRONQ_ERR_CUDA;
+  kv4_attend_kernel<D, NT, FINE><<<(unsigned)grid, THREADS, smem, st>>>(a);
   KQ_CHECK_LAUNCH();
   return KRONQ_OK;
 }
@@ -844,9 +857,9 @@ int run(AttendArgs& a, const Way& w, cudaStream_t st) {
   if (w.prompt)
     s = launch_prompt(a, D, st);
   else if (D == 256 || w.R == 8)
-    s = launch<D, 1>(a, st);
+    s = a.dt == FP16 ? launch<D, 1, true>(a, st) : launch<D, 1, false>(a, st);
   else
-    s = launch<D, D == 256 ? 1 : 2>(a, st);
+    s = a.dt == FP16 ? launch<D, D == 256 ? 1 : 2, true>(a, st) : launch<D, D == 256 ? 1 : 2, false>(a, st);
   if (s != KRONQ_OK) return s;
   // no sequence can be split when the longest one the table holds is one chunk
   const long long most = (((long long)a.b.max_pages << a.cache.lgP) + w.BLK - 1) / w.BLK;
