@@ -480,7 +480,8 @@ int kronq_kv4_gather(void* k_out, void* v_out, int dtype, int64_t T,
  * query sees are not read, and their table entries may be anything.  A query
  * that sees no key gets 0.
  * Sums, maxima and scores are fp32; probabilities, relative to a running
- * maximum and times the value's scale, are rounded to fp16 for the product.
+ * maximum and times the value's scale, are rounded to fp16 for the product (fp16
+ * queries with few rows, see below: to two fp16 terms).
  * bf16 queries with more than 64 rows (new tokens x query heads of a group; 40 at
  * head_dim 256) per sequence on average: keys and values are rounded to fp16 too, once or twice
  * 2^-11 relative to each, where the output is rounded at 2^-8.

@@ -38,7 +38,7 @@
 //
 // Measured (heads of 128, cold cache): 64 sequences of 4k to 8k tokens, 8 query heads
 // a key/value head, bf16: 99 us, 4.4 TB/s of codes and words; 4 sequences of 105k to
-// 131k tokens, 4 query heads, fp16: 102 us, 5.3 TB/s (of 6.55 that a copy moves).  One
+// 131k tokens, 4 query heads, fp16: 105 us, 5.1 TB/s (of 6.55 that a copy moves).  One
 // sequence of 8k is latency: 11.6 us for the two launches.
 #include <type_traits>
 
@@ -168,15 +168,19 @@ constexpr int FLUSH = 4;      // steps between subtractions of the zero points' 
 
 // FINE (fp16 outputs): probabilities in two fp16 terms.  One is off by 2^-11, as much as
 // the output's own rounding, and the two add up to 1.4 times its error; for bf16 outputs
-// it is an eighth of theirs.
-template <int D, int NT, bool FINE>
+// it is an eighth of theirs.  A tile of 4 rows has them twice, in the MMA's columns 0 .. 3
+// and 4 .. 7: all of a column but its second product is alike, and that one takes the
+// second terms; a larger tile takes the product twice.  4 x 128k, 4 query heads: 102 us
+// with one term, 105 in two columns, 119 with two products.
+enum Terms { ONE, TWO_COLUMNS, TWO_PRODUCTS };
+template <int D, int NT, int TERMS>
 __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_attend_kernel(const AttendArgs a) {
-  constexpr int R = 8 * NT;
+  constexpr int ROWS = 8 * NT, R = TERMS == TWO_COLUMNS ? 4 : ROWS;     // columns of the MMAs, rows of a tile
   using SP = Step<D>;
   constexpr int KW = SP::KW, MT = D / 16;
-  extern __shared__ __align__(128) uint8_t smem[];   // the warps' rings; then [WARPS][R][D] floats
+  extern __shared__ __align__(128) uint8_t smem[];   // the warps' rings; then [WARPS][ROWS][D] floats
   float* merge_o = reinterpret_cast<float*>(smem);
-  __shared__ float merge_ml[WARPS][R][2];
+  __shared__ float merge_ml[WARPS][ROWS][2];
   __shared__ __align__(16) Plan plans[WARPS];
 
   Unit u;
@@ -194,10 +198,11 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
   const int gr = lane >> 2, t = lane & 3;
   const int rows = s.n * a.g, r0 = u.tile * R;
   const int last = min(rows, r0 + R) - 1;
+  const int gq = TERMS == TWO_COLUMNS ? gr & 3 : gr;   // this lane's row of the tile (and + 8)
   int qi[NT];                                       // query of this lane's row (rows behind: the last)
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) qi[nt] = min(last, r0 + 8 * nt + gr) / a.g;
-  const int q0 = __shfl_sync(0xffffffffu, qi[0], 0), q1 = __shfl_sync(0xffffffffu, qi[NT - 1], 28);
+  for (int nt = 0; nt < NT; ++nt) qi[nt] = min(last, r0 + 8 * nt + gq) / a.g;
+  const int q0 = __shfl_sync(0xffffffffu, qi[0], 0), q1 = last / a.g;
   const Span sp = span_of<BLK>(a, s, q0, q1);
   const int per = ceil_div(sp.nb, u.nsplit);
   const int i0 = u.split * per, i1 = min(sp.nb, i0 + per);
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
   float qsum[NT][2], qmul[NT][2];        // of columns 2t, 2t + 1
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = r0 + 8 * nt + gr;
+    const int r = r0 + 8 * nt + gq;
     float x[KW][8];
     float big = 0.f, sum = 0.f;
     if (r < rows) {
@@ -509,10 +514,13 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
             if (x[nt][h][2 * k + 1] == -INFINITY) w1 = 0.f;
           }
           const uint32_t hi = pack_half2(w0, w1);
-          pf[nt][k] = turn8x8(hi);
-          if constexpr (FINE) {
+          if constexpr (TERMS != ONE) {
             const float2 up = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-            pl[nt][k] = turn8x8(pack_half2(w0 - up.x, w1 - up.y));
+            const uint32_t lo = pack_half2(w0 - up.x, w1 - up.y);
+            pf[nt][k] = turn8x8(TERMS == TWO_COLUMNS && t >= 2 ? lo : hi);
+            if constexpr (TERMS == TWO_PRODUCTS) pl[nt][k] = turn8x8(lo);
+          } else {
+            pf[nt][k] = turn8x8(hi);
           }
         }
       {
@@ -521,7 +529,7 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mma16816(z[nt], z01, z01, z23, z23, pf[nt][0], pf[nt][1]);
-          if constexpr (FINE) mma16816(z[nt], z01, z01, z23, z23, pl[nt][0], pl[nt][1]);
+          if constexpr (TERMS == TWO_PRODUCTS) mma16816(z[nt], z01, z01, z23, z23, pl[nt][0], pl[nt][1]);
         }
       }
 #pragma unroll
@@ -535,7 +543,8 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma16816(o[nt][2 * c + i], c01, b01, c23, b23, pf[nt][0], pf[nt][1]);
-            if constexpr (FINE) mma16816(o[nt][2 * c + i], c01, b01, c23, b23, pl[nt][0], pl[nt][1]);
+            if constexpr (TERMS == TWO_PRODUCTS)
+              mma16816(o[nt][2 * c + i], c01, b01, c23, b23, pl[nt][0], pl[nt][1]);
           }
         }
       }
@@ -590,7 +599,7 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
       for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, merge_ml[w][r][0]);
       const float f = exp2_approx(m[nt][c] - mx) * rfv;
       const float fe = f * 0x1p24f, fo = f * 0x1p20f;
-      float* row = merge_o + (warp * R + r) * D;
+      float* row = merge_o + (warp * ROWS + r) * D;
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         const int d = 16 * i + 2 * gr;
@@ -613,11 +622,19 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
       const float mw = merge_ml[w][r][0], lw = merge_ml[w][r][1];
       ls += lw * exp2_approx(mw - mx);
       const float4 v =
-          *reinterpret_cast<const float4*>(merge_o + (w * R + r) * D + 4 * (d4 ^ join_swizzle(r)));
+          *reinterpret_cast<const float4*>(merge_o + (w * ROWS + r) * D + 4 * (d4 ^ join_swizzle(r)));
       acc.x += v.x;
       acc.y += v.y;
       acc.z += v.z;
       acc.w += v.w;
+      if (TERMS == TWO_COLUMNS) {        // the second terms
+        const float4 x = *reinterpret_cast<const float4*>(merge_o + (w * ROWS + r + 4) * D +
+                                                          4 * (d4 ^ join_swizzle(r + 4)));
+        acc.x += x.x;
+        acc.y += x.y;
+        acc.z += x.z;
+        acc.w += x.w;
+      }
     }
     if (u.nsplit > 1) {
       *reinterpret_cast<float4*>(a.part_o + (slot + r) * D + 4 * d4) = acc;
@@ -793,10 +810,10 @@ struct Way {
   float unit_cost;
 };
 
-Way way_of(int64_t T, int g, int D, int64_t B) {
+Way way_of(int64_t T, int g, int D, int64_t B, int dt) {
   if (T * g > (D == 256 ? 40 : 64) * B)
     return {true, prompt_rows(D), prompt_block(D), PROMPT_MIN_KEYS / prompt_block(D), SMS, PROMPT_UNIT_COST};
-  const int R = D == 256 || T * g <= 8 * B ? 8 : 16;
+  const int R = dt == FP16 && T * g <= 4 * B ? 4 : D == 256 || T * g <= 8 * B ? 8 : 16;
   return {false, R, BLK, MIN_CHUNK, SMS * (D == 256 || R == 16 ? 2 : 4), UNIT_COST};
 }
 
@@ -814,16 +831,16 @@ Layout layout_of(const Way& w, int D, int heads, int64_t B) {
   return l;
 }
 
-template <int D, int NT, bool FINE>
+template <int D, int NT, int TERMS>
 int launch(AttendArgs& a, cudaStream_t st) {
-  constexpr int R = 8 * NT;
+  constexpr int ROWS = 8 * NT, R = TERMS == TWO_COLUMNS ? 4 : ROWS;
   const long long grid = max_units(a, R, BLK);
   if (grid > INT32_MAX) return KRONQ_ERR_UNSUPPORTED;
-    constexpr int rings = WARPS * RING * Step<D>::BYTES, join = WARPS * R * D * (int)sizeof(float);
+    constexpr int rings = WARPS * RING * Step<D>::BYTES, join = WARPS * ROWS * D * (int)sizeof(float);
   constexpr int smem = rings > join ? rings : join;
   static kqh::PerDevice attr;
-  if (kqh::smem_attr_once(attr, kv4_attend_kernel<D, NT, FINE>, smem) <= 0) return KRONQ_ERR_CUDA;
-  kv4_attend_kernel<D, NT, FINE><<<(unsigned)grid, THREADS, smem, st>>>(a);
+  if (kqh::smem_attr_once(attr, kv4_attend_kernel<D, NT, TERMS>, smem) <= 0) return KRONQ_ERR_CUDA;
+  kv4_attend_kernel<D, NT, TERMS><<<(unsigned)grid, THREADS, smem, st>>>(a);
   KQ_CHECK_LAUNCH();
   return KRONQ_OK;
 }
@@ -856,10 +873,12 @@ int run(AttendArgs& a, const Way& w, cudaStream_t st) {
   int s;
   if (w.prompt)
     s = launch_prompt(a, D, st);
+  else if (w.R == 4)
+    s = launch<D, 1, TWO_COLUMNS>(a, st);
   else if (D == 256 || w.R == 8)
-    s = a.dt == FP16 ? launch<D, 1, true>(a, st) : launch<D, 1, false>(a, st);
+    s = a.dt == FP16 ? launch<D, 1, TWO_PRODUCTS>(a, st) : launch<D, 1, ONE>(a, st);
   else
-    s = a.dt == FP16 ? launch<D, D == 256 ? 1 : 2, true>(a, st) : launch<D, D == 256 ? 1 : 2, false>(a, st);
+    s = a.dt == FP16 ? launch<D, D == 256 ? 1 : 2, TWO_PRODUCTS>(a, st) : launch<D, D == 256 ? 1 : 2, ONE>(a, st);
   if (s != KRONQ_OK) return s;
   // no sequence can be split when the longest one the table holds is one chunk
   const long long most = (((long long)a.b.max_pages << a.cache.lgP) + w.BLK - 1) / w.BLK;
@@ -871,7 +890,8 @@ int run(AttendArgs& a, const Way& w, cudaStream_t st) {
 
 size_t kq_kv4_attention_ws(int64_t T, int Hq, int heads, int D, int64_t B) {
   if (T < 0 || Hq <= 0 || heads <= 0 || Hq % heads || B <= 0 || (D != 64 && D != 128 && D != 256)) return 0;
-  return kv4::layout_of(kv4::way_of(T, Hq / heads, D, B), D, heads, B).total;
+  // (for either type: the tiles of 4 rows need less)
+  return kv4::layout_of(kv4::way_of(T, Hq / heads, D, B, kv4::BF16), D, heads, B).total;
 }
 
 int kq_kv4_attention(const void* q, int64_t q_st, int64_t q_sh, int dtype, int64_t T, int Hq, int D,
@@ -910,7 +930,7 @@ int kq_kv4_attention(const void* q, int64_t q_st, int64_t q_sh, int dtype, int64
   a.window = window > (1 << 30) ? 0 : window;    // wider than any sequence
   a.sinks = !a.window ? 0 : sinks > (1 << 30) ? 1 << 30 : sinks;
   a.scale_log2 = scale * 1.4426950408889634f;
-  const Way way = way_of(T, g, D, b.B);
+  const Way way = way_of(T, g, D, b.B, dtype);
   a.min_chunk = way.min_chunk;
   a.resident = way.resident;
   a.unit_cost = way.unit_cost;

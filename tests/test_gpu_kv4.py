@@ -267,6 +267,9 @@ def test_gather_values(cuda, D, P, dtype):
     (128, 64, 2, 2, "fp16", [3, 4], [100, 4], False, 0, 0),
     (128, 64, 1, 17, "bf16", [1, 2], [100, 40], True, 0, 0),
     (128, 64, 1, 40, "fp16", [1], [300], True, 0, 0),
+    (128, 64, 2, 1, "fp16", [9, 1, 1, 1], [200, 70, 1, 400], True, 0, 0),
+    (256, 32, 2, 2, "fp16", [1, 1], [300, 70], True, 0, 0),
+    (256, 64, 1, 2, "fp16", [3, 1], [900, 70], True, 60, 4),
 ])
 def test_attention(cuda, D, P, heads, g, dtype, new, kv, causal, window, sinks):
     r = np.random.default_rng(D + P + sum(kv) + window)
