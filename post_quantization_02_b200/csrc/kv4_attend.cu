@@ -787,9 +787,13 @@ __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, 
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 constexpr int SMS = 148;
-constexpr int MIN_CHUNK = 2;                         // 256 keys
-constexpr float UNIT_COST = 1.5f, PROMPT_UNIT_COST = 5.f;
+// The shortest chunks of keys: one new token over 8k takes 13.4 us with 256 keys, 14.4 with
+// 512 (before the join was cheap); 16 and 64 new tokens over 8k with the other kernel 25 and
+// 33 us with 256, 23 and 31 with 512, 31 and 41 with 1024.
+constexpr int MIN_CHUNK = 2;                         // key blocks
 constexpr int PROMPT_MIN_KEYS = 512;
+// What a unit costs beside its blocks; 1.5, 3 and 5 measure the same for the first kernel.
+constexpr float UNIT_COST = 1.5f, PROMPT_UNIT_COST = 5.f;
 
 // How a call is run.  Rows per sequence and key/value head decide (on average: lengths
 // are on the device).  The tensor-memory kernel's time is that of 128 rows (256: the

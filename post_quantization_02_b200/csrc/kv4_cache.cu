@@ -69,6 +69,7 @@ KQ_DEV f32x2 mul2_rn(f32x2 a, f32x2 b) {
 }
 
 // x: dims 8 l + 64 r + 2 i and the next, in the order written above, packed in pairs.
+// (Registers are capped for 4 to 6 blocks per SM: 34k tokens 391 us without, 367 with.)
 template <int D, int DT>
 __global__ void __launch_bounds__(TPB, D == 64 ? 6 : D == 128 ? 5 : 4) kv4_append_kernel(const AppendArgs a) {
   constexpr int R = D / 64;
@@ -493,7 +494,8 @@ int kq_kv4_append(const void* q, int64_t q_st, int64_t q_sh, const void* k, int6
   a.info = info;
   if (T > INT32_MAX) return KRONQ_ERR_UNSUPPORTED;
   a.T = (int)T;
-  // a block per token; with few tokens their vectors are spread over more blocks
+  // a block per token; with few tokens their vectors are spread over more blocks (34k tokens
+  // of 80 vectors: 367 us, spread 563; 3.8k tokens of 20: 24, spread 30)
   const int passes = (Hq + 2 * c.heads + ITEMS - 1) / ITEMS;
   const dim3 grid((unsigned)T, T < 8 * kqh::num_sms() ? (unsigned)passes : 1u);
   if (D == 64)
