@@ -516,22 +516,28 @@ def _kv4_calls():
     return _kv4
 
 
-def _raw(stream) -> int:
-    return 0 if stream is None else stream.cuda_stream
-
-
+# A call that is given a stream makes it current, for its launches and its allocations:
+# memory allocated on another stream may be handed out again there while a kernel of this
+# one still runs.
 def kronq_kv4_append(q, k, v, cache, block_table, q_start, kv_len, q_out=None, table=None,
                      interleaved: bool = False, positions=None, signs=None, info=None, stream=None):
     """New keys and values (T x heads x D, bf16 or fp16) into the 4-bit cache, keys and
     queries rotated on the way (see kronq.h).  q may be None; returns q_out, which is
-    allocated when it is not given."""
+    allocated when it is not given (on the call's stream)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kronq_kv4_append(q, k, v, cache, block_table, q_start, kv_len, q_out, table, interleaved,
+                                    positions, signs, info)
     return _kv4_calls().append(q, k, v, cache, block_table, q_start, kv_len, q_out, table, interleaved, positions,
-                               signs, info, _raw(stream))
+                               signs, info)
 
 
 def kronq_kv4_gather(cache, block_table, q_start, kv_len, k_out, v_out, info=None, stream=None):
     """The values the cache holds for the batch's new tokens (see kronq.h)."""
-    _kv4_calls().gather(cache, block_table, q_start, kv_len, k_out, v_out, info, _raw(stream))
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kronq_kv4_gather(cache, block_table, q_start, kv_len, k_out, v_out, info)
+    _kv4_calls().gather(cache, block_table, q_start, kv_len, k_out, v_out, info)
 
 
 def kronq_kv4_attention_workspace_size(T: int, q_heads: int, heads: int, head_dim: int, batch: int) -> int:
@@ -547,9 +553,13 @@ def kv4_workspace(T: int, q_heads: int, heads: int, head_dim: int, batch: int, d
 def kronq_kv4_attention(q, cache, block_table, q_start, kv_len, out=None, ws=None, scale: float | None = None,
                         causal: bool = True, window: int = 0, sinks: int = 0, lse=None, info=None, stream=None):
     """Attention of q (T x q_heads x D) over the 4-bit cache (see kronq.h); returns out.
-    out and ws are allocated when they are not given, scale is D^-1/2."""
+    out and ws are allocated when they are not given (on the call's stream), scale is D^-1/2."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kronq_kv4_attention(q, cache, block_table, q_start, kv_len, out, ws, scale, causal, window, sinks,
+                                       lse, info)
     return _kv4_calls().attention(q, cache, block_table, q_start, kv_len, out, ws, scale, causal, window, sinks,
-                                  lse, info, _raw(stream))
+                                  lse, info)
 
 
 TIMERS = {"lazy_update": 0, "chol_update": 1, "chol_panel": 2, "obs_block": 3}

@@ -134,9 +134,9 @@ struct Cache {
   }
 };
 
-void* stream_of(const Device& dev, int64_t stream) {
-  return stream ? reinterpret_cast<void*>(stream) : c10::cuda::getCurrentCUDAStream(dev.index).stream();
-}
+// The current stream: outputs and workspaces that are allocated here belong to it too, so a
+// call cannot be given another one.
+void* stream_of(const Device& dev) { return c10::cuda::getCurrentCUDAStream(dev.index).stream(); }
 
 // 3-dim inputs before their sizes are used
 void three(const Tensor& t, const char* name) {
@@ -146,7 +146,7 @@ void three(const Tensor& t, const char* name) {
 std::optional<Tensor> append(const Maybe& q, const Tensor& k, const Tensor& v, const Tensor& cache,
                              const Tensor& block_table, const Tensor& q_start, const Tensor& kv_len, Maybe q_out,
                              const Maybe& table, bool interleaved, const Maybe& positions, const Maybe& signs,
-                             const Maybe& info, int64_t stream) {
+                             const Maybe& info) {
   three(k, "k");
   const int dt = dtype_code(k, "k", false);
   const auto type = k.scalar_type();
@@ -186,12 +186,12 @@ std::optional<Tensor> append(const Maybe& q, const Tensor& k, const Tensor& v, c
                          k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), dt, T, q_heads,
                          q_heads ? q_out->data_ptr() : nullptr, tp, n_rows, (int)rot, interleaved, pp, sp, c.data,
                          c.pages, c.page, c.heads, c.D, c.table, c.ld, c.max_pages, c.q_start, c.kv_len, c.B, ip,
-                         stream_of(dev, stream)));
+                         stream_of(dev)));
   return q_out;
 }
 
 void gather(const Tensor& cache, const Tensor& block_table, const Tensor& q_start, const Tensor& kv_len,
-            const Tensor& k_out, const Tensor& v_out, const Maybe& info, int64_t stream) {
+            const Tensor& k_out, const Tensor& v_out, const Maybe& info) {
   three(k_out, "k_out");
   const int dt = dtype_code(k_out, "k_out", true);
   const Device dev(k_out, "k_out");
@@ -204,7 +204,7 @@ void gather(const Tensor& cache, const Tensor& block_table, const Tensor& q_star
   int32_t* ip = vector<int32_t>(info, "info", at::kInt, 1, dev);
   check("kronq_kv4_gather",
         kronq_kv4_gather(k_out.data_ptr(), v_out.data_ptr(), dt, k_out.size(0), c.data, c.pages, c.page, c.heads, c.D,
-                         c.table, c.ld, c.max_pages, c.q_start, c.kv_len, c.B, ip, stream_of(dev, stream)));
+                         c.table, c.ld, c.max_pages, c.q_start, c.kv_len, c.B, ip, stream_of(dev)));
 }
 
 std::pair<Tensor, Tensor> gather_new(const Tensor& cache, const Tensor& block_table, const Tensor& q_start,
@@ -215,13 +215,13 @@ std::pair<Tensor, Tensor> gather_new(const Tensor& cache, const Tensor& block_ta
   const auto options = cache.options().dtype(type);
   const std::array<int64_t, 3> sizes = {tokens, cache.size(1), head_dim};
   Tensor k = at::empty(sizes, options), v = at::empty(sizes, options);
-  gather(cache, block_table, q_start, kv_len, k, v, info, 0);
+  gather(cache, block_table, q_start, kv_len, k, v, info);
   return {k, v};
 }
 
 Tensor attention(const Tensor& q, const Tensor& cache, const Tensor& block_table, const Tensor& q_start,
                  const Tensor& kv_len, Maybe out, Maybe ws, std::optional<double> scale, bool causal, int64_t window,
-                 int64_t sinks, const Maybe& lse, const Maybe& info, int64_t stream) {
+                 int64_t sinks, const Maybe& lse, const Maybe& info) {
   three(q, "q");
   const int dt = dtype_code(q, "q", false);
   const int64_t T = q.size(0), q_heads = q.size(1), D = q.size(2);
@@ -254,7 +254,7 @@ Tensor attention(const Tensor& q, const Tensor& cache, const Tensor& block_table
                             (float)(scale ? *scale : 1.0 / std::sqrt((double)D)), causal,
                             (int)std::min<int64_t>(window, far), (int)std::min<int64_t>(sinks, far), out->data_ptr(),
                             out->stride(0), out->stride(1), lp, ip, ws->data_ptr(),
-                            (size_t)ws->numel() * ws->element_size(), stream_of(dev, stream)));
+                            (size_t)ws->numel() * ws->element_size(), stream_of(dev)));
   return *out;
 }
 

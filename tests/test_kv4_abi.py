@@ -114,3 +114,56 @@ def test_binding_refusals(L):
             kv4.attend(**{**good, **change})
     with pytest.raises(ValueError):
         kv4.gather(cache, bt, qs, kv, 3, 128)
+
+
+class _Recorder:
+    """Stands for the compiled binding: notes the stream that is current at each call."""
+
+    def __init__(self):
+        self.current, self.seen = [], []
+
+    def context(self, stream):
+        import contextlib
+
+        @contextlib.contextmanager
+        def entered():
+            self.current.append(stream)
+            yield
+            self.current.pop()
+        return entered()
+
+    def __getattr__(self, name):
+        if name not in ("append", "gather", "attention", "gather_new"):
+            raise AttributeError(name)
+
+        def call(*args):
+            # no argument is a stream's handle: 0 is the default stream's, not "none"
+            self.seen.append((name, self.current[-1] if self.current else None, args))
+        return call
+
+
+def test_calls_run_and_allocate_on_the_given_stream(monkeypatch):
+    """The stream of a call is current while its outputs and workspace are allocated and its
+    kernels launched: what is allocated on another stream may be handed out again while they run.
+    The default stream, whose handle is 0, counts as given."""
+    rec = _Recorder()
+    monkeypatch.setattr(abi, "_kv4_calls", lambda: rec)
+    monkeypatch.setattr(torch.cuda, "stream", rec.context)
+
+    class Stream:
+        def __init__(self, handle):
+            self.cuda_stream = handle
+
+    x = torch.zeros(1)
+    for s in (None, Stream(0), Stream(77)):
+        rec.seen.clear()
+        abi.kronq_kv4_append(x, x, x, x, x, x, x, stream=s)
+        abi.kronq_kv4_gather(x, x, x, x, x, x, stream=s)
+        abi.kronq_kv4_attention(x, x, x, x, x, stream=s)
+        kv4.append(x, x, x, x, x, x, x, stream=s)
+        kv4.gather(x, x, x, x, 1, 64, stream=s)
+        kv4.attend(x, x, x, x, x, stream=s)
+        assert len(rec.seen) == 6
+        for name, current, args in rec.seen:
+            assert current is s, name
+            assert not any(type(a) is int and a == 77 for a in args), name
