@@ -479,12 +479,18 @@ int kronq_kv4_gather(void* k_out, void* v_out, int dtype, int64_t T,
  * or j < sinks: a sliding window and a few first tokens that stay visible.  Pages no
  * query sees are not read, and their table entries may be anything.  A query
  * that sees no key gets 0.
- * Sums, maxima and scores are fp32; probabilities, relative to a running
- * maximum and times the value's scale, are rounded to fp16 for the product (fp16
- * queries with few rows, see below: to two fp16 terms).
+ * Sums, maxima and scores are fp32; probabilities times the value's scale are
+ * rounded to fp16 for the product (fp16 queries with few rows, see below: to two
+ * fp16 terms), relative to the largest of them that the row has: below 2^-33 of
+ * it (2^-25 among 64 keys with scales 2^8 apart) they count as 0.
  * bf16 queries with more than 64 rows (new tokens x query heads of a group; 40 at
  * head_dim 256) per sequence on average: keys and values are rounded to fp16 too, once or twice
  * 2^-11 relative to each, where the output is rounded at 2^-8.
+ * What a row does not see has no part in its result, however large.  Values of the
+ * whole range of fp32 are attended to (beyond 10^30, probabilities below 2^-20 of the
+ * value's own may be missing from the sum that divides); scores have to
+ * stay finite, and queries below 2^115.  A NaN value or key makes the rows that see it NaN (lse too
+ * where there are many rows).
  *
  * q (T x q_heads x head_dim), out (same): KRONQ_BF16 or KRONQ_FP16, strides in
  * elements as above; out 8-byte aligned with strides that are multiples of 4.

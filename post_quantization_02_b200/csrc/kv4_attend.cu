@@ -33,7 +33,7 @@
 // own in shared memory, filled by cp.async two steps ahead: no barrier between
 // warps, and some 130 KB in flight per SM.  (Bulk copies from one lane cost
 // more: 89 against 20 issued instructions per 16 tokens.)  The running maximum
-// is only moved when a score passes it by 2^8 (all lanes of a column agree by
+// is only moved when a weight passes it by 2^5 (all lanes of a column agree by
 // vote), so most steps have no cross-lane reduction.
 //
 // Measured (heads of 128, cold cache): 64 sequences of 4k to 8k tokens, 8 query heads
@@ -74,6 +74,17 @@ KQ_DEV uint32_t turn8x8(uint32_t x) {
 KQ_DEV float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 2^(x/2).  Maxima follow weights, so where one part saw a value of 10^37 they are 2^100 apart,
+// and sums of probabilities that count take a factor that no fp32 number holds: it is applied
+// in two halves.
+KQ_DEV float exp2_half(float x) { return exp2_approx(0.5f * x); }
+
+// (in rules on ranges only)
+KQ_DEV float log2_approx(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -162,6 +173,16 @@ KQ_DEV int join_swizzle(int r) { return 2 * ((r >> 1) & 3); }
 // The running maximum before there is one: finite, so that a row that has seen no
 // key has sums of 0 and weights of 2^(NO_MAX - max) = 0 or 1, never a NaN.
 constexpr float NO_MAX = -0x1p127f;
+
+// Where a row's numbers lie.  With m the row's running maximum, p = 2^(x - m) is summed in
+// fp32, and p s' 2^-LIFT, the weight of a value's codes, is what fp16 has to hold.  So m follows
+// the largest weight, not the largest score: a new one is put at 2^BASE, and m moves when one
+// passes 2^LAG.  It belongs to the row alone: value vectors far larger than the rest do not
+// push the rest out of fp16's range in rows that do not see them.  Weights below 2^-35 of the
+// row's largest are lost.  LIFT keeps p normal where scales are large (p of a key with scale 2^100
+// is 2^(BASE + LIFT - 100) at most); FAR bounds p where they are tiny (zero vectors have
+// 2^-100): a score counts at least as a weight 2^FAR below it.
+constexpr float BASE = 10.f, LAG = 15.f, LIFT = 8.f, FAR = 80.f;
 
 constexpr int RING = 3;
 constexpr int FLUSH = 4;      // steps between subtractions of the zero points' part
@@ -365,9 +386,6 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
         z[nt][c] = 0.f;
       }
   };
-  // values' scales are taken times fv, a power of two, so that p s' fits fp16: the
-  // largest so far lies below 2^6 (times 2^8 of a lagging maximum, below 2^14)
-  float fv = 0.f, sv_max = -1.f;
 
   // byte offsets within a stage of what this lane reads
   const int tok = 4 * (gr >> 1) + (gr & 1);         // its keys: tok + 16 h + 2 k
@@ -423,7 +441,7 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
         for (int k = 0; k < 2; ++k) {
           const int j = j0 + tok + 16 * h + 2 * k;
           // what no row sees may be memory that was never written
-          if (!((here >> h) & 1) || !(j < any_hi && (j >= any_lo || j < a.sinks))) sv[h][k] = 0.f;
+          if (!((here >> h) & 1) || !(j < any_hi && (j >= any_lo || j < a.sinks))) sv[h][k] = 1.f;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -450,19 +468,14 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
             y[nt][h][2 * k + c] = fmaf(x[nt][h][2 * k + c], f, -m[nt][c]);
             top = fmaxf(top, y[nt][h][2 * k + c]);
           }
-    if (__any_sync(0xffffffffu, top > 8.f || sv_big > sv_max)) {
-      // new maxima (per column, over the lanes of equal t) and value scale
-      float big = sv_big;
+    // (a bound of the lane's largest weight: its largest score with its largest scale)
+    if (__any_sync(0xffffffffu, top + log2_approx(sv_big) > LAG + LIFT || top > LAG + LIFT + FAR)) {
+      // new maxima (per column, over the lanes of equal t)
+      float at[2][2];
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-      float turn = 1.f;
-      if (big > sv_max && big > 0.f) {
-        const int e = min(max(127 - (int)(__float_as_uint(big) >> 23), -100), 100);
-        const float nf = __uint_as_float((uint32_t)(127 + e) << 23);
-        turn = fv == 0.f ? 1.f : nf / fv;
-        fv = nf;
-        sv_max = 64.f / nf;
-      }
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) at[h][k] = fmaxf(log2_approx(sv[h][k]), -FAR) - (BASE + LIFT);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float al[2];
@@ -475,7 +488,7 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
             for (int k = 0; k < 2; ++k) {
               float& v = y[nt][h][2 * k + c];
               v = x[nt][h][2 * k + c] * (masked ? 1.f : sk[h][k] * qmul[nt][c]);
-              nm = fmaxf(nm, v);
+              nm = fmaxf(nm, v + at[h][k]);
             }
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, d));
@@ -486,7 +499,6 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
           al[c] = m[nt][c] == nm ? 1.f : exp2_approx(m[nt][c] - nm);
           m[nt][c] = nm;
           l[nt][c] *= al[c];
-          al[c] *= turn;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) z[nt][j] *= al[j & 1];
@@ -504,7 +516,7 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float svf = sv[h][k] * fv;
+          const float svf = sv[h][k] * (1.f / (1 << (int)LIFT));
           const float p0 = exp2_approx(y[nt][h][2 * k]), p1 = exp2_approx(y[nt][h][2 * k + 1]);
           l[nt][0] += p0;
           l[nt][1] += p1;
@@ -588,7 +600,6 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
       }
     }
   __syncthreads();
-  const float rfv = fv == 0.f ? 0.f : 1.f / fv;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -597,8 +608,8 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
       float mx = merge_ml[0][r][0];
 #pragma unroll
       for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, merge_ml[w][r][0]);
-      const float f = exp2_approx(m[nt][c] - mx) * rfv;
-      const float fe = f * 0x1p24f, fo = f * 0x1p20f;
+      const float root = exp2_half(m[nt][c] - mx), f = root * root;
+      const float fe = f * (0x1p24f * (1 << (int)LIFT)), fo = f * (0x1p20f * (1 << (int)LIFT));
       float* row = merge_o + (warp * ROWS + r) * D;
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
@@ -620,7 +631,8 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
       const float mw = merge_ml[w][r][0], lw = merge_ml[w][r][1];
-      ls += lw * exp2_approx(mw - mx);
+      const float root = exp2_half(mw - mx);
+      ls += lw * root * root;
       const float4 v =
           *reinterpret_cast<const float4*>(merge_o + (w * ROWS + r) * D + 4 * (d4 ^ join_swizzle(r)));
       acc.x += v.x;
@@ -690,8 +702,8 @@ __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, 
 #pragma unroll
       for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
       m = __shfl_sync(0xffffffffu, m, 0);              // (of the splits, lanes 0 .. 7)
-      const float w = exp2_approx(q.m - m);
-      float l = q.l * w;
+      const float root = exp2_half(q.m - m), w = root * root;
+      float l = q.l * root * root;
 #pragma unroll
       for (int d = 1; d < 8; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
       l = __shfl_sync(0xffffffffu, l, 0);
@@ -757,8 +769,8 @@ __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, 
           v[e + 3] = x.w;
         }
       }
-      const float w = exp2_approx(q.m - m);
-      l += q.l * w;
+      const float root = exp2_half(q.m - m), w = root * root;
+      l += q.l * root * root;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[e], o[e]);
     }

@@ -6,15 +6,17 @@
 //   fp16  the unpacked numbers are c - z, exact; scores and probabilities take the
 //         scale of their key, x = S s_j scale log2(e), P = 2^(x - m) s'_j, and the only
 //         rounding besides fp32's is P's.
-//   bf16  the unpacked numbers are the keys and values themselves, s (c - z) rounded to
-//         fp16 (the scale in two terms, so rounded once; a value's scale in one), and
+//   bf16  the unpacked numbers are the keys and values themselves, s (c - z) times a power
+//         of two of the step, rounded to fp16 (the scale in two terms, so rounded once; a
+//         value's scale in one), and
 //         queries are taken to fp16 by a power of two per row, exactly.  That is 2^-11
 //         relative per key and value where the output is rounded at 2^-8, and it spares
 //         every row reading two numbers per key: reads of the same 16 bytes by all lanes
 //         cost four passes through shared memory each, and those were 1000 of the 2400
 //         passes per step that bounded the kernel.
-// The running maximum m is a whole number and moves only when a score passes it by 8;
-// what was summed before is then scaled by a power of two.
+// The running maximum m is a whole number, of the weights that P holds (see kv4_attend.cu), and
+// moves only when one passes it by 5 binades or more; what was summed before is then scaled by a
+// power of two.
 //
 // One block = up to 256 rows (two tiles of 128; one at head_dim 256) of one
 // sequence and key/value head, over its keys 64 at a time.  Warps:
@@ -55,6 +57,19 @@ constexpr int BN = 64, GROUP = 16, GROUPS = BN / GROUP;    // keys per step; tha
 constexpr int JOB = 32, JOBS = BN / JOB;                   // keys per unpacking job; jobs for a step's keys
 constexpr float NO_MAX = -0x1p127f;     // a split's maximum where it saw no key
 
+// Scales in fp16.  The scales of a step's values (bf16: and of its keys) share a power of two
+// that is set for each step, 2^V_TOP and 2^K_TOP times [1, 2) for the largest: operands of 15
+// times that fit, and ones down to 2^-24 of the largest scale are normal numbers.  A step
+// whose scales are further apart than V_SPREAD or K_SPREAD binaries is a wide one: its operands
+// are c - z (values: 2^V_TOP of it), exact, and every row takes its keys' scales for itself, so
+// that a row that does not see the largest keeps what it sees.  Neither limit is a matter of
+// speed: V_SPREAD is what a row's weights may lie lower in P's range without harm, K_SPREAD
+// leaves a score 2^-19 of itself.
+constexpr uint32_t kZeroScale = 0x0d800000u;      // 2^-100: a zero vector's; its score is 0 whatever its factor
+constexpr uint32_t V_SPREAD = 8, K_SPREAD = 16;
+constexpr uint32_t WIDE = 1u << 31;
+constexpr float FAR = 80.f;                       // as in kv4_attend.cu
+
 template <int D>
 struct Shape {
   static constexpr int NT = D == 256 ? 1 : 2;        // tiles of 128 rows
@@ -81,14 +96,19 @@ struct Shape {
 
 // What the other warps need to know of a step's keys.
 struct alignas(16) Numbers {
-  float fk[BN], sv[BN];      // fp16 queries: score factor; value scale x fv
+  float fk[BN], sv[BN];      // fp16 queries, wide steps: score factor; value scale x 2^lift
+  float far[BN];             // wide steps: log2 of the value scale, for the running maximum
   uint32_t ks[BN];           // bf16: key scale x 2^f as two halves (high term, low term)
-  uint16_t vs[BN];           // bf16: value scale x fv
+  uint16_t vs[BN];           // bf16: value scale x 2^lift
   uint8_t zeros[BN];         // key's zero point | value's << 4
   uint64_t codes[GROUPS];    // address of the group's first key's codes, 0: no page
-  uint32_t absent;           // bit per group: no page
-  float turn, fv;            // fv over fv of the step before; fv
-  float down;                // bf16: 2^-f
+  // (one read by the softmax warps: each waits its turn behind the unpackers' stores)
+  struct alignas(16) All {
+    uint32_t absent;         // bit per group: no page; WIDE
+    float lift, up;          // of the step's value scales; 2^lift
+    float down;              // bf16: 2^-f
+  } all;
+  float back;                // 2^-lift of what it would be in a step that is not wide, within 2^+-64
 };
 
 struct alignas(16) Ctl {
@@ -178,6 +198,9 @@ KQ_DEV uint32_t load4(const uint32_t* p) {
   return v;
 }
 
+// of a power of two
+KQ_DEV float exponent(float x) { return (float)((int)(__float_as_uint(x) >> 23) - 127); }
+
 KQ_DEV float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -223,9 +246,9 @@ template <int D, bool BF>
 __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs a) {
   using SH = Shape<D>;
   constexpr int NT = SH::NT, R = SH::R, ATOMS = SH::ATOMS;
-  // how far scores may pass the running maximum, and where it is put below a new one: P is
-  // at most 2^14, times a value's scale below 2^6 on the fp16 way
-  constexpr float LAG = BF ? 14.f : 8.f, BASE = BF ? 6.f : 0.f;
+  // How far weights may pass the running maximum, and where it is put below a new one.
+  constexpr float LAG = BF ? 15.f : 14.f, BASE = 9.f;
+  constexpr int V_TOP = BF ? 10 : 0, K_TOP = 10;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl ctl;
   uint8_t* q_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -467,7 +490,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     set_up();
     if (steps > 0) ask_words(nxt, 0, page0);
     if (steps > 1) ask_words(after, 1, page1);
-    float fv = 0.f;
     for (int j = 0; j < steps; ++j) {
       cur = nxt;
       nxt = after;
@@ -476,32 +498,46 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         page = ask_page(j + 3);
       }
       if (j >= 8 && !wait(&ctl.num_free[j & 7], (j >> 3) + 1)) break;
-      // fv: a power of two that keeps value scales below 2^6 (see kv4_attend.cu).  Scales
-      // are not negative: their bits are in the numbers' order; a NaN counts as 0.
-      const uint32_t s0 = cur.v[0] & ~15u, s1 = cur.v[1] & ~15u;
-      const float big = __uint_as_float(__reduce_max_sync(
-          0xffffffffu, max(s0 > 0x7f800000u ? 0u : s0, s1 > 0x7f800000u ? 0u : s1)));
-      float turn = 1.f;
-      if (big > 0.f && (fv == 0.f || big * fv > 64.f)) {
-        const int e = min(max(127 - (int)(__float_as_uint(big) >> 23), -100), 100);
-        const float nf = __uint_as_float((uint32_t)(127 + e) << 23);
-        if (fv != 0.f) turn = nf / fv;
-        fv = nf;
+      // Scales are not negative: their bits are in the numbers' order.  (0: nobody sees it.  A
+      // zero vector's value scale counts too: its key's score must not decide where the others'
+      // weights lie.)
+      uint32_t v_top = 0u, v_low = ~0u, k_top = 0u, k_low = ~0u;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t v = cur.v[i] & ~15u, k = cur.k[i] & ~15u;
+        if (v && v < 0x7f800000u) {
+          v_top = max(v_top, v);
+          v_low = min(v_low, v);
+        }
+        if (BF && k > kZeroScale && k < 0x7f800000u) {
+          k_top = max(k_top, k);
+          k_low = min(k_low, k);
+        }
       }
-      Numbers& n = ctl.num[j & 7];
-      // bf16: f takes the step's largest key scale to [1/2, 1) x 2
-      float kup = 1.f;
+      v_top = __reduce_max_sync(0xffffffffu, v_top);
+      v_low = __reduce_min_sync(0xffffffffu, v_low);
       if (BF) {
-        const uint32_t k0 = cur.k[0] & ~15u, k1 = cur.k[1] & ~15u;
-        const uint32_t kb = __reduce_max_sync(0xffffffffu, max(k0 > 0x7f800000u ? 0u : k0, k1 > 0x7f800000u ? 0u : k1));
-        const int e = min(max(127 - (int)(kb >> 23), -126), 126);
-        kup = __uint_as_float((uint32_t)(127 + e) << 23);
-        if (lane == 0) n.down = __uint_as_float((uint32_t)(127 - e) << 23);
+        k_top = __reduce_max_sync(0xffffffffu, k_top);
+        k_low = __reduce_min_sync(0xffffffffu, k_low);
       }
+      const bool wide = v_top > v_low + (V_SPREAD << 23) || (BF && k_top > k_low + (K_SPREAD << 23));
+      // 2^lift takes the largest value scale to [1, 2), for bf16 to 2^10 times that
+      const int by_top = v_top ? 127 + V_TOP - (int)(v_top >> 23) : 0, lift = wide ? 0 : by_top;
+      const float up = __uint_as_float((uint32_t)(127 + lift) << 23);
+      Numbers& n = ctl.num[j & 7];
+      // bf16: f takes the largest key scale to [1, 2) 2^10
+      const int f = wide || !k_top ? 0 : 127 + K_TOP - (int)(k_top >> 23);
+      const float kup = __uint_as_float((uint32_t)(127 + f) << 23);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int t = lane + 32 * i;
-        float ks = word_scale(cur.k[i]), vs = word_scale(cur.v[i]) * fv;
+        float ks = word_scale(cur.k[i]), vs = word_scale(cur.v[i]) * up;
+        if (!BF || wide) {
+          const float vk = wide ? vs * (1.f / (1 << V_TOP)) : vs;
+          n.fk[t] = BF ? ks : ks * a.scale_log2;
+          n.sv[t] = vk;
+          if (wide) n.far[t] = fmaxf(log2f(vk), -FAR);
+        }
         if (BF) {
           // a value that is not finite must not meet the zero probabilities of rows that do
           // not see it: it counts as 0, and its key makes the score of those that do a NaN
@@ -512,20 +548,17 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
           ks *= kup;
           const __half hi = __float2half_rn(ks);
           const __half2 k2 = __halves2half2(hi, __float2half_rn(ks - __half2float(hi)));
-          n.ks[t] = *reinterpret_cast<const uint32_t*>(&k2);
-          n.vs[t] = __half_as_ushort(__float2half_rn(vs));
-        } else {
-          n.fk[t] = ks * a.scale_log2;
-          n.sv[t] = vs;
+          n.ks[t] = wide ? 0x00003c00u : *reinterpret_cast<const uint32_t*>(&k2);        // 1
+          n.vs[t] = __half_as_ushort(__float2half_rn(wide ? (float)(1 << V_TOP) : vs));
         }
         n.zeros[t] = (uint8_t)((cur.k[i] & 15u) | ((cur.v[i] & 15u) << 4));
       }
       const uint32_t there = __ballot_sync(0xffffffffu, cur.codes != 0);
       if (lane < GROUPS) n.codes[lane] = cur.codes;
       if (lane == 0) {
-        n.absent = ~there & ((1u << GROUPS) - 1);
-        n.turn = turn;
-        n.fv = fv;
+        n.all = {(~there & ((1u << GROUPS) - 1)) | (wide ? WIDE : 0u), (float)lift, up,
+                 __uint_as_float((uint32_t)(127 - f) << 23)};
+        n.back = __uint_as_float((uint32_t)(127 - min(max(by_top, -64), 64)) << 23);
       }
       __syncwarp();
       if (lane == 0) kq::mbar_arrive(&ctl.num_full[j & 7]);
@@ -549,7 +582,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     };
     struct Codes {
       uint4 c[SH::LOADS];
-      uint32_t zeros[SH::LOADS], scale[SH::LOADS];
     };
     // job n: step n / 4, keys (n & 2 == 0) or values, half n & 1 of the step
     static_assert(JOBS == 2 && JOB == 2 * GROUP, "four jobs to a step, two pages to a job");
@@ -560,12 +592,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       if (!wait(&ctl.num_full[j & 7], j >> 3)) return false;
       const Numbers& num = ctl.num[j & 7];
       const int64_t rel = (n & 2 ? vrel : 0) + ct * (D / 2) + 16 * c;
-#pragma unroll
-      for (int i = 0; i < SH::LOADS; ++i) {
-        const int t = JOB * g + i * TPL + ct;
-        q.zeros[i] = num.zeros[t];
-        if (BF) q.scale[i] = n & 2 ? num.vs[t] : num.ks[t];
-      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint64_t p = num.codes[2 * g + h];
@@ -585,28 +611,48 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     for (; n < jobs && ok; n += UNPACKERS) {
       const int j = n >> 2, g = n & 1, st = j & SM;
       cur = nxt;
-      if (n + UNPACKERS < jobs) ok = ask(nxt, n + UNPACKERS);
       const bool values = n & 2;
+      // (these keys' numbers stay until the step's softmax, which waits for this job)
+      const Numbers& num = ctl.num[j & 7];
+      uint32_t zeros[SH::LOADS], scale[SH::LOADS];
+#pragma unroll
+      for (int i = 0; i < SH::LOADS; ++i) {
+        const int t = JOB * g + i * TPL + ct;
+        zeros[i] = num.zeros[t];
+        scale[i] = !BF ? 0u : values ? num.vs[t] : num.ks[t];
+      }
+      if (n + UNPACKERS < jobs) ok = ask(nxt, n + UNPACKERS);
       if (j >= STAGES) ok = ok && wait(values ? &ctl.v_empty[st] : &ctl.k_empty[st], (j >> LG) + 1);
       if (!ok) break;
       const uint32_t dst = at + g * (JOB * 128) + st * SH::STAGE + (values ? SH::KV_BYTES : 0);
+      auto unpack = [&](bool of_values) {
 #pragma unroll
-      for (int i = 0; i < SH::LOADS; ++i) {
-        const uint32_t z = values ? cur.zeros[i] >> 4 : cur.zeros[i] & 15u;
-        const uint32_t z1 = 0x64006400u + z * 0x00010001u, z2 = 0xd400d400u + z * 0x00100010u;
-        const uint32_t hi = __byte_perm(cur.scale[i], 0, 0x1010), lo = __byte_perm(cur.scale[i], 0, 0x3232);
-        const uint32_t w[4] = {cur.c[i].x, cur.c[i].y, cur.c[i].z, cur.c[i].w};
-        if (!BF) {
+        for (int i = 0; i < SH::LOADS; ++i) {
+          const uint32_t z = of_values ? zeros[i] >> 4 : zeros[i] & 15u;
+          const uint32_t z1 = 0x64006400u + z * 0x00010001u, z2 = 0xd400d400u + z * 0x00100010u;
+          const uint32_t hi = __byte_perm(scale[i], 0, 0x1010), lo = __byte_perm(scale[i], 0, 0x3232);
+          const uint32_t w[4] = {cur.c[i].x, cur.c[i].y, cur.c[i].z, cur.c[i].w};
+          if (!BF) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) put(dst, i, k, codes_f16(w[k], z1, z2));
-        } else if (values) {
+            for (int k = 0; k < 4; ++k) put(dst, i, k, codes_f16(w[k], z1, z2));
+          } else if (of_values) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) put(dst, i, k, scaled(codes_f16(w[k], z1, z2), hi));
-        } else {
+            for (int k = 0; k < 4; ++k) put(dst, i, k, scaled(codes_f16(w[k], z1, z2), hi));
+          } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) put(dst, i, k, scaled(codes_f16(w[k], z1, z2), hi, lo));
+            for (int k = 0; k < 4; ++k) put(dst, i, k, scaled(codes_f16(w[k], z1, z2), hi, lo));
+          }
         }
-      }
+      };
+      // (heads of 256, bf16: unpacking keys bounds the step, and a copy of the code for either
+      // operand is the faster one: 602 us against 652 for two prompts of 1024 over 6000.  Heads
+      // of 128 lose 1 % by it, fp16 at 256 14 %.)
+      if (!(BF && D == 256))
+        unpack(values);
+      else if (values)
+        unpack(true);
+      else
+        unpack(false);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
@@ -630,20 +676,114 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     const int lo = lo_of(qi), hi = hi_of(qi);
     // what all rows of the warp see (rows are in order)
     const int all_lo = lo_of(__shfl_sync(0xffffffffu, qi, 31)), all_hi = hi_of(__shfl_sync(0xffffffffu, qi, 0));
-    // the running maximum, a whole number, and how far scores may pass it; 0 and -infinity's
-    // neighbour until the row has seen a key
-    float m = 0.f, lag = -0x1.fffffep127f;
-    f32x2 l2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+    // the running maximum, a whole number; 0 until the row has seen a key
+    float m = 0.f;
+    // the sum of probabilities, relative to 2^m / back: O's unit follows the weights, and a weight
+    // of a scale of 2^100 would push other keys' probabilities out of fp32
+    float l = 0.f, back = 0.f, back_max = 0.f;        // back: 0 until a key is seen; back_max: of the warp's rows
+    // how far weights may pass the maximum
+    auto lag = [&]() { return back > 0.f ? LAG : -0x1.fffffep127f; };
     bool stop = false;
-    auto step = [&](auto is_masked, int j, int key0) {
+    // Two warps to a row: the larger of their maxima.  Also the only way out of the steps, for
+    // both at once: neither waits in vain.
+    auto agree = [&](float& high) {
+      ctl.pair[part][tr] = make_float2(high, ok ? 1.f : 0.f);
+      pair_sync(bar);
+      const float2 other = ctl.pair[part ^ 1][tr];
+      high = max3(high, other.x, other.x);
+      stop = !__all_sync(0xffffffffu, ok && other.y != 0.f);
+      ok = ok && !stop;
+    };
+    // The maximum moves by a whole number; what was summed before turns by a power of two.
+    auto move = [&](float high, float to_back, int j) -> float {
+      const bool up = high > lag();
+      const float by = up ? (high < INFINITY ? ceilf(high) - BASE : high) : 0.f;
+      const float al = up && back > 0.f ? exp2_approx(-by) : 1.f;
+      if (up) {
+        if (back > 0.f) l *= al * (to_back / back);
+        back = to_back;
+      }
+      back_max = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(back)));
+      m += by;
+      if (j > 0) {
+        ok = wait(&ctl.pv_done[tile], j - 1) && ok;
+        kq::tc_fence_after();
+#pragma unroll 1
+        for (int d = part * (D / HALVES); d < (part + 1) * (D / HALVES); d += 16) {
+          uint32_t o[16];
+          tmem_ld16(o_at + d, o);
+          kq::tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+          tmem_st16(o_at + d, o);
+        }
+      }
+      return by;
+    };
+    // Any step, slowly: masks and per-key numbers always, l's terms for themselves, scores read
+    // twice to hold few of them.
+    auto any_step = [&](int j, int key0, const Numbers::All& all) {
+      const uint32_t s_at = tbase + (2 * tile + (j & 1)) * BN;
+      const Numbers& num = ctl.num[j & 7];
+      const uint32_t gone = all.absent;
+      const bool wide = gone & WIDE, by_key = !BF || wide;
+      const float to_x = BF ? row * all.down : 1.f, m0 = m + all.lift;
+      float by = 0.f;
+      auto scores = [&](int k0, float (&y)[16]) {
+        uint32_t x[16];
+        tmem_ld16(s_at + k0, x);
+        kq::tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int key = key0 + k0 + k;
+          const bool seen = !((gone >> (k0 >> 4)) & 1u) && key < hi && (key >= lo || key < a.sinks);
+          y[k] = seen ? fmaf(__uint_as_float(x[k]), by_key ? num.fk[k0 + k] * to_x : to_x, -m0) - by : -INFINITY;
+        }
+      };
+      float high = -INFINITY;
+#pragma unroll 1
+      for (int k0 = COLS * part; k0 < COLS * (part + 1); k0 += 16) {
+        float y[16];
+        scores(k0, y);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) high = fmaxf(high, wide ? y[k] + num.far[k0 + k] : y[k]);
+      }
+      if constexpr (HALVES == 2) {
+        pair_sync(bar);        // (the other has read what was told in the step before)
+        agree(high);
+        if (stop) return;
+      }
+      if (HALVES == 2 || __any_sync(0xffffffffu, high > lag())) by = move(high, num.back, j);
+      const float far = all.lift + exponent(back);
+#pragma unroll 1
+      for (int k0 = COLS * part; k0 < COLS * (part + 1); k0 += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float y[16];
+          scores(k0 + 16 * c, y);
+          float w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            l += exp2_approx(y[k] + far);
+            w[k] = y[k] == -INFINITY ? 0.f : exp2_approx(y[k]) * (by_key ? num.sv[k0 + 16 * c + k] : 1.f);   // (0 times a NaN)
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) pk[8 * c + k] = pack_half2(w[2 * k], w[2 * k + 1]);
+        }
+        if (HALVES == 2) pair_sync(bar);       // (P of the second half goes over scores of the first)
+        tmem_st16(s_at + (k0 >> 1), pk);
+      }
+    };
+    auto step = [&](auto is_masked, int j, int key0, const Numbers::All& all) {
       constexpr bool masked = decltype(is_masked)::value;
       const uint32_t s_at = tbase + (2 * tile + (j & 1)) * BN;
       const Numbers& num = ctl.num[j & 7];
-      const float turn = num.turn;
-      const uint32_t gone = masked ? num.absent : 0u;
-      f32x2 t[COLS / 2];           // scores relative to the running maximum
+      const uint32_t gone = masked ? all.absent : 0u;
+      f32x2 t[COLS / 2];           // scores less lift and the running maximum
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      const f32x2 neg_m = pack2(-m, -m), row2 = BF ? pack2(row * num.down, row * num.down) : 0ull;
+      const float less = -m - all.lift, to_x = BF ? row * all.down : 0.f;
+      const f32x2 neg_m = pack2(less, less), row2 = pack2(to_x, to_x);
       float xs[COLS / 32][32];
 #pragma unroll
       for (int h = 0; h < COLS / 32; ++h) kq::tmem_ld32(s_at + 32 * (h + part), xs[h]);
@@ -674,46 +814,21 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         }
       }
       float high = max3(max3(top[0], top[1], top[2]), top[3], top[3]);
-      const bool moves = high > lag || turn != 1.f;
+      const bool moves = high > lag();
       // (two warps to a row: also before either writes P over scores of the other)
       if (HALVES == 2 ? pair_or(bar, moves || !ok) : __any_sync(0xffffffffu, moves)) {
         if constexpr (HALVES == 2) {
-          ctl.pair[part][tr] = make_float2(high, ok ? 1.f : 0.f);
-          pair_sync(bar);
-          const float2 other = ctl.pair[part ^ 1][tr];
-          high = max3(high, other.x, other.x);
-          // (this is the only way out of the steps, for both at once: neither waits in vain)
-          stop = !__all_sync(0xffffffffu, ok && other.y != 0.f);
-          ok = ok && !stop;
+          agree(high);
           if (stop) return;
         }
-        // the maximum moves by a whole number; what was summed before turns by a power of two
-        const bool up = high > lag;
-        const float by = up ? (high < INFINITY ? ceilf(high) - BASE : high) : 0.f;
-        const float al = up && lag == LAG ? exp2_approx(-by) : 1.f;
-        if (up) lag = LAG;
-        m += by;
-        const f32x2 down = pack2(-by, -by), al2 = pack2(al, al);
-        l2[0] = mul2(l2[0], al2);
-        l2[1] = mul2(l2[1], al2);
+        const float by = move(high, num.back, j);
+        const f32x2 down = pack2(-by, -by);
 #pragma unroll
         for (int k = 0; k < COLS / 2; ++k) t[k] = add2(t[k], down);
-        if (j > 0) {
-          ok = wait(&ctl.pv_done[tile], j - 1) && ok;
-          kq::tc_fence_after();
-          const float f = al * turn;
-#pragma unroll 1
-          for (int d = part * (D / HALVES); d < (part + 1) * (D / HALVES); d += 16) {
-            uint32_t o[16];
-            tmem_ld16(o_at + d, o);
-            kq::tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st16(o_at + d, o);
-          }
-        }
       }
       const ulonglong2* sv = reinterpret_cast<const ulonglong2*>(num.sv);
+      f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+      const float to_l = all.up * back;
 #pragma unroll
       for (int h = 0; h < COLS / 32; ++h) {
         uint32_t pk[16];
@@ -724,7 +839,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
           for (int k = 0; k < 2; ++k) {
             const float2 v = unpack2(t[16 * h + 2 * i + k]);
             const f32x2 p = pack2(exp2_approx(v.x), exp2_approx(v.y));
-            l2[k] = add2(l2[k], p);
+            sum[k] = add2(sum[k], p);
             float2 w = unpack2(BF ? p : mul2(p, k ? f.y : f.x));
             if constexpr (masked && !BF) {                     // (0 times a NaN scale)
               if (v.x == -INFINITY) w.x = 0.f;
@@ -735,6 +850,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         }
         tmem_st16(s_at + 16 * (h + part), pk);
       }
+      const float2 ls = unpack2(add2(sum[0], sum[1]));
+      l = fmaf(ls.x + ls.y, to_l, l);
     };
     for (int j = 0; j < steps; ++j) {
       ok = ok && wait(&ctl.s_full[tile][j & 1], j >> 1);
@@ -742,10 +859,27 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       if (HALVES == 1 && !ok) break;
       kq::tc_fence_after();
       const int key0 = key_of(i0 + j);
-      if (ctl.num[j & 7].absent || !(key0 + BN <= all_hi && (key0 >= all_lo || key0 + BN <= a.sinks)))
-        step(std::true_type{}, j, key0);
-      else
-        step(std::false_type{}, j, key0);
+      const Numbers::All all = ctl.num[j & 7].all;
+      // (probabilities that lie far below their place among l's need exponentials of their own)
+      // (which of the three copies comes first decides how the compiler lays out the others: 2 x
+      // 2048 tokens over 16k, heads of 128, bf16 1267 us this way round, 1399 the other; fp16
+      // 1433 and 1380; heads of 64, 2 x 1500 over 6000, 329 and 321)
+      if constexpr (BF && D >= 128) {
+        if ((all.absent & WIDE) || all.up * back_max > 0x1p30f)
+          any_step(j, key0, all);
+        else if (!all.absent && key0 + BN <= all_hi && (key0 >= all_lo || key0 + BN <= a.sinks))
+          step(std::false_type{}, j, key0, all);
+        else
+          step(std::true_type{}, j, key0, all);
+      } else {
+        const bool slow = (all.absent & WIDE) || all.up * back_max > 0x1p30f;
+        if (!slow && !all.absent && key0 + BN <= all_hi && (key0 >= all_lo || key0 + BN <= a.sinks))
+          step(std::false_type{}, j, key0, all);
+        else if (slow)
+          any_step(j, key0, all);
+        else
+          step(std::true_type{}, j, key0, all);
+      }
       if (HALVES == 2 && stop) break;
       kq::tmem_wait_st();
       kq::tc_fence_before();
@@ -756,8 +890,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       }
     }
     // ---- output
-    const float2 ls = unpack2(add2(l2[0], l2[1]));
-    float l = ls.x + ls.y;
     if constexpr (HALVES == 2) {
       pair_sync(bar);
       ctl.pair[part][tr].x = l;
@@ -767,8 +899,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     }
     if (steps > 0) ok = ok && wait(&ctl.o_full, 0);
     kq::tc_fence_after();
-    const float fv = steps > 0 ? ctl.num[(steps - 1) & 7].fv : 0.f;
-    const float rfv = fv != 0.f ? 1.f / fv : 0.f;
     const int row_in = ctl.unit.tile * R + 128 * tile + tr, to_head = ctl.unit.head;
     const bool mine = row_in < ctl.seq.n * a.g;
     const int64_t slot = ((int64_t)ctl.unit.slot * a.cache.heads + to_head) * R + 128 * tile + tr;
@@ -781,7 +911,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       static_assert(SH::Q_BYTES + SH::STAGES * SH::STAGE >= R * D * 4, "room for the output");
       constexpr int DP = D / HALVES;                   // dims of this warp's
       float* buf = reinterpret_cast<float*>(q_smem) + warp * 32 * DP;
-      const float f = split ? rfv : l == 0.f ? 0.f : rfv / l;
+      const float f = split ? back : l == 0.f ? 0.f : back / l;
+      m -= exponent(back);
 #pragma unroll 1
       for (int d = 0; d < DP; d += 32) {
         uint32_t o[32];
@@ -808,7 +939,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       if (mine && !split)
         to = reinterpret_cast<uint64_t>(static_cast<uint16_t*>(a.out) + (int64_t)out_row * a.o_st +
                                         (int64_t)hq * a.o_sh + part * DP);
-      if (mine && split && part == 0) a.part_ml[slot] = {lag == LAG ? m : NO_MAX, l};
+      if (mine && split && part == 0) a.part_ml[slot] = {back > 0.f ? m : NO_MAX, l};
       if (mine && !split && part == 0 && a.lse)
         a.lse[(int64_t)out_row * a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       __syncwarp();
