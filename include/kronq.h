@@ -413,10 +413,13 @@ int kronq_unpack(const uint32_t* packed, int64_t m, int64_t n, int bits,
  *
  * A batch that contradicts itself or the cache (a length beyond the table or
  * below the sequence's new tokens where that matters, a page number outside
- * the cache, a position outside the rotation table, rows beyond T) is noticed
- * on the device: `info` (optional device int32) becomes
+ * the cache, a position outside the rotation table, rows beyond T, a q_start that
+ * goes back) is noticed on the device: `info` (optional device int32) becomes
  * KRONQ_ERR_INVALID_ARG, nothing outside the caller's tensors is touched, and
- * tokens without a place are skipped (not written; keys nobody sees).
+ * tokens without a place are skipped (not written; keys nobody sees), and so are
+ * sequences whose rows leave the tensor.  Where
+ * q_start goes back, attention leaves out that sequence and the ones behind it; append
+ * and read-back take a row that several sequences claim for one of them.
  */
 enum kronq_dtype { KRONQ_BF16 = 0, KRONQ_FP16 = 1, KRONQ_FP32 = 2 };
 

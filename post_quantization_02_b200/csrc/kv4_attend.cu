@@ -207,11 +207,6 @@ __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_atte
   Unit u;
   if (!find_unit<R, BLK, THREADS>(a, &u)) return;
   const int head = u.head;
-  // (only a batch whose rows overlap can ask for more slots than there are)
-  if (u.nsplit > 1 && (u.slot < 0 || u.slot >= a.slots)) {
-    kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
-    return;
-  }
   const Seq s = seq_of(a, u.b, nullptr);
   if (threadIdx.x == 0 && head == 0 && u.tile == 0 && u.split == 0)
     a.meta[u.b] = make_int2(u.slot, u.nsplit);
@@ -667,12 +662,17 @@ __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, 
   __shared__ float sum_l[WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = blockIdx.x;
-  const int b = find_sequence(a.b.q_start, a.b.B, i);
-  const Seq s = seq_of(a, min(max(b, 0), a.b.B - 1), nullptr);
+  int b = find_sequence(a.b.q_start, a.b.B, i);
+  Seq s = seq_of(a, min(max(b, 0), a.b.B - 1), nullptr);
   // the attention kernel's results from here on (every thread waits: this kernel's
   // end stands for that one's too)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (b < 0 || b >= a.b.B) return;
+  const int good = a.meta[a.b.B].x;
+  if (good < a.b.B) {                    // (starts that go back: the search is over those in front)
+    b = good > 0 ? find_sequence(a.b.q_start, good, i) : -1;
+    s = seq_of(a, min(max(b, 0), a.b.B - 1), nullptr);
+  }
+  if (b < 0 || b >= good) return;
   if (i < s.row0 || i >= s.row0 + s.n) return;
   const int2 mt = a.meta[b];
   const int ns = mt.y;
@@ -686,7 +686,6 @@ __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, 
       if (hq >= a.Hq) return;
       const int head = hq / a.g, r = (i - s.row0) * a.g + hq - head * a.g;
       const int tile = r / R;
-      if (mt.x < 0 || mt.x + (tile + 1ll) * ns > a.slots) return;
       const int64_t stride = (int64_t)a.cache.heads * R;
       const int64_t s0 = ((int64_t)(mt.x + tile * ns) * a.cache.heads + head) * R + (r - tile * R);
       const Part q = lane < ns ? a.part_ml[s0 + lane * stride] : Part{-INFINITY, 0.f};
@@ -739,8 +738,6 @@ __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, 
     if (hq >= a.Hq) return;
     const int head = hq / a.g, r = (i - s.row0) * a.g + hq - head * a.g;
     const int tile = r / R;
-    // (overlapping rows: a sequence may have no numbers, or more splits than slots)
-    if (mt.x < 0 || mt.x + (tile + 1ll) * ns > a.slots) return;
     const int64_t stride = (int64_t)a.cache.heads * R;
     const int64_t s0 = ((int64_t)(mt.x + tile * ns) * a.cache.heads + head) * R + (r - tile * R);
     float m = -INFINITY;
@@ -841,7 +838,7 @@ Layout layout_of(const Way& w, int D, int heads, int64_t B) {
   const size_t rows = (size_t)max_slots(heads, w.resident) * heads * w.R;
   Layout l;
   l.meta = 0;
-  l.ml = up256((size_t)B * sizeof(int2));
+  l.ml = up256((size_t)(B + 1) * sizeof(int2));
   l.o = l.ml + up256(rows * sizeof(Part));
   l.total = l.o + up256(rows * D * sizeof(float));
   return l;
@@ -950,7 +947,6 @@ int kq_kv4_attention(const void* q, int64_t q_st, int64_t q_sh, int dtype, int64
   a.min_chunk = way.min_chunk;
   a.resident = way.resident;
   a.unit_cost = way.unit_cost;
-  a.slots = (int)max_slots(c.heads, way.resident);
   a.info = info;
   const Layout w = layout_of(way, D, c.heads, b.B);
   uint8_t* base = static_cast<uint8_t*>(ws);

@@ -43,8 +43,7 @@ struct AttendArgs {
   float unit_cost;       // what a unit costs beside its key blocks, in key blocks
   float* part_o;         // slots x heads x R x D
   Part* part_ml;         // slots x heads x R
-  int2* meta;            // per sequence: first slot, splits
-  int slots;             // there are that many
+  int2* meta;            // per sequence: first slot, splits; then the sequences that count
   int32_t* info;
 };
 
@@ -107,7 +106,9 @@ constexpr int CHOICES = 8;
 KQ_DEV int eighths(int k) { return k < 7 ? 8 + k : 16; }
 
 // Finds the block's unit (all threads call it; false: there is none); heads change
-// fastest, so blocks without one come last.  Of up to 32
+// fastest, so blocks without one come last.  Where q_start goes back, the sequences from there
+// on have none: their rows may be others' too, and units and slots are counted for rows that
+// are one sequence's.  Of up to 32
 // sequences every warp finds it by itself, one sequence a lane, without a barrier.
 // Work and costs are fp32 sums in one order, so all blocks agree; the chunk is
 // rounded up by more than their error, which keeps max_units a bound.
@@ -115,6 +116,7 @@ template <int R, int BLK, int THREADS>
 KQ_DEV bool find_unit(const AttendArgs& a, Unit* out) {
   constexpr int WARPS = THREADS / 32;
   __shared__ float sums[WARPS];
+  __shared__ int firsts[WARPS];
   __shared__ uint32_t counts[WARPS][CHOICES];
   __shared__ unsigned long long wsum[WARPS];
   __shared__ Unit found;
@@ -126,22 +128,38 @@ KQ_DEV bool find_unit(const AttendArgs& a, Unit* out) {
   const int b0 = min(a.b.B, wide ? tid * per : lane), b1 = min(a.b.B, b0 + per);
   int tiles1 = 0, blocks1 = 0;                 // kept when a thread has one sequence
   float work = 0.f;
+  int good = a.b.B;                            // the sequences that count
   for (int b = b0; b < b1; ++b) {
     bool bad;
     seq_work<R, BLK>(a, seq_of(a, b, &bad), &tiles1, &blocks1);
     if (bad && blockIdx.x == 0) kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
+    if (bad && a.b.q_start[b + 1] < a.b.q_start[b]) good = min(good, b);
     work += (float)tiles1 * (float)blocks1;
   }
+  good = __reduce_min_sync(0xffffffffu, good);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
   if (wide) {
-    if (lane == 0) sums[warp] = work;
+    if (lane == 0) {
+      sums[warp] = work;
+      firsts[warp] = good;
+    }
     if (tid == 0) found.b = -1;
     __syncthreads();
     work = 0.f;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) work += sums[w];
+    for (int w = 0; w < WARPS; ++w) {
+      work += sums[w];
+      good = min(good, firsts[w]);
+    }
   }
+  if (blockIdx.x == 0 && tid == 0) a.meta[a.b.B] = make_int2(good, 0);
+  if (b0 >= good) tiles1 = 0;
+  // (work counts the others too: the chunk is no smaller for it)
+  auto work_of = [&](int b) {
+    if (per > 1) seq_work<R, BLK>(a, seq_of(a, b, nullptr), &tiles1, &blocks1);
+    if (b >= good) tiles1 = 0;
+  };
   work *= a.cache.heads;
   // lane k: the chunk of choice k % CHOICES
   const float aim = 0.125f * (float)(eighths(lane % CHOICES) * a.resident);
@@ -156,7 +174,7 @@ KQ_DEV bool find_unit(const AttendArgs& a, Unit* out) {
       r[k] = __shfl_sync(0xffffffffu, mine_r, k);
     }
     for (int b = b0; b < b1; ++b) {
-      if (per > 1) seq_work<R, BLK>(a, seq_of(a, b, nullptr), &tiles1, &blocks1);
+      work_of(b);
 #pragma unroll
       for (int k = 0; k < CHOICES; ++k)
         n[k] += (float)tiles1 * fmaxf(1.f, ceilf((float)blocks1 * r[k]));
@@ -184,7 +202,7 @@ KQ_DEV bool find_unit(const AttendArgs& a, Unit* out) {
   // low half: units; high half: those that need a slot
   unsigned long long units = 0;
   for (int b = b0; b < b1; ++b) {
-    if (per > 1) seq_work<R, BLK>(a, seq_of(a, b, nullptr), &tiles1, &blocks1);
+    work_of(b);
     const int ns = max(1, ceil_div(blocks1, chunk));
     const unsigned long long k = (unsigned long long)tiles1 * ns;
     units += k + (ns > 1 ? k << 32 : 0);
@@ -207,7 +225,7 @@ KQ_DEV bool find_unit(const AttendArgs& a, Unit* out) {
   Unit x = {-1, 0, 0, 1, out->head, 0};
   if (u >= base && u < base + (int)(uint32_t)units) {
     for (int b = b0; b < b1; ++b) {
-      if (per > 1) seq_work<R, BLK>(a, seq_of(a, b, nullptr), &tiles1, &blocks1);
+      work_of(b);
       const int ns = max(1, ceil_div(blocks1, chunk)), k = tiles1 * ns;
       if (u < base + k) {
         x.tile = (u - base) / ns;

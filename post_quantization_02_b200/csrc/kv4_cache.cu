@@ -61,6 +61,25 @@ KQ_DEV int64_t page_of(const Batch& b, const Cache& c, int s, int at) {
   return id >= 0 && id < c.pages ? id : -1;
 }
 
+// The index of row i of sequence s among its tokens; negative where the sequence's rows are not
+// rows of the tensor or end in front of i (starts that go back).
+KQ_DEV int index_of(const Batch& b, int s, int i, int T) {
+  const int s0 = b.q_start[s], s1 = b.q_start[s + 1], len = b.kv_len[s];
+  return s0 >= 0 && s1 <= T && i < s1 ? len - (s1 - i) : -1;
+}
+
+// Block 0 looks for row starts that go back or leave the tensor's rows (after a search, which
+// leaves them in L1).
+KQ_DEV void check_starts(const Batch& b, int T, int32_t* info) {
+  if (blockIdx.x || blockIdx.y) return;
+  bool bad = false;
+  for (int s = threadIdx.x; s < b.B; s += TPB) {
+    const int s0 = b.q_start[s], s1 = b.q_start[s + 1];
+    bad |= s0 < 0 || s1 < s0 || s1 > T;
+  }
+  if (bad) kq::record_error(info, KRONQ_ERR_INVALID_ARG);
+}
+
 // Products that are rounded by themselves: packed ones (and fused ones with a zero) are
 // contracted with the packed sum behind them.
 KQ_DEV f32x2 mul2_rn(f32x2 a, f32x2 b) {
@@ -106,8 +125,9 @@ __global__ void __launch_bounds__(TPB, D == 64 ? 6 : D == 128 ? 5 : 4) kv4_appen
   };
   ask(item);
   const int s = find_sequence(a.b.q_start, a.b.B, i);
+  check_starts(a.b, a.T, a.info);
   if (s < 0 || s >= a.b.B) return;                       // a row of no sequence
-  const int at = a.b.kv_len[s] - (a.b.q_start[s + 1] - i);
+  const int at = index_of(a.b, s, i, a.T);
   const int64_t pos = a.positions ? a.positions[i] : at;
   const bool placed = at >= 0 && (!a.rot || (pos >= 0 && pos < a.table_rows));
   const int64_t page = placed ? page_of(a.b, a.cache, s, at) : -1;
@@ -351,7 +371,7 @@ __global__ void __launch_bounds__(TPB) kv4_gather_kernel(const GatherArgs a) {
     if (i < a.T) {                         // (the same in the whole warp)
       const int s = find_sequence(a.b.q_start, a.b.B, i);
       if (s >= 0 && s < a.b.B) {
-        const int at = a.b.kv_len[s] - (a.b.q_start[s + 1] - i);
+        const int at = index_of(a.b, s, i, a.T);
         const int64_t page = page_of(a.b, a.cache, s, at);
         if (page >= 0) {
           p = a.cache.base + page * Hkv * (int64_t)a.cache.block_bytes;
@@ -366,6 +386,7 @@ __global__ void __launch_bounds__(TPB) kv4_gather_kernel(const GatherArgs a) {
       slots[n] = slot;
     }
   }
+  check_starts(a.b, a.T, a.info);
   __syncthreads();
   const int l = threadIdx.x & 7;
   constexpr int U = N == 1 ? 1 : 4;        // vectors in flight

@@ -258,11 +258,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
   Unit u;
   if (!find_unit<R, BN, THREADS>(a, &u)) return;
   const int head = u.head;
-  // (only a batch whose rows overlap can ask for more slots than there are)
-  if (u.nsplit > 1 && (u.slot < 0 || u.slot >= a.slots)) {
-    kq::record_error(a.info, KRONQ_ERR_INVALID_ARG);
-    return;
-  }
   const Seq s = seq_of(a, u.b, nullptr);
   if (threadIdx.x == 0 && head == 0 && u.tile == 0 && u.split == 0)
     a.meta[u.b] = make_int2(u.slot, u.nsplit);

@@ -5,8 +5,10 @@ import numpy as np
 import pytest
 import torch
 
+from gpu_helpers import t
+from oracle import kv4 as ok
 from post_quantization_02_b200 import abi, kv4
-from test_gpu_kv4 import Setup
+from test_gpu_kv4 import Setup, check_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +72,82 @@ def test_allocations_belong_to_the_given_stream(cuda, new):
             torch.full((n,), 127, dtype=torch.uint8, device=cuda)
         torch.cuda.synchronize()
         assert torch.equal(got_q, want_q) and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("new,heads", [(1, 2), (90, 2), (2, 1)])
+@pytest.mark.parametrize("B,first", [(3, 1), (20, 7), (40, 33), (300, 200), (2000, 1200)])
+def test_row_starts_that_decrease(cuda, new, heads, B, first):
+    """Where q_start goes back, that sequence and the ones behind it, whose rows others may claim, are
+    left out: noticed, the ones in front are right, and what an earlier call left in the workspace
+    has no part in the result."""
+    r = np.random.default_rng(B)
+    L, D = 3000, 128
+    st = Setup(cuda, r, [new], [L], heads, D, 64)
+    st.fill_fast(torch.Generator(cuda).manual_seed(5))
+    bt = t(np.repeat(st.bt, B, 0), cuda)                  # (all over the same pages)
+    T, g = B * new, 4
+    q = torch.randn(T, heads * g, D, device=cuda).bfloat16()
+    kv = torch.randint(L // 2, L + 1, (B,), generator=torch.Generator(cuda).manual_seed(6), device=cuda,
+                       dtype=torch.int32)
+    start = torch.arange(B + 1, device=cuda, dtype=torch.int32) * new
+    need = abi.kronq_kv4_attention_workspace_size(T, heads * g, heads, D, B)
+    ws = torch.empty(need, dtype=torch.uint8, device=cuda)
+    good = kv4.attend(q, st.cache, bt, start, kv, ws=ws)
+    stale = ws.clone()
+    bad = start.clone()
+    bad[first + 1:] -= (start[first + 1] - start[first // 2]).item()     # rows from here on a second time
+    info = torch.zeros(1, dtype=torch.int32, device=cuda)
+    outs = []
+    for fill in ("stale", 0, 127):
+        ws.copy_(stale) if fill == "stale" else ws.fill_(fill)
+        info.zero_()
+        lse = torch.full((T, heads * g), 5.0, device=cuda)
+        out = torch.full_like(q, 5.0)
+        kv4.attend(q, st.cache, bt, bad, kv, out=out, lse=lse, ws=ws, info=info)
+        assert info.item() == -1
+        outs.append((out, lse))
+    n = first * new                                       # rows of the sequences in front
+    for out, lse in outs:
+        assert torch.equal(out, outs[0][0]) and torch.equal(lse, outs[0][1])
+        assert (out[n:] == 5).all() and (lse[n:] == 5).all()
+    # (fewer sequences are split otherwise: not the same bits)
+    seqs = sorted({0, first - 1})
+    st.new, st.kv, st.start = [new] * B, kv.tolist(), start.cpu().numpy()
+    st.bt = bt.cpu().numpy()
+    check_attention(st, q, outs[0][0], D ** -0.5, rows=[0, new // 2, new - 1], seqs=seqs)
+    check_attention(st, q, good, D ** -0.5, rows=[0], seqs=seqs)
+
+
+@pytest.mark.parametrize("heads", [1, 8])
+def test_append_and_gather_notice_bad_rows(cuda, heads):
+    """q_start that goes back or leaves the tensor's rows is noticed; no token goes to a place that is
+    not one of its sequence's new tokens."""
+    r = np.random.default_rng(50)
+    D, P, B, n = 64, 16, 100, 3
+    st = Setup(cuda, r, [n] * B, [40] * B, heads, D, P)
+    T = B * n
+    k = torch.randn(T, heads, D, device=cuda).bfloat16()
+    info = torch.zeros(1, dtype=torch.int32, device=cuda)
+    kv4.append(None, k, k, st.cache, *st.args, info=info)
+    kv4.gather(st.cache, *st.args, tokens=T, head_dim=D, info=info)
+    assert info.item() == 0
+    back, beyond, before = (st.args[1].clone() for _ in range(3))
+    back[60:] -= 50 * n
+    beyond[B] = T + 2
+    before[0] = -2
+    for start in (back, beyond, before):
+        st.cache.fill_(255)
+        info.zero_()
+        kv4.append(None, k, k, st.cache, st.args[0], start, st.args[2], info=info)
+        assert info.item() == -1
+        # only slots 37 .. 39 of a sequence can be new tokens
+        raw = st.cache.cpu().numpy()
+        for b in range(B):
+            blk = raw[st.bt[b]]
+            kc, _, kw, _ = ok.split_block(blk, P, D)
+            free = np.ones((3, P), dtype=bool)
+            free[2, 5:8] = False
+            assert (kw[np.broadcast_to(free[:, None], kw.shape)] == 0xFFFFFFFF).all()
+        info.zero_()
+        kv4.gather(st.cache, st.args[0], start, st.args[2], tokens=T, head_dim=D, info=info)
+        assert info.item() == -1
