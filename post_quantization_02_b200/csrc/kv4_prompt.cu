@@ -451,9 +451,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     auto seen = [&](int t) { return t < any_hi && (t >= any_lo || t < a.sinks); };
     auto ask_page = [&](int j) -> int {
       const int t0 = key_of(i0 + j) + GROUP * lane;
-      // (a table entry of INT32_MIN is taken for keys that are not seen)
+      // (INT32_MIN: nobody sees the group's keys; a negative entry becomes -1)
       if (j >= steps || lane >= GROUPS || !(t0 < any_hi && (t0 + GROUP > any_lo || t0 < a.sinks))) return INT32_MIN;
-      return (int)load4(reinterpret_cast<const uint32_t*>(a.b.table + u.b * a.b.table_ld + (t0 >> a.cache.lgP)));
+      return max(-1, (int)load4(reinterpret_cast<const uint32_t*>(a.b.table + u.b * a.b.table_ld + (t0 >> a.cache.lgP))));
     };
     struct Words {
       uint32_t k[2], v[2];

@@ -151,3 +151,20 @@ def test_append_and_gather_notice_bad_rows(cuda, heads):
         info.zero_()
         kv4.gather(st.cache, st.args[0], start, st.args[2], tokens=T, head_dim=D, info=info)
         assert info.item() == -1
+
+
+@pytest.mark.parametrize("new", [1, 90])
+@pytest.mark.parametrize("entry", [-2 ** 31, -1, 2 ** 31 - 1])
+def test_any_bad_page_number_is_noticed(cuda, new, entry):
+    r = np.random.default_rng(51)
+    st = Setup(cuda, r, [new], [400], 1, 128, 64)
+    st.fill_fast(torch.Generator(cuda).manual_seed(7))
+    q = torch.randn(st.T, 4, 128, device=cuda).half()
+    bt = st.bt.copy()
+    bt[0, 2] = entry
+    info = torch.zeros(1, dtype=torch.int32, device=cuda)
+    kv4.attend(q, st.cache, t(bt, cuda), *st.args[1:], info=info)
+    assert info.item() == -1
+    info.zero_()                                   # nobody sees it: it may be anything
+    kv4.attend(q, st.cache, t(bt, cuda), *st.args[1:], window=100, info=info)
+    assert info.item() == 0
