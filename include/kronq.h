@@ -409,7 +409,8 @@ int kronq_unpack(const uint32_t* packed, int64_t m, int64_t n, int bits,
  * q_start[b]) + i; tokens page_size t .. lie in page block_table[b table_ld + t],
  * t < max_pages.  Rows in front of q_start[0] and from q_start[batch] up to T
  * are padding: what they hold does not matter, and they are never written.  Pages may be shared between
- * sequences for reading; two new tokens must not have the same place.
+ * sequences for reading; two new tokens must not have the same place.  T = 0 is no
+ * error, with batch = 0 too (block_table and kv_len may then be NULL).
  *
  * A batch that contradicts itself or the cache (a length beyond the table or
  * below the sequence's new tokens where that matters, a page number outside

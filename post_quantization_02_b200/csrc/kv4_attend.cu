@@ -917,7 +917,7 @@ int kq_kv4_attention(const void* q, int64_t q_st, int64_t q_sh, int dtype, int64
       (window && !causal) || !(scale == scale))
     return KRONQ_ERR_INVALID_ARG;
   if (T == 0) return KRONQ_OK;
-  if (!q || !out || !kqh::aligned(q, 2) || !kqh::aligned(out, 8) || q_st < 0 || q_sh < 0 || o_st < 0 ||
+  if (!b.B || !q || !out || !kqh::aligned(q, 2) || !kqh::aligned(out, 8) || q_st < 0 || q_sh < 0 || o_st < 0 ||
       o_sh < 0 || o_st % 4 || o_sh % 4 || !kqh::aligned(lse, 4))
     return KRONQ_ERR_INVALID_ARG;
   if (!ws || !kqh::aligned(ws, 256) || ws_bytes < kq_kv4_attention_ws(T, Hq, c.heads, D, b.B))

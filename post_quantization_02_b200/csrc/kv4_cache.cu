@@ -450,10 +450,11 @@ int kq_kv4_views(void* cache, int64_t pages, int page_size, int heads, int D, co
   if (D != 64 && D != 128 && D != 256) return KRONQ_ERR_UNSUPPORTED;
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256)
     return KRONQ_ERR_UNSUPPORTED;
-  if (!cache || !q_start || !kv_len || pages <= 0 || pages > INT32_MAX || heads <= 0 || heads > 65535 ||
-      B <= 0 || B > (1 << 20))
+  // (no sequences: their tensors have no memory; calls with tokens refuse it)
+  if (!cache || (B && (!q_start || !kv_len)) || pages <= 0 || pages > INT32_MAX || heads <= 0 ||
+      heads > 65535 || B < 0 || B > (1 << 20))
     return KRONQ_ERR_INVALID_ARG;
-  if (max_pages < 0 || table_ld < max_pages || (max_pages && !table)) return KRONQ_ERR_INVALID_ARG;
+  if (max_pages < 0 || table_ld < max_pages || (B && max_pages && !table)) return KRONQ_ERR_INVALID_ARG;
   if (max_pages > (1 << 30) / page_size) return KRONQ_ERR_UNSUPPORTED;   // token indices stay below 2^30
   if (!kqh::aligned(cache, 16) || !kqh::aligned(table, 4) || !kqh::aligned(q_start, 4) ||
       !kqh::aligned(kv_len, 4))
@@ -496,6 +497,7 @@ int kq_kv4_append(const void* q, int64_t q_st, int64_t q_sh, const void* k, int6
   if (rot && (!table || table_rows <= 0 || !kqh::aligned(table, 16))) return KRONQ_ERR_INVALID_ARG;
   if (!kqh::aligned(positions, 4) || !kqh::aligned(signs, 8)) return KRONQ_ERR_INVALID_ARG;
   if (T == 0) return KRONQ_OK;
+  if (!b.B) return KRONQ_ERR_INVALID_ARG;
   AppendArgs a = {};
   if (!rows_ok(k, k_st, k_sh, &a.k) || !rows_ok(v, v_st, v_sh, &a.v)) return KRONQ_ERR_INVALID_ARG;
   if (Hq) {
@@ -534,7 +536,7 @@ int kq_kv4_gather(void* k_out, void* v_out, int dtype, int64_t T, int D, const C
   if (dtype != BF16 && dtype != FP16 && dtype != FP32) return KRONQ_ERR_UNSUPPORTED;
   if (T < 0) return KRONQ_ERR_INVALID_ARG;
   if (T == 0) return KRONQ_OK;
-  if (!k_out || !v_out || !kqh::aligned(k_out, 16) || !kqh::aligned(v_out, 16)) return KRONQ_ERR_INVALID_ARG;
+  if (!b.B || !k_out || !v_out || !kqh::aligned(k_out, 16) || !kqh::aligned(v_out, 16)) return KRONQ_ERR_INVALID_ARG;
   GatherArgs a = {};
   a.k_out = k_out;
   a.v_out = v_out;

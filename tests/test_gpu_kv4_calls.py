@@ -168,3 +168,20 @@ def test_any_bad_page_number_is_noticed(cuda, new, entry):
     info.zero_()                                   # nobody sees it: it may be anything
     kv4.attend(q, st.cache, t(bt, cuda), *st.args[1:], window=100, info=info)
     assert info.item() == 0
+
+
+def test_an_empty_step(cuda):
+    """No sequences: nothing to do, and no error."""
+    D, cache = 128, kv4.make_cache(3, 16, 2, 128, cuda)
+    cache.fill_(9)
+    batch = (torch.empty(0, 4, dtype=torch.int32, device=cuda), torch.zeros(1, dtype=torch.int32, device=cuda),
+             torch.empty(0, dtype=torch.int32, device=cuda))
+    k = torch.empty(0, 2, D, dtype=torch.bfloat16, device=cuda)
+    q = torch.empty(0, 8, D, dtype=torch.bfloat16, device=cuda)
+    info = torch.zeros(1, dtype=torch.int32, device=cuda)
+    assert kv4.append(q, k, k, cache, *batch, rope=kv4.rope_table(8, D, device=cuda), info=info).shape == q.shape
+    assert kv4.attend(q, cache, *batch, info=info).shape == q.shape
+    assert kv4.gather(cache, *batch, tokens=0, head_dim=D, info=info)[0].shape == k.shape
+    assert info.item() == 0 and (cache == 9).all()
+    with pytest.raises(abi.KronqError):
+        kv4.attend(torch.empty(1, 8, D, dtype=torch.bfloat16, device=cuda), cache, *batch)

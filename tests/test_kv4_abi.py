@@ -167,3 +167,15 @@ def test_calls_run_and_allocate_on_the_given_stream(monkeypatch):
         for name, current, args in rec.seen:
             assert current is s, name
             assert not any(type(a) is int and a == 77 for a in args), name
+
+
+def test_nothing_to_do(L):
+    """No sequences and no tokens (a step in which nothing is scheduled) is no error; tokens of no
+    sequence's are."""
+    empty = dict(T=0, B=0, kv=None, bt=None)
+    assert _append(L, **empty) == 0 and _attend(L, **empty) == 0 and _attend(L, **empty, ws=None, n=0) == 0
+    assert _append(L, **empty, k=None, v=None, q=None, q_out=None) == 0
+    assert L.kronq_kv4_gather(None, None, 0, 0, P, 8, 16, 2, 128, None, 4, 4, P, None, 0, None, None) == 0
+    for some in (dict(B=0), dict(B=0, kv=None, bt=None)):
+        assert _append(L, **some) == -1 and _attend(L, **some) == -1
+    assert _append(L, T=0, B=-1) == -1 and _attend(L, T=0, B=-1) == -1
