@@ -451,7 +451,7 @@ size_t kronq_kv4_block_bytes(int page_size, int head_dim);
  * KRONQ_FP16, last dimension contiguous, token and head strides in elements
  * (>= 0; any, with addresses and strides that are multiples of 16 bytes read
  * fastest).  q_out: T x q_heads x head_dim contiguous, 16-byte aligned, same
- * type.  q_heads = 0: no queries (q, q_out NULL).
+ * type; q itself or apart from q, k and v.  q_heads = 0: no queries (q, q_out NULL).
  */
 int kronq_kv4_append(const void* q, int64_t q_stride_t, int64_t q_stride_h,
                      const void* k, int64_t k_stride_t, int64_t k_stride_h,
@@ -497,7 +497,8 @@ int kronq_kv4_gather(void* k_out, void* v_out, int dtype, int64_t T,
  * where there are many rows).
  *
  * q (T x q_heads x head_dim), out (same): KRONQ_BF16 or KRONQ_FP16, strides in
- * elements as above; out 8-byte aligned with strides that are multiples of 4.
+ * elements as above; out 8-byte aligned with strides that are multiples of 4, its
+ * rows apart from each other and, unless it is q (same strides), from q's.
  * q_heads is a multiple of heads; query head h reads key/value head
  * h / (q_heads / heads).  lse: optional T x q_heads fp32, the natural
  * log-sum-exp of the scaled scores (-inf where no key is seen), to join results

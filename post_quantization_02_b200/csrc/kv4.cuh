@@ -156,6 +156,19 @@ KQ_DEV int find_sequence(const int32_t* __restrict__ q_start, int B, int i) {
 }  // namespace kv4
 
 // Host side (kv4_cache.cu, kv4_attend.cu).
+// T x H rows of D 16-bit elements, strides of the token and of the head.
+struct KqRows {
+  const void* p;
+  int64_t st, sh, T, H, D;
+  uintptr_t begin() const { return reinterpret_cast<uintptr_t>(p); }
+  uintptr_t end() const { return begin() + 2 * ((T - 1) * st + (H - 1) * sh + D); }
+  bool meets(const KqRows& o) const { return begin() < o.end() && o.begin() < end(); }    // as ranges
+  // no two rows share memory (token-major or head-major)
+  bool apart() const {
+    return ((H == 1 || sh >= D) && (T == 1 || st >= (H - 1) * sh + D)) ||
+           ((T == 1 || st >= D) && (H == 1 || sh >= (T - 1) * st + D));
+  }
+};
 // The checks every entry point of the cache shares; fills the kernels' views.
 int kq_kv4_views(void* cache, int64_t pages, int page_size, int heads, int D, const int32_t* table,
                  int64_t table_ld, int64_t max_pages, const int32_t* q_start, const int32_t* kv_len,

@@ -920,6 +920,17 @@ int kq_kv4_attention(const void* q, int64_t q_st, int64_t q_sh, int dtype, int64
   if (!b.B || !q || !out || !kqh::aligned(q, 2) || !kqh::aligned(out, 8) || q_st < 0 || q_sh < 0 || o_st < 0 ||
       o_sh < 0 || o_st % 4 || o_sh % 4 || !kqh::aligned(lse, 4))
     return KRONQ_ERR_INVALID_ARG;
+  // The output may lie over the queries (a block reads its rows before it writes them); any other
+  // overlap would be a race.  With equal strides, rows that interleave are told from those that
+  // overlap by where they lie within a token.
+  const KqRows from = {q, q_st, q_sh, T, Hq, D}, to = {out, o_st, o_sh, T, Hq, D};
+  if (!to.apart()) return KRONQ_ERR_INVALID_ARG;
+  if (from.meets(to) && !(q == out && (T == 1 || q_st == o_st) && (Hq == 1 || q_sh == o_sh))) {
+    const int64_t span = (Hq - 1) * o_sh + D;
+    if (T == 1 || q_st != o_st || q_sh != o_sh || o_st < span) return KRONQ_ERR_INVALID_ARG;
+    const int64_t at = ((static_cast<const uint16_t*>(out) - static_cast<const uint16_t*>(q)) % o_st + o_st) % o_st;
+    if (at < span || at + span > o_st) return KRONQ_ERR_INVALID_ARG;
+  }
   if (!ws || !kqh::aligned(ws, 256) || ws_bytes < kq_kv4_attention_ws(T, Hq, c.heads, D, b.B))
     return KRONQ_ERR_WORKSPACE;
   const int g = Hq / c.heads;

@@ -223,8 +223,10 @@ __global__ void __launch_bounds__(TPB, D == 64 ? 6 : D == 128 ? 5 : 4) kv4_appen
         }
       }
     }
-    // (the next vector comes while this one is transformed)
+    // (the next vector comes while this one is transformed; what this one's lanes read of each
+    // other is read before any of them writes)
     ask(item + stride);
+    __syncwarp();
 
     if (a.signs && __any_sync(0xffffffffu, kind < 2)) {
       f32x2 y[R][4];
@@ -502,6 +504,13 @@ int kq_kv4_append(const void* q, int64_t q_st, int64_t q_sh, const void* k, int6
   if (!rows_ok(k, k_st, k_sh, &a.k) || !rows_ok(v, v_st, v_sh, &a.v)) return KRONQ_ERR_INVALID_ARG;
   if (Hq) {
     if (!rows_ok(q, q_st, q_sh, &a.q) || !q_out || !kqh::aligned(q_out, 16)) return KRONQ_ERR_INVALID_ARG;
+    // A vector is read by its own 8 lanes before they write it, so queries may be rotated where
+    // they lie; any other overlap would be a race.
+    const KqRows to = {q_out, (int64_t)Hq * D, D, T, Hq, D};
+    const bool in_place = q == q_out && (T == 1 || q_st == to.st) && (Hq == 1 || q_sh == to.sh);
+    if ((!in_place && to.meets({q, q_st, q_sh, T, Hq, D})) || to.meets({k, k_st, k_sh, T, c.heads, D}) ||
+        to.meets({v, v_st, v_sh, T, c.heads, D}))
+      return KRONQ_ERR_INVALID_ARG;
   }
   a.q_out = static_cast<uint16_t*>(q_out);
   a.cache = c;

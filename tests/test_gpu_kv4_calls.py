@@ -185,3 +185,46 @@ def test_an_empty_step(cuda):
     assert info.item() == 0 and (cache == 9).all()
     with pytest.raises(abi.KronqError):
         kv4.attend(torch.empty(1, 8, D, dtype=torch.bfloat16, device=cuda), cache, *batch)
+
+
+@pytest.mark.parametrize("D,rot,inter,signs", [(128, 128, False, False), (128, 64, False, False), (64, 64, False, True),
+                                               (256, 128, False, False), (128, 32, True, False)])
+@pytest.mark.parametrize("T", [5, 2000])
+def test_queries_rotated_in_place(cuda, D, rot, inter, signs, T):
+    r = np.random.default_rng(52)
+    st = Setup(cuda, r, [T], [T], 2, D, 64)
+    q = torch.randn(T, 6, D, device=cuda).bfloat16()
+    k = torch.randn(T, 2, D, device=cuda).bfloat16()
+    sg = t((1 - 2 * r.integers(0, 2, D)).astype(np.int8), cuda) if signs else None
+    more = dict(rope=kv4.rope_table(T, rot, device=cuda), interleaved=inter, signs=sg)
+    want = kv4.append(q, k, k, st.cache, *st.args, **more)
+    got = q.clone()
+    kv4.append(got, k, k, st.cache, *st.args, q_out=got, **more)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("new", [1, 90])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_attention_over_its_queries(cuda, new, dtype):
+    """The output over the queries, contiguous and within a projection's rows; beside them."""
+    r = np.random.default_rng(53)
+    st = Setup(cuda, r, [new, new], [9000, 500], 2, 128, 64)
+    st.fill_fast(torch.Generator(cuda).manual_seed(8))
+    q = torch.randn(st.T, 8, 128, device=cuda).to(dtype)
+    want = kv4.attend(q, st.cache, *st.args)
+    got = q.clone()
+    kv4.attend(got, st.cache, *st.args, out=got)
+    assert torch.equal(got, want)
+    wide = torch.randn(st.T, 20, 128, device=cuda).to(dtype)
+    keep = wide.clone()
+    wide[:, 3:11] = q
+    kv4.attend(wide[:, 3:11], st.cache, *st.args, out=wide[:, 11:19])
+    assert torch.equal(wide[:, 11:19], want) and torch.equal(wide[:, 3:11], q)
+    kv4.attend(wide[:, 3:11], st.cache, *st.args, out=wide[:, 3:11])
+    assert torch.equal(wide[:, 3:11], want)
+    assert torch.equal(wide[:, :3], keep[:, :3]) and torch.equal(wide[:, 19:], keep[:, 19:])
+    for out in (wide[:, 4:12], wide[:, 1:9]):
+        with pytest.raises(abi.KronqError):
+            kv4.attend(wide[:, 3:11], st.cache, *st.args, out=out)
+    with pytest.raises(abi.KronqError):
+        kv4.attend(q, st.cache, *st.args, out=want[:, :1].expand(st.T, 8, 128))

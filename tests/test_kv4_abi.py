@@ -179,3 +179,32 @@ def test_nothing_to_do(L):
     for some in (dict(B=0), dict(B=0, kv=None, bt=None)):
         assert _append(L, **some) == -1 and _attend(L, **some) == -1
     assert _append(L, T=0, B=-1) == -1 and _attend(L, T=0, B=-1) == -1
+
+
+def at(elements):
+    """An address so many 16-bit elements behind P."""
+    return ctypes.c_void_p(P.value + 2 * elements)
+
+
+@pytest.mark.parametrize("kw,code", [
+    # rows of the output that share memory
+    (dict(ot=0), -1), (dict(oh=0), -1), (dict(ot=256), -1), (dict(oh=64), -1), (dict(ot=508), -1),
+    (dict(ot=128, oh=508), -1), (dict(T=1, ot=0), -6), (dict(ot=128, oh=512), -6), (dict(ot=1024, oh=256), -6),
+    # the output over the queries: only as they lie
+    (dict(out=at(0)), -6), (dict(out=at(128)), -1), (dict(out=at(512)), -1), (dict(out=at(4 * 512)), -6),
+    (dict(q=at(512), out=at(0)), -1), (dict(out=at(0), ot=1024), -1),
+    # ... or beside them in the same buffer
+    (dict(qt=1024, ot=1024, out=at(512)), -6), (dict(qt=1024, ot=1024, out=at(1024 + 512)), -6),
+    (dict(qt=1024, ot=1024, out=at(508)), -1), (dict(qt=1024, ot=1024, out=at(516)), -1),
+    (dict(qt=1024, ot=1024, out=at(1024)), -1),
+])
+def test_outputs_that_overlap(L, kw, code):
+    """-6: the arguments are taken (the workspace, which is too small here, is looked at last)."""
+    assert _attend(L, **{**dict(n=0, out=at(1 << 20)), **kw}) == code
+
+
+@pytest.mark.parametrize("kw", [dict(q_out=at(8)), dict(q_out=at(512)), dict(q=at(512)), dict(qt=1024),
+                                dict(qh=256, qt=1024), dict(k=at(16)), dict(k=at(2047)), dict(v=at(1000))])
+def test_rotated_queries_that_overlap_inputs(L, kw):
+    far = dict(q=P, q_out=P, k=at(1 << 20), v=at(1 << 21))
+    assert _append(L, **{**far, **kw}) == -1
