@@ -59,8 +59,12 @@ def _build_binding(force: bool = False) -> None:
     import torch
     from torch.utils import cpp_extension
 
-    if not force and BINDING.exists() and BINDING.stat().st_mtime >= max(
-            p.stat().st_mtime for p in (BINDING_SRC, *INCLUDE.glob("*.h"))):
+    # the torch and the interpreter it is built against: another one's would not fit it
+    against = f"{torch.__version__} {sys.version}"
+    stamp = OBJ / "_kv4.built_against"
+    if (not force and BINDING.exists() and BINDING.stat().st_mtime >= max(
+            p.stat().st_mtime for p in (BINDING_SRC, *INCLUDE.glob("*.h")))
+            and stamp.exists() and stamp.read_text() == against):
         return
     lib = pathlib.Path(torch.__file__).resolve().parent / "lib"
     cuda = pathlib.Path(nvcc()).resolve().parents[1]
@@ -73,6 +77,8 @@ def _build_binding(force: bool = False) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"building the torch binding failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    OBJ.mkdir(exist_ok=True)
+    stamp.write_text(against)
 
 
 def build(force: bool = False, verbose: bool = False) -> pathlib.Path:

@@ -2,6 +2,7 @@
 (nothing is launched) and through the binding's own checks."""
 
 import ctypes
+import pathlib
 
 import pytest
 import torch
@@ -208,3 +209,31 @@ def test_outputs_that_overlap(L, kw, code):
 def test_rotated_queries_that_overlap_inputs(L, kw):
     far = dict(q=P, q_out=P, k=at(1 << 20), v=at(1 << 21))
     assert _append(L, **{**far, **kw}) == -1
+
+
+def test_binding_is_rebuilt_for_another_torch(L, monkeypatch, tmp_path):
+    """The binding is compiled against torch's headers: with another torch installed it is stale."""
+    calls = []
+
+    class Done:
+        returncode, stdout, stderr = 0, "", ""
+
+    def run(cmd, **kw):
+        calls.append(cmd)
+        pathlib.Path(cmd[cmd.index("-o") + 1]).write_bytes(b"")
+        return Done()
+
+    src = tmp_path / "kv4_torch.cpp"
+    src.write_text("")
+    monkeypatch.setattr(build, "BINDING", tmp_path / "_kv4.so")
+    monkeypatch.setattr(build, "BINDING_SRC", src)
+    monkeypatch.setattr(build, "INCLUDE", tmp_path)
+    monkeypatch.setattr(build, "OBJ", tmp_path / "_build")
+    monkeypatch.setattr(build.subprocess, "run", run)
+    build._build_binding()
+    build._build_binding()
+    assert len(calls) == 1
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    build._build_binding()
+    build._build_binding()
+    assert len(calls) == 2
