@@ -228,3 +228,99 @@ def test_attention_over_its_queries(cuda, new, dtype):
             kv4.attend(wide[:, 3:11], st.cache, *st.args, out=out)
     with pytest.raises(abi.KronqError):
         kv4.attend(q, st.cache, *st.args, out=want[:, :1].expand(st.T, 8, 128))
+
+
+def small_call(cuda):
+    """Arguments that each call takes as they are."""
+    cache = kv4.make_cache(4, 16, 2, 128, cuda)
+    cache.zero_()
+    q = torch.zeros(3, 4, 128, dtype=torch.bfloat16, device=cuda)
+    k = torch.zeros(3, 2, 128, dtype=torch.bfloat16, device=cuda)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=cuda)  # noqa: E731
+    return q, k, cache, i32(0, 1, 2, 3)[None], i32(0, 3), i32(3)
+
+
+def test_append_refusals_on_the_device(cuda):
+    q, k, cache, bt, qs, kv = small_call(cuda)
+    good = dict(q=q, k=k, v=k, cache=cache, block_table=bt, q_start=qs, kv_len=kv)
+    rope, signs = torch.zeros(4, 128, device=cuda), torch.ones(128, dtype=torch.int8, device=cuda)
+    good.update(rope=rope, signs=signs, positions=torch.zeros(3, dtype=torch.int32, device=cuda),
+                info=torch.zeros(1, dtype=torch.int32, device=cuda), q_out=torch.empty_like(q))
+    kv4.append(**good)
+    for change, what in (
+            (dict(k=k.float()), "k must be bfloat16 or float16"), (dict(v=k.half()), "v must be"),
+            (dict(q=q.half()), "q must be"), (dict(k=k[0]), "k must have 3 dims"),
+            (dict(v=k[:2]), r"v has shape \(2, 2, 128\), expected \(3, heads, 128\)"),
+            (dict(v=k[:, :, :64]), "v has shape"), (dict(q=q[:2]), "q has shape"),
+            (dict(v=k[:, :1]), "differ in their heads"), (dict(cache=cache[:, :1].contiguous()), "differ in their heads"),
+            (dict(v=torch.zeros(3, 128, 2, dtype=k.dtype, device=cuda).transpose(1, 2)), "unit stride"),
+            (dict(cache=cache.view(torch.int8)), "contiguous uint8"), (dict(cache=cache[:, :1]), "contiguous uint8"),
+            (dict(cache=cache[0]), "contiguous uint8"),
+            (dict(cache=cache[:, :, :-1].contiguous()), "does not hold whole tokens"),
+            (dict(block_table=bt.long()), "must be int32"), (dict(q_start=qs.long()), "must be int32"),
+            (dict(kv_len=kv.long()), "must be int32"), (dict(block_table=bt[0]), "block_table has 2 dims"),
+            (dict(q_start=qs[:1]), "q_start 1 entries"), (dict(kv_len=qs), "kv_len 2"),
+            (dict(block_table=bt.repeat(1, 2)[:, ::2]), "unit stride"),
+            (dict(block_table=bt.expand(2, 4), q_start=qs.new_zeros(3), kv_len=qs), "rows overlap"),
+            (dict(rope=rope.double()), "table must hold"), (dict(rope=rope[0]), "table must have 2 dims"),
+            (dict(rope=rope[:, ::2]), "table must hold"), (dict(signs=signs[:64]), "signs must hold 128"),
+            (dict(signs=signs.int()), "signs must hold"), (dict(positions=good["positions"][:2]), "positions must hold 3"),
+            (dict(positions=good["positions"].long()), "positions must hold"),
+            (dict(info=torch.zeros(2, dtype=torch.int32, device=cuda)), "info must hold 1"),
+            (dict(q_out=torch.empty_like(q)[:, :, :64]), "q_out must be"), (dict(q_out=q.half()), "q_out must be"),
+            (dict(q=None), "q and q_out go together"),
+            (dict(k=k.cpu()), "k must be a CUDA tensor"), (dict(v=k.cpu()), "v is on cpu"), (dict(q=q.cpu()), "q is on cpu"),
+            (dict(cache=cache.cpu()), "cache is on cpu"), (dict(block_table=bt.cpu()), "block_table is on cpu"),
+            (dict(q_start=qs.cpu()), "q_start is on cpu"), (dict(kv_len=kv.cpu()), "kv_len is on cpu"),
+            (dict(rope=rope.cpu()), "table is on cpu"), (dict(signs=signs.cpu()), "signs is on cpu"),
+            (dict(q_out=torch.empty_like(q).cpu()), "q_out is on cpu")):
+        with pytest.raises(ValueError, match=what):
+            kv4.append(**{**good, **change})
+    for change in (dict(rope=rope[:, :8].contiguous()), dict(rope=torch.zeros(4, 144, device=cuda)),
+                   dict(rope=rope[:0]), dict(cache=torch.zeros(4, 2, 24 * 136, dtype=torch.uint8, device=cuda))):
+        with pytest.raises(abi.KronqError):
+            kv4.append(**{**good, **change})
+
+
+def test_attention_refusals_on_the_device(cuda):
+    q, k, cache, bt, qs, kv = small_call(cuda)
+    good = dict(q=q, cache=cache, block_table=bt, q_start=qs, kv_len=kv, out=torch.empty_like(q),
+                lse=torch.zeros(3, 4, device=cuda), info=torch.zeros(1, dtype=torch.int32, device=cuda),
+                ws=abi.kv4_workspace(3, 4, 2, 128, 1, device=cuda))
+    kv4.attend(**good)
+    for change, what in (
+            (dict(q=q.float()), "q must be bfloat16 or float16"), (dict(q=q[0]), "q must have 3 dims"),
+            (dict(q=torch.zeros(3, 128, 4, dtype=q.dtype, device=cuda).transpose(1, 2)), "unit stride"),
+            (dict(q=q[:, :, :64]), "does not hold whole tokens|out has shape"),
+            (dict(out=q.half()), "out must be"), (dict(out=q[:2]), "out has shape"), (dict(out=q[:, :2]), "out has shape"),
+            (dict(out=torch.zeros(3, 4, 256, dtype=q.dtype, device=cuda)[:, :, ::2]), "unit stride"),
+            (dict(lse=torch.zeros(3, 3, device=cuda)), "lse has shape"), (dict(lse=torch.zeros(12, device=cuda)), "lse has shape"),
+            (dict(lse=torch.zeros(3, 4, dtype=torch.float64, device=cuda)), "lse must hold"),
+            (dict(lse=torch.zeros(3, 8, device=cuda)[:, ::2]), "lse must hold"),
+            (dict(info=torch.zeros(1, device=cuda)), "info must hold"), (dict(window=-1), "must not be negative"),
+            (dict(sinks=-1), "must not be negative"), (dict(ws=good["ws"][::2]), "ws must be contiguous"),
+            (dict(q_start=qs[:1]), "q_start 1 entries"), (dict(kv_len=kv.long()), "must be int32"),
+            (dict(cache=cache[:, :, :-1].contiguous()), "does not hold whole tokens"),
+            (dict(out=q.cpu()), "out is on cpu"), (dict(lse=good["lse"].cpu()), "lse is on cpu"),
+            (dict(ws=good["ws"].cpu()), "ws is on cpu"), (dict(info=good["info"].cpu()), "info is on cpu")):
+        with pytest.raises(ValueError, match=what):
+            kv4.attend(**{**good, **change})
+    for change in (dict(q=q[:, :3], out=None, lse=None), dict(window=4, causal=False), dict(scale=float("nan")),
+                   dict(ws=good["ws"][:256])):
+        with pytest.raises(abi.KronqError):
+            kv4.attend(**{**good, **change})
+
+
+def test_gather_refusals_on_the_device(cuda):
+    _, k, cache, bt, qs, kv = small_call(cuda)
+    kv4.gather(cache, bt, qs, kv, 3, 128)
+    for args, what in (((cache, bt, qs, kv, -1, 128), "must not be negative"), ((cache, bt, qs, kv, 3, 0), "must not be negative"),
+                       ((cache, bt, qs, kv, 3, 100), "does not hold whole tokens"), ((cache[0], bt, qs, kv, 3, 128), "3 dims"),
+                       ((cache, bt, qs, kv, 3, 128, torch.float64), "must be bfloat16, float16 or float32")):
+        with pytest.raises(ValueError, match=what):
+            kv4.gather(*args)
+    for ko, vo, what in ((k, k.half(), "v_out must be"), (k, k[:2], "v_out must be"), (k.transpose(0, 1), k, "contiguous"),
+                         (k[:, :1].contiguous(), k[:, :1].contiguous(), "differ in their heads"), (k.cpu(), k, "CUDA tensor"),
+                         (k, k.cpu(), "v_out is on cpu")):
+        with pytest.raises(ValueError, match=what):
+            abi.kronq_kv4_gather(cache, bt, qs, kv, ko, vo)

@@ -24,6 +24,7 @@ import numpy as np
 import pytest
 import torch
 
+import kv4_cases
 from gpu_helpers import t
 from oracle import kv4 as ok
 from post_quantization_02_b200 import kv4
@@ -248,3 +249,39 @@ def test_fp16_outputs_that_cancel(cuda, D, new, g, L):
     out = kv4.attend(q, st.cache, *st.args)
     assert few(st.T, g, 2, D)
     check(st, q, out, D ** -0.5, 2, 33)
+
+
+@pytest.mark.parametrize("D,g,L,n", [(128, 4, 8, 8), (128, 1, 4, 4), (64, 3, 2, 2), (256, 4, 16, 16),     # 4 rows at most
+                                     (128, 8, 8, 8), (256, 6, 4, 4), (64, 5, 16, 16),                    # 8
+                                     (128, 16, 8, 8), (64, 12, 4, 4),                                    # 16
+                                     (128, 4, 9000, 8), (128, 8, 9000, 16), (64, 16, 20000, 8), (256, 2, 9000, 8)])
+def test_two_terms_of_a_weight(cuda, D, g, L, n):
+    """fp16 outputs of pairs that cancel (kv4_cases.py: one fp16 term of each weight is beyond the
+    bound), in a short sequence and spread over a long one whose other keys are far below."""
+    r = np.random.default_rng(60 + D + g)
+    heads, B, P = 4, 2, 64
+    st = Setup(cuda, r, [1] * B, [L] * B, heads, D, P)
+    raw = st.cache.cpu().numpy()
+    far_code, far_scale, far_zero = kv4_cases.key_far_below()
+    one = words_of(1.0)
+    raw[:, :, :P * D // 2] = far_code
+    raw[:, :, P * D:P * D + 4 * P] = np.full(P, words_of(far_scale, far_zero), np.uint32).view(np.uint8)
+    raw[:, :, P * D + 4 * P:] = np.full(P, one, np.uint32).view(np.uint8)
+    want = {}
+    for b in range(B):
+        for h in range(heads):
+            s, z, c = kv4_cases.pairs(r, n, D)
+            want[b, h] = (*kv4_cases.exact(s, z, c), s)
+            at = np.sort(r.permutation(L)[:n])
+            for j, i in zip(at, r.permutation(n)):
+                blk = raw[st.bt[b, j // P], h]
+                ok.put(blk, P, D, j % P, np.zeros(D, np.uint8), one, 0)
+                ok.put(blk, P, D, j % P, c[i], ok.words(s[i:i + 1], z[i:i + 1])[0], 1)
+    st.cache.copy_(torch.from_numpy(raw))
+    q = torch.from_numpy(np.abs(r.standard_normal((B, heads * g, D))) + 0.5).to(cuda, torch.float16)
+    out = f64(kv4.attend(q, st.cache, *st.args))
+    for (b, h), (o, v, s) in want.items():
+        tol = kv4_cases.bound(o, v, s, 2.0 ** -10) + 2.0 ** -25       # (outputs that fp16 holds as subnormals)
+        for row in range(h * g, (h + 1) * g):
+            bad = ~(np.abs(out[b, row] - o) <= tol)
+            assert not bad.any(), (b, row, out[b, row][bad][:4], o[bad][:4], tol[bad][:4])

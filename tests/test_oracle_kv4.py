@@ -4,6 +4,7 @@ rotation's invariances, and attention's masks."""
 import numpy as np
 import pytest
 
+import kv4_cases
 from oracle import kv4 as ok
 from oracle import transform
 
@@ -76,3 +77,16 @@ def test_masks():
     assert not ok.visible(-1, 4, True, 0, 0).any()
     o, lse, p = ok.attend(np.ones(4), np.ones((3, 4)), np.ones((3, 4)), 1.0, np.zeros(3, bool))
     assert not o.any() and lse == -np.inf and not p.any()
+
+
+@pytest.mark.parametrize("n,D", [(2, 64), (2, 128), (4, 256), (8, 128), (16, 64)])
+def test_cancelling_pairs_catch_one_term(n, D):
+    """The inputs of the GPU's test of fp16 weights in two terms: rounding them to one is beyond its bound
+    (but where the few weights of a draw happen to lie next to fp16 numbers)."""
+    caught = 0
+    for seed in range(20):
+        s, z, c = kv4_cases.pairs(np.random.default_rng(seed), n, D)
+        o, v = kv4_cases.exact(s, z, c)
+        tol = kv4_cases.bound(o, v, s, 2.0 ** -10)
+        caught += (np.abs(kv4_cases.with_one_term(s, z, c) - o) > tol).any()
+    assert caught >= 15
