@@ -487,9 +487,10 @@ int kronq_kv4_gather(void* k_out, void* v_out, int dtype, int64_t T,
  * rounded to fp16 for the product (fp16 queries with few rows, see below: to two
  * fp16 terms), relative to the largest of them that the row has: below 2^-33 of
  * it (2^-25 among 64 keys with scales 2^8 apart) they count as 0.
- * bf16 queries with more than 64 rows (new tokens x query heads of a group; 40 at
- * head_dim 256) per sequence on average: keys and values are rounded to fp16 too, once or twice
- * 2^-11 relative to each, where the output is rounded at 2^-8.
+ * More than 64 rows (new tokens x query heads of a group; fp16 at head_dim 256: 40) per sequence
+ * on average: fp16 queries' probabilities have one term, 2^-11 relative to each, where the
+ * output is rounded at 2^-11; with bf16 queries keys and values are rounded to fp16
+ * too, once or twice 2^-11 relative to each, where the output is rounded at 2^-8.
  * What a row does not see has no part in its result, however large.  Values of the
  * whole range of fp32 are attended to (beyond 10^30, probabilities below 2^-20 of the
  * value's own may be missing from the sum that divides); scores have to

@@ -795,26 +795,37 @@ __global__ void __launch_bounds__(THREADS) kv4_merge_kernel(const AttendArgs a, 
 
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
+// (of the device this is written for, not asked for: a workspace's size is the same everywhere)
 constexpr int SMS = 148;
 // The shortest chunks of keys: one new token over 8k takes 13.4 us with 256 keys, 14.4 with
 // 512 (before the join was cheap); 16 and 64 new tokens over 8k with the other kernel 25 and
 // 33 us with 256, 23 and 31 with 512, 31 and 41 with 1024.
 constexpr int MIN_CHUNK = 2;                         // key blocks
 constexpr int PROMPT_MIN_KEYS = 512;
-// What a unit costs beside its blocks; 1.5, 3 and 5 measure the same for the first kernel.
+// What a unit costs beside its blocks.  It matters little: with 0 for both, 1 x 8k 13.5 us and
+// 12 x 3k 20.6 as with these, 4 x 128k 110 (108); with 5 and 15 they take 14.1, 22.0 and 108.
 constexpr float UNIT_COST = 1.5f, PROMPT_UNIT_COST = 5.f;
 
 // How a call is run.  Rows per sequence and key/value head decide (on average: lengths
 // are on the device).  The tensor-memory kernel's time is that of 128 rows (256: the
 // second tile rides along) whatever there are; the other's grows with every 16 (head_dim
 // 256: 8), and per row it is the slower one:
-//   rows            16    24    32    48    64    80    96
-//   head_dim 128    39    60    61    77   103   135   151     8 sequences of 8k, 8 heads
-//                   95    97    98   100   102   104   106     (us; this kernel, kv4_prompt.cu)
-//   head_dim 256    65    82   110   160   192
-//                  129   131   132   135   138
-//   head_dim 64     30    46    47    59    79   113   116
-//                   73    75    75    77    79    82    84
+//   rows                 16    24    32    40    48    64    80    96
+//   head_dim 128 bf16    43    61    62    75    76   100   133   147     8 sequences of 8k, 8 heads
+//                        99   100   100   100   100   101   104   104     (us; this kernel, kv4_prompt.cu)
+//                fp16    48    71    72    90    91   122   170   180
+//                        97    97    97    98    97    98   100   101
+//   head_dim 256 bf16    68    84   110   138   160   197   249   289
+//                       210   210   212   212   214   211   214   216
+//                fp16    76    95   126   157   183   229   289   336
+//                       123   123   123   124   126   127   128   129
+//   head_dim 64  bf16    31    45    46    56    57    74   106   108
+//                        76    76    76    77    78    78    79    80
+//                fp16    34    52    52    64    65    86   123   125
+//                        84    84    84    85    85    86    86    87
+// fp16 queries stay with this kernel some rows longer than it is the faster one, for its second
+// terms (see Terms; the other kernel's error against 64 bits is 1.4 times that of the output's
+// rounding).
 // Tiles of 8 rows (twice the blocks per SM) where 8 are enough: 16 rows take 42 us with
 // them, 39 with tiles of 16.
 struct Way {
@@ -824,7 +835,7 @@ struct Way {
 };
 
 Way way_of(int64_t T, int g, int D, int64_t B, int dt) {
-  if (T * g > (D == 256 ? 40 : 64) * B)
+  if (T * g > (D == 256 && dt == FP16 ? 40 : 64) * B)
     return {true, prompt_rows(D), prompt_block(D), PROMPT_MIN_KEYS / prompt_block(D), SMS, PROMPT_UNIT_COST};
   const int R = dt == FP16 && T * g <= 4 * B ? 4 : D == 256 || T * g <= 8 * B ? 8 : 16;
   return {false, R, BLK, MIN_CHUNK, SMS * (D == 256 || R == 16 ? 2 : 4), UNIT_COST};
@@ -849,7 +860,7 @@ int launch(AttendArgs& a, cudaStream_t st) {
   constexpr int ROWS = 8 * NT, R = TERMS == TWO_COLUMNS ? 4 : ROWS;
   const long long grid = max_units(a, R, BLK);
   if (grid > INT32_MAX) return KRONQ_ERR_UNSUPPORTED;
-    constexpr int rings = WARPS * RING * Step<D>::BYTES, join = WARPS * ROWS * D * (int)sizeof(float);
+  constexpr int rings = WARPS * RING * Step<D>::BYTES, join = WARPS * ROWS * D * (int)sizeof(float);
   constexpr int smem = rings > join ? rings : join;
   static kqh::PerDevice attr;
   if (kqh::smem_attr_once(attr, kv4_attend_kernel<D, NT, TERMS>, smem) <= 0) return KRONQ_ERR_CUDA;
@@ -903,8 +914,9 @@ int run(AttendArgs& a, const Way& w, cudaStream_t st) {
 
 size_t kq_kv4_attention_ws(int64_t T, int Hq, int heads, int D, int64_t B) {
   if (T < 0 || Hq <= 0 || heads <= 0 || Hq % heads || B <= 0 || (D != 64 && D != 128 && D != 256)) return 0;
-  // (for either type: the tiles of 4 rows need less)
-  return kv4::layout_of(kv4::way_of(T, Hq / heads, D, B, kv4::BF16), D, heads, B).total;
+  // (for either type)
+  const auto need = [&](int dt) { return kv4::layout_of(kv4::way_of(T, Hq / heads, D, B, dt), D, heads, B).total; };
+  return std::max(need(kv4::BF16), need(kv4::FP16));
 }
 
 int kq_kv4_attention(const void* q, int64_t q_st, int64_t q_sh, int dtype, int64_t T, int Hq, int D,

@@ -981,7 +981,7 @@ int launch(const AttendArgs& a, cudaStream_t st) {
   if (grid > INT32_MAX) return KRONQ_ERR_UNSUPPORTED;
   static kqh::PerDevice attr;
   if (kqh::smem_attr_once(attr, kv4_prompt_kernel<D, BF>, SH::SMEM) <= 0) return KRONQ_ERR_CUDA;
-    kv4_prompt_kernel<D, BF><<<(unsigned)grid, THREADS, SH::SMEM, st>>>(a);
+  kv4_prompt_kernel<D, BF><<<(unsigned)grid, THREADS, SH::SMEM, st>>>(a);
   KQ_CHECK_LAUNCH();
   return KRONQ_OK;
 }

@@ -90,8 +90,8 @@ def check(st, q, out, scale, terms, floor, causal=True, window=0, sinks=0, lse=N
                     assert abs(lse[row, h].item() - want) <= (p @ u) + 2.0 ** -20 * (1 + abs(want)), (b, i, h)
 
 
-def few(T, g, B, D):
-    return T * g <= (40 if D == 256 else 64) * B
+def few(T, g, B, D, dtype="bf16"):
+    return T * g <= (40 if D == 256 and dtype == "fp16" else 64) * B
 
 
 @pytest.mark.parametrize("dtype,big", [("fp16", 6e4), ("bf16", 1e5), ("bf16", 1e12), ("bf16", 3e38)])
@@ -111,7 +111,7 @@ def test_values_far_apart(cuda, D, new, g, dtype, big):
         w.put(0, j, 0, x[::-1] if j & 1 else x, 1)
     w.done()
     q = torch.from_numpy(r.standard_normal((st.T, g, D))).to(cuda, DT[dtype])
-    is_few = few(new, g, 1, D)
+    is_few = few(new, g, 1, D, dtype)
     rows = range(new) if new < 20 else [0, 1, 4, 5, 31, 33, 59, 60, 61, new // 2 - 1, new // 2, new - 2, new - 1]
     for win, snk in ((0, 0), (window, sinks), (window, 0), (1, 0)):
         lse = torch.empty(st.T, g, device=cuda)
@@ -174,7 +174,7 @@ def test_one_key_holds_the_probability(cuda, dtype, new, g, first):
     q = torch.ones(st.T, heads * g, D, device=cuda).to(DT[dtype])
     lse = torch.empty(st.T, heads * g, device=cuda)
     out = kv4.attend(q, st.cache, *batch, scale=1 / D, lse=lse)
-    is_few = few(new, g, 1, D)
+    is_few = few(new, g, 1, D, dtype)
     terms = (2 if dtype == "fp16" else 1) if is_few else (1 if dtype == "fp16" else 3)
     check(st, q, out, 1 / D, terms, 33, lse=lse, rows=[new - 1], seqs=[0, B - 1],
           keys_rounded=not is_few and dtype == "bf16")
@@ -200,7 +200,7 @@ def test_zero_and_tiny_values(cuda, dtype, new, g):
     q = torch.from_numpy(r.standard_normal((st.T, g, D)) * 3).to(cuda, DT[dtype])
     lse = torch.empty(st.T, g, device=cuda)
     out = kv4.attend(q, st.cache, *st.args, lse=lse)
-    is_few = few(st.T, g, 3, D)
+    is_few = few(st.T, g, 3, D, dtype)
     terms = (2 if dtype == "fp16" else 1) if is_few else (1 if dtype == "fp16" else 3)
     # (scales below 2^-80 lie lower in fp16's range: these are at 2^-86)
     check(st, q, out, D ** -0.5, terms, 28, lse=lse, rows=[0, 1 % new, new - 1],
@@ -247,7 +247,7 @@ def test_fp16_outputs_that_cancel(cuda, D, new, g, L):
     w.done()
     q = torch.from_numpy(np.abs(r.standard_normal((st.T, 2 * g, D))) + 0.5).to(cuda, torch.float16)
     out = kv4.attend(q, st.cache, *st.args)
-    assert few(st.T, g, 2, D)
+    assert few(st.T, g, 2, D, "fp16")
     check(st, q, out, D ** -0.5, 2, 33)
 
 
