@@ -871,13 +871,24 @@ int launch(AttendArgs& a, cudaStream_t st) {
 
 template <int D>
 int launch_merge(const AttendArgs& a, int R, cudaStream_t st) {
-  // Rows by themselves where the device holds a block for each or a sequence may have more
-  // splits than a warp takes (on average less than 2 resident / (heads B)); else four to a
-  // block.  512 rows of 12 splits: 23 us with a block each, 28 with four to a block; 4096 of
-  // two: 104 and 99.
+  // Query heads of a token to a block: one where the device holds a block for each row or a
+  // sequence may have many splits (their number is resident / (heads B) on average, and a warp
+  // takes 8), else four; a token's all where there are so many rows that blocks which find
+  // nothing to do are the cost.  The whole call in us, heads of 128, bf16:
+  //   rows, resident / (heads B)     1      4    all
+  //      512    4.6                44.2   49.5   94.7
+  //     1024    2.3                63.5   62.3   69.7
+  //     4096    1.2                 115    108    123
+  //     4096    4.6                90.5   85.0   96.4
+  //     2048    9.2                 163    167    267
+  //     2048   18.5                61.3   62.8    109
+  //    16384    9.2                 206    180    183
+  //    65536    4.6                 440    362    360
+  //   131072    9.2                1241   1190   1175
+  //   262144   18.5                 883    776    747
   const long long rows = (long long)a.T * a.Hq;
-  const bool few = 2ll * a.resident <= 12ll * a.cache.heads * a.b.B;
-  const int hpb = rows <= 4 * SMS || (!few && rows <= 16384) ? 1 : rows <= 65536 ? 4 : a.Hq;
+  const bool few = a.resident <= 6ll * a.cache.heads * a.b.B;
+  const int hpb = rows <= 4 * SMS || (!few && rows <= 8192) ? 1 : rows <= 65536 ? 4 : a.Hq;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.T, (unsigned)((a.Hq + hpb - 1) / hpb));
   cfg.blockDim = dim3(THREADS);
