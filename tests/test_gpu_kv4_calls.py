@@ -324,3 +324,68 @@ def test_gather_refusals_on_the_device(cuda):
                          (k, k.cpu(), "v_out is on cpu")):
         with pytest.raises(ValueError, match=what):
             abi.kronq_kv4_gather(cache, bt, qs, kv, ko, vo)
+
+
+@pytest.mark.parametrize("new", [2, 70])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_padding_in_front_and_behind(cuda, new, dtype):
+    """Rows in front of the first sequence and behind the last, full of NaN: left as they were, and of no
+    effect; the first sequence has no new tokens."""
+    r = np.random.default_rng(54)
+    st = Setup(cuda, r, [0, new, new], [100, 900, 300], 2, 128, 64)
+    st.fill_fast(torch.Generator(cuda).manual_seed(9))
+    a, b = 5, 5 + st.T
+    T = b + 7
+    start = st.args[1] + 5
+    wide = torch.full((T, 12, 128), float("nan"), device=cuda).to(dtype)
+    wide[a:b] = torch.randn(st.T, 12, 128, device=cuda).to(dtype)
+    q, k, v = wide[:, :8], wide[:, 8:10], wide[:, 10:]
+    rope = kv4.rope_table(900, 64, device=cuda)
+    info = torch.zeros(1, dtype=torch.int32, device=cuda)
+    before = st.cache.clone()
+    want_q = kv4.append(q[a:b], k[a:b], v[a:b], st.cache, *st.args, rope=rope)
+    want_cache = st.cache.clone()
+    want = kv4.attend(want_q, st.cache, *st.args)
+    want_k, want_v = kv4.gather(st.cache, *st.args, tokens=st.T, head_dim=128, dtype=dtype)
+    st.cache.copy_(before)
+    args = (st.args[0], start, st.args[2])
+    q_out = torch.full((T, 8, 128), 3.0, dtype=dtype, device=cuda)
+    kv4.append(q, k, v, st.cache, *args, rope=rope, q_out=q_out, info=info)
+    assert torch.equal(st.cache, want_cache) and torch.equal(q_out[a:b], want_q)
+    assert (q_out[:a] == 3).all() and (q_out[b:] == 3).all()
+    out = torch.full((T, 8, 128), 3.0, dtype=dtype, device=cuda)
+    lse = torch.full((T, 8), 3.0, device=cuda)
+    q_out[:a], q_out[b:] = float("nan"), float("nan")
+    kv4.attend(q_out, st.cache, *args, out=out, lse=lse, info=info)
+    ko, vo = (torch.full((T, 2, 128), 3.0, dtype=dtype, device=cuda) for _ in range(2))
+    abi.kronq_kv4_gather(st.cache, *args, ko, vo, info)
+    assert info.item() == 0
+    for got, w in ((out, want), (ko, want_k), (vo, want_v)):
+        assert torch.equal(got[a:b], w) and (got[:a] == 3).all() and (got[b:] == 3).all()
+    assert (lse[:a] == 3).all() and (lse[b:] == 3).all() and (lse[a:b] != 3).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_pages_beyond_32_bits(cuda, D):
+    """A cache of 5 GB, used at both of its ends: byte offsets pass 2^32."""
+    r = np.random.default_rng(55)
+    P, heads = 256, 4
+    block = abi.kronq_kv4_block_bytes(P, D)
+    pages = (5 << 30) // (heads * block)
+    assert (pages - 3) * heads * block > 1 << 32
+    big = kv4.make_cache(pages, P, heads, D, cuda)
+    for new in (1, 40):
+        small = Setup(cuda, r, [new, new], [700, 600], heads, D, P)
+        small.fill_fast(torch.Generator(cuda).manual_seed(10))
+        ids = torch.tensor([pages - 1, 0, pages - 2, pages // 2, 1, pages - 3, pages - 4, 2], device=cuda)
+        assert small.pages <= len(ids)
+        big[ids[:small.pages]] = small.cache
+        bt = torch.where(small.args[0] >= 0, ids[small.args[0].clamp_min(0).long()], -1).int()
+        k = torch.randn(small.T, heads, D, device=cuda).bfloat16()
+        q = torch.randn(small.T, heads * 4, D, device=cuda).bfloat16()
+        outs = []
+        for cache, table in ((small.cache, small.args[0]), (big, bt)):
+            kv4.append(None, k, k.flip(0), cache, table, *small.args[1:])
+            outs.append((kv4.attend(q, cache, table, *small.args[1:]),
+                         *kv4.gather(cache, table, *small.args[1:], tokens=small.T, head_dim=D)))
+        assert all(torch.equal(x, y) for x, y in zip(*outs))
