@@ -8,8 +8,10 @@
 // and zero points are per token, so they are taken out of both products: the
 // tensor cores multiply the bare codes, and 128 codes of a token cost one scale.
 //
-// What bounds it is not the copy but the integer instructions that turn 4-bit codes
-// into operands.  A code in the low bits of a half is the subnormal c 2^-24 (c 2^-20
+// What bounds it is not the copy but the chain of a warp's step, from codes to operands
+// to scores to probabilities to products: at 16 warps per SM the schedulers issue in 57 % of
+// their cycles and no pipe is busier (integer 55, tensor 30, memory 54), and the stalls are
+// fixed latencies.  So operands are made with few instructions.  A code in the low bits of a half is the subnormal c 2^-24 (c 2^-20
 // four bits up), exact in fp16 x fp16 -> fp32 products, so:
 //   keys    unpacking is one AND per two codes and one shift per four pairs; the
 //           factors 16 of every other pair go into the queries' fragments;
@@ -37,9 +39,9 @@
 // vote), so most steps have no cross-lane reduction.
 //
 // Measured (heads of 128, cold cache): 64 sequences of 4k to 8k tokens, 8 query heads
-// a key/value head, bf16: 99 us, 4.4 TB/s of codes and words; 4 sequences of 105k to
-// 131k tokens, 4 query heads, fp16: 105 us, 5.1 TB/s (of 6.55 that a copy moves).  One
-// sequence of 8k is latency: 11.6 us for the two launches.
+// a key/value head, bf16: 102 us at an SM clock of 1875 MHz, 4.2 TB/s of codes and words; 4
+// sequences of 105k to 131k tokens, 4 query heads, fp16: 116 us at 1760 MHz, 4.6 TB/s (of 6.55
+// that a copy moves).  One sequence of 8k is latency: 12.6 us for the two launches.
 #include <type_traits>
 
 #include "kv4_attend.cuh"
@@ -191,8 +193,8 @@ constexpr int FLUSH = 4;      // steps between subtractions of the zero points' 
 // the output's own rounding, and the two add up to 1.4 times its error; for bf16 outputs
 // it is an eighth of theirs.  A tile of 4 rows has them twice, in the MMA's columns 0 .. 3
 // and 4 .. 7: all of a column but its second product is alike, and that one takes the
-// second terms; a larger tile takes the product twice.  4 x 128k, 4 query heads: 102 us
-// with one term, 105 in two columns, 119 with two products.
+// second terms; a larger tile takes the product twice.  4 x 128k, 4 query heads, side
+// by side: 102 us with one term, 105 in two columns, 119 with two products.
 enum Terms { ONE, TWO_COLUMNS, TWO_PRODUCTS };
 template <int D, int NT, int TERMS>
 __global__ void __launch_bounds__(THREADS, D <= 128 && NT == 1 ? 4 : 2) kv4_attend_kernel(const AttendArgs a) {

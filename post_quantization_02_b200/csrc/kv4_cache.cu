@@ -20,10 +20,11 @@
 // bytes per lane and 128 bytes per vector and r, the first three butterflies and the
 // last (D/64) are inside the lane, three go by shuffle, and a run of 8 dims is one
 // word of codes.  (64 dims per lane, with fewer shuffles, needs 160 registers: a fifth
-// slower.)  What bounds it is instructions, so fp32 operations go in packed pairs, a
+// slower.)  What bounds it is instructions (70 % of the issue slots) and the loads, stores and
+// shuffles among them (76 % of what L1 passes), so fp32 operations go in packed pairs, a
 // block looks its token's place up once for all its vectors, and the first vector is
 // asked for before that.  Measured: 34k tokens of 64 query and 2 x 8 key/value heads of
-// 128, bf16, both rotations: 363 us, 3.6 TB/s read and written; without rotations 268.
+// 128, bf16, both rotations: 367 us, 3.6 TB/s read and written; without rotations 268.
 #include "kv4.cuh"
 
 namespace {
@@ -356,10 +357,11 @@ struct GatherArgs {
 };
 
 // Reads tokens back as the values they stand for, the last new tokens of each sequence:
-// bound by the stores (2 bytes or 4 for half a byte read).  A block takes N tokens; their
+// bound by the stores (2 bytes or 4 for half a byte read; bf16 and fp32 write at the same rate,
+// though bf16 has the integer pipe at 71 % and fp32 does half the work a byte).  A block takes N tokens; their
 // places are looked up once, a warp per token, and 8 lanes read a vector as above.  N = 8
 // keeps four vectors of a thread in flight; few tokens are spread instead (N = 1).  34k
-// tokens of 2 x 8 heads of 128 as bf16: 41 us, 4.3 TB/s read and written (N = 1: 50).
+// tokens of 2 x 8 heads of 128 as bf16: 41 us, 3.4 TB/s written (N = 1: 50); as fp32 76, 3.7.
 template <int D, int N>
 __global__ void __launch_bounds__(TPB) kv4_gather_kernel(const GatherArgs a) {
   constexpr int R = D / 64;

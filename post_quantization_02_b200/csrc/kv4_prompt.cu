@@ -5,7 +5,11 @@
 // memory, P is the tensor-memory operand, over S.  Two ways, by the queries' type:
 //   fp16  the unpacked numbers are c - z, exact; scores and probabilities take the
 //         scale of their key, x = S s_j scale log2(e), P = 2^(x - m) s'_j, and the only
-//         rounding besides fp32's is P's.
+//         rounding besides fp32's is P's.  That is 2^-11 of each, as much as the output's own,
+//         and makes the error 1.4 times that one's (kv4_attend.cu takes two terms).  A second
+//         term would fit over the scores, but twice the products and the subtractions in the
+//         softmax took 1782 us for 1376 (two chunks of 2048 over 16k), 187 for 173 under the
+//         window below.
 //   bf16  the unpacked numbers are the keys and values themselves, s (c - z) times a power
 //         of two of the step, rounded to fp16 (the scale in two terms, so rounded once; a
 //         value's scale in one), and
@@ -36,13 +40,16 @@
 // Dims stay in the order unpacking yields within each 8 (0 4 1 5 2 6 3 7): queries
 // are stored that way and the output is put right when it leaves.
 //
-// Measured: two chunks of 2048 tokens over 16k, 32 query heads of 128, bf16: 1.32 ms,
-// 778 TFLOP/s of the two products.  A step of 64 keys takes 2200 to 2800 cycles: the
-// softmax of a row some 1900 (500 for scores and maximum, 1200 for exponentials and P),
-// the MMAs 1280 of tensor pipe (S reads 48 KB of shared memory per tile, 384 cycles where
+// Measured: two chunks of 2048 tokens over 16k, 32 query heads of 128, bf16: 1.27 ms,
+// 810 TFLOP/s of the two products; fp16 1.38 ms.  A step of 64 keys takes 2200 to 2800 cycles:
+// the softmax of a row some 1900 (600 to 900 for scores and maximum, 1200 for exponentials and
+// P), the MMAs 1280 of tensor pipe (S reads 48 KB of shared memory per tile, 384 cycles where
 // the products would take 256), issued one behind the other.  A unit costs some 12 us
 // beside its steps (division of the work, first loads, output): 1777 tokens under a window
-// of 1024, heads of 256: 172 us, 449 TFLOP/s (204 with one warp to a row).
+// of 1024, heads of 256, fp16: 172 us, 452 TFLOP/s (204 with one warp to a row); of a step's
+// 2600 cycles there, a softmax warp waits 720 for scores, takes 930 to the maximum that two
+// warps agree on and 740 to P.  Heads of 256, bf16: the two warps that unpack keys bound it (two
+// prompts of 1024 over 6000, 600 us: the MMA warp waits 3000 of 4900 cycles for them).
 //
 // All waits are bounded; one that gives up records KRONQ_ERR_TIMEOUT in `info`.
 #include <type_traits>
