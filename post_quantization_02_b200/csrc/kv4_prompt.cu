@@ -69,9 +69,9 @@ constexpr float NO_MAX = -0x1p127f;     // a split's maximum where it saw no key
 // times that fit, and ones down to 2^-24 of the largest scale are normal numbers.  A step
 // whose scales are further apart than V_SPREAD or K_SPREAD binaries is a wide one: its operands
 // are c - z (values: 2^V_TOP of it), exact, and every row takes its keys' scales for itself, so
-// that a row that does not see the largest keeps what it sees.  Neither limit is a matter of
-// speed: V_SPREAD is what a row's weights may lie lower in P's range without harm, K_SPREAD
-// leaves a score 2^-19 of itself.
+// that a row that does not see the largest keeps what it sees.  The limits are not a
+// matter of speed: by V_SPREAD binaries a row's weights may lie lower in P's range without
+// harm; K_SPREAD leaves a key's numbers 2^-19 of themselves exact.
 constexpr uint32_t kZeroScale = 0x0d800000u;      // 2^-100: a zero vector's; its score is 0 whatever its factor
 constexpr uint32_t V_SPREAD = 8, K_SPREAD = 16;
 constexpr uint32_t WIDE = 1u << 31;
