@@ -13,6 +13,14 @@ from test_gpu_kv4 import Setup, check_attention
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def own_random_numbers(cuda):
+    """The same inputs whatever ran before, and none taken from what runs behind."""
+    with torch.random.fork_rng(devices=[cuda]):
+        torch.manual_seed(2024)
+        yield
+
+
 def busy(stream):
     """Some 50 ms of work on the stream."""
     with torch.cuda.stream(stream):

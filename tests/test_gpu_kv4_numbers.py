@@ -33,6 +33,14 @@ from test_gpu_kv4 import DT, Setup, f64
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def own_random_numbers(cuda):
+    """The same inputs whatever ran before, and none taken from what runs behind."""
+    with torch.random.fork_rng(devices=[cuda]):
+        torch.manual_seed(2024)
+        yield
+
+
 def words_of(scale, zero=0):
     return ok.words(np.asarray([scale], dtype=np.float32).view(np.uint32).__and__(np.uint32(0xFFFFFFF0)).view(
         np.float32), np.asarray([zero], dtype=np.uint8))[0]
